@@ -312,6 +312,151 @@ IA_API ia_status_t ia_decode_step_ex(const ia_shape_t* shape, const ia_options_t
                                      void* state, float* o, float* num, float* den, void* stream);
 
 /*
+ * Linear attention with one fixed decay per head: the layer's sibling mixer
+ * with a real matrix state, for the same prefill / training / decode calls.
+ * No counterpart in the paper's layer; per (b,h), lambda = exp(log_decay_h):
+ *
+ *   S_t = lambda S_{t-1} + k_t v_t^T          d_k x d_v
+ *   o_t = scale * q_t^T S_t                    token t is in S_t
+ *
+ *   - q, k [B,H,N,d_k], v [B,H,N,d_v] in the input dtype (bf16 or fp32); o and
+ *     the gradients have the INPUT dtype (unlike the layer above, whose outputs
+ *     are fp32): with a plain sum there is no quotient whose parts must be kept
+ *     apart, and bf16 outputs halve the bytes written.  Sums and states are
+ *     fp32; a bf16 result is rounded once at the end.
+ *   - log_decay [H] fp32, <= 0 (0: no decay; -inf: only the token itself).  A
+ *     positive or NaN entry sets the device flag reported as
+ *     IA_ERR_PARAM_RANGE by ia_check_device_errors(); the outputs are then not
+ *     to be used.  The decay is a constant of the model: no gradient is formed
+ *     for it.
+ *   - A NaN or an infinity in token t reaches no token before it (after it, in
+ *     the reverse direction of dk and dv); from t on, values that the
+ *     definition leaves finite may be NaN as well.
+ *   - State: [B,H,d_k,d_v] fp32, ia_linear_state_bytes() bytes.
+ *   - d_k, d_v in 1 .. 256.
+ */
+typedef struct {
+  int B, H, N;          /* batch, heads, sequence length (N >= 1; ignored by decode and state calls) */
+  int d_k, d_v;         /* widths of q/k and of v */
+  ia_dtype_t in_dtype;
+} ia_linear_shape_t;
+
+IA_API size_t ia_linear_state_bytes(const ia_linear_shape_t* shape);
+
+/* Workspace bytes of the two sequence calls (0 when the sequences are not cut
+ * into segments).  Ask with the device of the call current: the number of
+ * segments depends on its SM count. */
+IA_API size_t ia_linear_prefill_workspace_bytes(const ia_linear_shape_t* shape);
+IA_API size_t ia_linear_fwd_bwd_workspace_bytes(const ia_linear_shape_t* shape);
+
+/* Kernels of the sequence calls: IA_PATH_TENSOR_CORE for bf16 inputs with d_k
+ * and d_v in {64, 128} (chunks of 128 tokens on tcgen05), else
+ * IA_PATH_SEQUENTIAL (the same chunked algebra in fp32 on CUDA cores). */
+IA_API ia_path_t ia_linear_path(const ia_linear_shape_t* shape);
+
+/* Segments per sequence that the two calls run (1 = whole sequences). */
+IA_API int ia_linear_prefill_segments(const ia_linear_shape_t* shape);
+IA_API int ia_linear_fwd_bwd_segments(const ia_linear_shape_t* shape);
+
+/*
+ * Causal prefill.  state_in: NULL = zero state.  state_out: optional, the
+ * state after token N-1 (may not overlap state_in).
+ */
+IA_API ia_status_t ia_linear_prefill_fwd(const ia_linear_shape_t* shape, const void* q, const void* k,
+                                         const void* v, const float* log_decay, float scale,
+                                         const float* state_in, void* o, float* state_out, void* workspace,
+                                         size_t workspace_bytes, void* stream);
+
+/*
+ * Training step from a zero state: o and, for the upstream gradient dO
+ * [B,H,N,d_v], dq = scale * S_t dO_t, dk = scale * D_t v_t and
+ * dv = scale * D_t^T k_t with D_t = lambda D_{t+1} + q_t dO_t^T.
+ */
+IA_API ia_status_t ia_linear_fwd_bwd(const ia_linear_shape_t* shape, const void* q, const void* k, const void* v,
+                                     const float* log_decay, float scale, const void* dO, void* o, void* dq,
+                                     void* dk, void* dv, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * One token: q, k [B,H,d_k], v [B,H,d_v] -> o [B,H,d_v].
+ *   parents NULL: row b of state_out is row b of state_in advanced by the
+ *     token; state_out may be state_in's buffer (in place).
+ *   parents [B/beams, beams] int32 (device): sequence g*beams + j continues
+ *     from row g*beams + parents[g][j] of state_in, so that the reordering of
+ *     a beam search costs no pass of its own.  state_out must then be another
+ *     buffer than state_in.  A parent outside 0 .. beams-1 (ia_beam_select
+ *     gives -1 for a missing candidate) stands for the zero state.
+ */
+IA_API ia_status_t ia_linear_decode_step(const ia_linear_shape_t* shape, const void* q, const void* k,
+                                         const void* v, const float* log_decay, float scale,
+                                         const float* state_in, const int* parents, int beams,
+                                         float* state_out, void* o, void* stream);
+
+/*
+ * Layer norm over rows of D values, x and y [rows, D] in one dtype, weight and
+ * bias [D] fp32 (NULL: 1 and 0), mean and rstd [rows] fp32 (both optional):
+ *   y = (x - mean) * rstd * weight + bias,  rstd = 1 / sqrt(var + eps), var the
+ * mean square of x - mean.  Statistics in fp32, the variance from the centred
+ * values.  1 <= D <= 2^24.  y may be x's buffer.
+ */
+IA_API ia_status_t ia_layer_norm_fwd(long long rows, int D, ia_dtype_t dtype, const void* x, const float* weight,
+                                     const float* bias, float eps, void* y, float* mean, float* rstd,
+                                     void* stream);
+
+/*
+ * Its backward pass, from the mean and rstd that the forward pass saved:
+ *   dx = rstd * (g - mean(g) - xhat * mean(g * xhat)),  g = dy * weight,
+ *   dweight = sum over rows of dy * xhat,  dbias = sum over rows of dy
+ * (both optional, fp32, overwritten; summed in a fixed order, so equal calls
+ * give equal bits).  dx [rows, D] has x's dtype and may be dy's or x's buffer.
+ */
+IA_API size_t ia_layer_norm_bwd_workspace_bytes(long long rows, int D, ia_dtype_t dtype);
+IA_API ia_status_t ia_layer_norm_bwd(long long rows, int D, ia_dtype_t dtype, const void* dy, const void* x,
+                                     const float* weight, const float* mean, const float* rstd, void* dx,
+                                     float* dweight, float* dbias, void* workspace, size_t workspace_bytes,
+                                     void* stream);
+
+/*
+ * Beam search's selection.  For each of G requests, the K best of its
+ * beams x vocabulary candidates by
+ *   scores[g][w] + logits[g][w][t] - logsumexp(logits[g][w][:])
+ * in descending order, ties to the lower beam, then the lower token:
+ * out_scores [G,K] fp32, out_parents and out_tokens [G,K] int32.
+ *   - logits [G,W,V] fp32 or bf16, scores [G,W] fp32.
+ *   - finished [G,W] bytes (optional): a beam whose byte is not 0 offers one
+ *     candidate, end_token at its unchanged score; its logits are not read.
+ *   - No candidate: a token whose logit is -inf, a beam whose score is not
+ *     finite, and every token of an unfinished beam whose logits hold a NaN
+ *     or +inf or nothing above -inf.
+ *   - Places that no candidate is left for: score -inf, parent and token -1.
+ * The order is that of the exact scores: sums run in fp32 with a known bound,
+ * and where that bound could not separate two beams' candidates, their sums
+ * are taken again in fp64.
+ * 1 <= W <= 64, 1 <= K <= 64, V >= 1; end_token is in 0 .. V-1 when finished
+ * is given.
+ */
+IA_API size_t ia_beam_select_workspace_bytes(int G, int W, int V, int K, ia_dtype_t dtype);
+IA_API ia_status_t ia_beam_select(int G, int W, int V, int K, ia_dtype_t dtype, const void* logits,
+                                  const float* scores, const unsigned char* finished, int end_token,
+                                  float* out_scores, int* out_parents, int* out_tokens, void* workspace,
+                                  size_t workspace_bytes, void* stream);
+
+/*
+ * Reordering of the recurrent states after a selection: sequence
+ * g*beams_out + j of state_out becomes sequence g*beams_in + parents[g][j] of
+ * state_in, parents [B/beams_in, beams_out] int32 (device); a parent outside
+ * 0 .. beams_in-1 gives a zero state.  shape->B counts the sequences of
+ * state_in, a multiple of beams_in; state_out holds B/beams_in*beams_out.
+ * With beams_out = beams_in state_out may be state_in's buffer (in place:
+ * only beams that change are moved); otherwise the buffers must not overlap.
+ * beams_in and beams_out are in 1 .. 64.
+ */
+IA_API ia_status_t ia_state_reorder(const ia_shape_t* shape, int beams_in, int beams_out, const int* parents,
+                                    const void* state_in, void* state_out, void* stream);
+IA_API ia_status_t ia_linear_state_reorder(const ia_linear_shape_t* shape, int beams_in, int beams_out,
+                                           const int* parents, const float* state_in, float* state_out,
+                                           void* stream);
+
+/*
  * Profiling aid (no counterpart in the paper): registers two caller-owned
  * CUDA events (cudaEvent_t handles).  While set, every later entry-point call
  * records `begin` on its stream immediately before launching its dominant

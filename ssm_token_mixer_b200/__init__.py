@@ -10,6 +10,11 @@ Entry points (same names as the C-ABI):
   prefill_fwd(q, k, v, delta, M, ...)   causal prefill, returns o (+ num, den, state)
   fwd_bwd(q, k, v, delta, dO, M, ...)   training step: o, dq, dk, dv, dDelta
   decode_step(q, k, v, delta, state, M)  one recurrent step, state updated in place
+  linear_prefill_fwd, linear_fwd_bwd, linear_decode_step
+                                        the same three for linear attention with one decay per head
+  layer_norm_fwd, layer_norm_bwd        layer norm and its gradients
+  beam_select(logits, scores, K, ...)   the best K continuations over beams and vocabulary
+  state_reorder, linear_state_reorder   the recurrent states follow their beams' parents
 """
 from __future__ import annotations
 
@@ -22,6 +27,11 @@ __all__ = ["IAError", "load_library", "state_bytes", "prefill_workspace_bytes",
            "fwd_bwd_workspace_bytes", "prefill_path", "fwd_bwd_path", "prefill_static_max_heads",
            "prefill_fwd", "prefill_fwd_static", "prefill_fwd_ex", "fwd_bwd", "decode_step",
            "decode_step_ex", "check_device_errors",
+           "linear_state_bytes", "linear_path", "linear_prefill_workspace_bytes",
+           "linear_fwd_bwd_workspace_bytes", "linear_prefill_segments", "linear_fwd_bwd_segments",
+           "linear_prefill_fwd", "linear_fwd_bwd", "linear_decode_step", "linear_state_reorder",
+           "layer_norm_fwd", "layer_norm_bwd", "layer_norm_bwd_workspace_bytes", "beam_select",
+           "beam_select_workspace_bytes", "state_reorder",
            "selftest_wait_expiry", "set_launch_events", "library_path", "IA_F32", "IA_BF16"]
 
 IA_F32, IA_BF16 = 0, 1
@@ -47,6 +57,11 @@ class IAShape(ctypes.Structure):
     _fields_ = [("B", ctypes.c_int), ("H", ctypes.c_int), ("N", ctypes.c_int),
                 ("d_xi", ctypes.c_int), ("d_v", ctypes.c_int), ("M", ctypes.c_int),
                 ("in_dtype", ctypes.c_int), ("delta_per_mode", ctypes.c_int)]
+
+
+class IALinearShape(ctypes.Structure):
+    _fields_ = [("B", ctypes.c_int), ("H", ctypes.c_int), ("N", ctypes.c_int), ("d_k", ctypes.c_int),
+                ("d_v", ctypes.c_int), ("in_dtype", ctypes.c_int)]
 
 
 class IAOptions(ctypes.Structure):
@@ -99,6 +114,22 @@ def load_library():
     lib.ia_decode_step_ex.argtypes = [S, O] + [P] * 9 + [P]
     lib.ia_state_carry.restype = ctypes.c_int
     lib.ia_state_carry.argtypes = [S, P, P, ctypes.c_longlong, P, P, P, P]
+    L, I, F, LL, Z = ctypes.POINTER(IALinearShape), ctypes.c_int, ctypes.c_float, ctypes.c_longlong, ctypes.c_size_t
+    for name, res, args in (
+            ("ia_linear_state_bytes", Z, [L]), ("ia_linear_path", I, [L]),
+            ("ia_linear_prefill_workspace_bytes", Z, [L]), ("ia_linear_fwd_bwd_workspace_bytes", Z, [L]),
+            ("ia_linear_prefill_segments", I, [L]), ("ia_linear_fwd_bwd_segments", I, [L]),
+            ("ia_linear_prefill_fwd", I, [L, P, P, P, P, F, P, P, P, P, Z, P]),
+            ("ia_linear_fwd_bwd", I, [L, P, P, P, P, F, P, P, P, P, P, P, Z, P]),
+            ("ia_linear_decode_step", I, [L, P, P, P, P, F, P, P, I, P, P, P]),
+            ("ia_layer_norm_fwd", I, [LL, I, I, P, P, P, F, P, P, P, P]),
+            ("ia_layer_norm_bwd_workspace_bytes", Z, [LL, I, I]),
+            ("ia_layer_norm_bwd", I, [LL, I, I, P, P, P, P, P, P, P, P, P, Z, P]),
+            ("ia_beam_select_workspace_bytes", Z, [I, I, I, I, I]),
+            ("ia_beam_select", I, [I, I, I, I, I, P, P, P, I, P, P, P, P, Z, P]),
+            ("ia_state_reorder", I, [S, I, I, P, P, P, P]),
+            ("ia_linear_state_reorder", I, [L, I, I, P, P, P, P])):
+        getattr(lib, name).restype, getattr(lib, name).argtypes = res, args
     lib.ia_set_launch_events.restype = ctypes.c_int
     lib.ia_set_launch_events.argtypes = [P, P]
     lib.ia_check_device_errors.restype = ctypes.c_int
@@ -532,6 +563,317 @@ def decode_step_ex(q, k, v, state, M, delta=None, A=None, delta_t=None, gain=Non
                                _ptr(A), _ptr(state), _ptr(o), _ptr(num), _ptr(den), _stream(stream))
     _check(rc, "ia_decode_step_ex")
     return {"o": o, "num": num, "den": den}
+
+
+# ------------------------------------------------- linear attention, norm, beams
+class _On:
+    """Makes a call's device and stream current while outputs and scratch are
+    allocated and the kernels are launched, so that a tensor of another device
+    than the current one works and memory allocated for another stream belongs
+    to that stream's pool.  `raw` is the stream's handle."""
+
+    def __init__(self, dev, stream):
+        if stream is not None:
+            if stream.device != dev:
+                raise ValueError(f"stream is on {stream.device}, the tensors on {dev}")
+            self.ctx = torch.cuda.stream(stream)   # makes its device current too
+            self.raw = stream.cuda_stream
+        else:
+            self.ctx = torch.cuda.device(dev) if dev.index != torch.cuda.current_device() else None
+            self.raw = torch.cuda.current_stream(dev).cuda_stream
+
+    def __enter__(self):
+        if self.ctx is not None:
+            self.ctx.__enter__()
+        return self.raw
+
+    def __exit__(self, *exc):
+        if self.ctx is not None:
+            self.ctx.__exit__(*exc)
+        return False
+
+
+def _linear_shape(B, H, N, d_k, d_v, dtype) -> IALinearShape:
+    code = dtype if isinstance(dtype, int) else (IA_BF16 if dtype in (torch.bfloat16, "bf16") else IA_F32)
+    return IALinearShape(int(B), int(H), int(N), int(d_k), int(d_v), code)
+
+
+def linear_state_bytes(B, H, d_k, d_v) -> int:
+    return int(load_library().ia_linear_state_bytes(ctypes.byref(_linear_shape(B, H, 1, d_k, d_v, IA_F32))))
+
+
+def linear_path(B, H, N, d_k, d_v, dtype):
+    """'tensor_core' or 'sequential' (CUDA cores): the kernels of the linear sequence calls for this shape."""
+    return PATHS[load_library().ia_linear_path(ctypes.byref(_linear_shape(B, H, N, d_k, d_v, dtype)))]
+
+
+def linear_prefill_workspace_bytes(B, H, N, d_k, d_v, dtype) -> int:
+    return int(load_library().ia_linear_prefill_workspace_bytes(ctypes.byref(_linear_shape(B, H, N, d_k, d_v, dtype))))
+
+
+def linear_fwd_bwd_workspace_bytes(B, H, N, d_k, d_v, dtype) -> int:
+    return int(load_library().ia_linear_fwd_bwd_workspace_bytes(ctypes.byref(_linear_shape(B, H, N, d_k, d_v, dtype))))
+
+
+def linear_prefill_segments(B, H, N, d_k, d_v, dtype) -> int:
+    return int(load_library().ia_linear_prefill_segments(ctypes.byref(_linear_shape(B, H, N, d_k, d_v, dtype))))
+
+
+def linear_fwd_bwd_segments(B, H, N, d_k, d_v, dtype) -> int:
+    return int(load_library().ia_linear_fwd_bwd_segments(ctypes.byref(_linear_shape(B, H, N, d_k, d_v, dtype))))
+
+
+def _small(name, *sizes):
+    """The library takes sizes as C ints, which would drop higher bits without a word."""
+    if max(sizes) > 0x7fffffff:
+        raise ValueError(f"{name}: sizes above 2^31 - 1 are not supported, got {sizes}")
+
+
+def _check_linear_args(dim, q, k, v, log_decay):
+    """q, k [B,H,(N,)d_k], v [B,H,(N,)d_v] in one input dtype, log_decay [H] fp32.  Returns the C shape."""
+    names = "[B,H,N,d_k]" if dim == 4 else "[B,H,d_k]"
+    _need("q", q)
+    if q.dim() != dim:
+        raise ValueError(f"q must be {names}, got shape {tuple(q.shape)}")
+    code = _dtype_code(q)
+    _need("k", k, q.shape, q.dtype)
+    _need("v", v, dtype=q.dtype)
+    if v.dim() != dim or v.shape[:-1] != q.shape[:-1]:
+        raise ValueError(f"v must be {names.replace('d_k', 'd_v')} with q's leading sizes, got {tuple(v.shape)}")
+    _need("log_decay", log_decay, (q.shape[1],), torch.float32)
+    _small("q, v", *q.shape, *v.shape)
+    return IALinearShape(q.shape[0], q.shape[1], q.shape[2] if dim == 4 else 1, q.shape[-1], v.shape[-1], code)
+
+
+def _scratch(nbytes, dev, workspace):
+    """(tensor or None, pointer, bytes) of a call's workspace: the caller's, or a new one of nbytes."""
+    if workspace is None:
+        if nbytes == 0:
+            return None, None, 0
+        workspace = torch.empty(nbytes, dtype=torch.uint8, device=dev)
+    return workspace, _ptr(workspace), _nbytes(workspace)
+
+
+def linear_prefill_fwd(q, k, v, log_decay, scale=None, state_in=None, want_state=False, o=None, workspace=None,
+                       stream=None):
+    """Causal linear attention with one decay per head (see ia_linear_prefill_fwd in include/ia.h):
+    S_t = exp(log_decay_h) S_(t-1) + k_t v_t^T, o_t = scale q_t^T S_t.
+
+    q, k [B,H,N,d_k], v [B,H,N,d_v] (fp32 or bf16), log_decay [H] fp32 (<= 0), scale d_k**-0.5 when None,
+    state_in [B,H,d_k,d_v] fp32 (flat or not).  Returns dict with o [B,H,N,d_v] in the input dtype and, on
+    request, state (flat fp32, after the last token)."""
+    lib = load_library()
+    shp = _check_linear_args(4, q, k, v, log_decay)
+    n_state = shp.B * shp.H * shp.d_k * shp.d_v
+    if state_in is not None:
+        _need("state_in", state_in, dtype=torch.float32, numel=n_state)
+    if o is not None:
+        _need("o", o, v.shape, q.dtype)
+    if workspace is not None:
+        _need("workspace", workspace)
+    dev = _cuda_device([("q", q), ("k", k), ("v", v), ("log_decay", log_decay), ("state_in", state_in), ("o", o),
+                        ("workspace", workspace)])
+    ref = ctypes.byref(shp)
+    with _On(dev, stream) as raw:
+        if o is None:
+            o = torch.empty(v.shape, dtype=q.dtype, device=dev)
+        st = torch.empty(n_state, dtype=torch.float32, device=dev) if want_state else None
+        ws, wp, wb = _scratch(lib.ia_linear_prefill_workspace_bytes(ref), dev, workspace)
+        rc = lib.ia_linear_prefill_fwd(ref, _ptr(q), _ptr(k), _ptr(v), _ptr(log_decay),
+                                       shp.d_k ** -0.5 if scale is None else scale, _ptr(state_in), _ptr(o),
+                                       _ptr(st), wp, wb, raw)
+    _check(rc, "ia_linear_prefill_fwd")
+    return {"o": o, "state": st}
+
+
+def linear_fwd_bwd(q, k, v, log_decay, dO, scale=None, workspace=None, stream=None):
+    """Linear attention's training step from a zero state: dict(o, dq, dk, dv), all in the input dtype.
+    log_decay is a constant of the model and gets no gradient."""
+    lib = load_library()
+    shp = _check_linear_args(4, q, k, v, log_decay)
+    _need("dO", dO, v.shape, q.dtype)
+    if workspace is not None:
+        _need("workspace", workspace)
+    dev = _cuda_device([("q", q), ("k", k), ("v", v), ("log_decay", log_decay), ("dO", dO), ("workspace", workspace)])
+    ref = ctypes.byref(shp)
+    with _On(dev, stream) as raw:
+        o, dv = (torch.empty(v.shape, dtype=q.dtype, device=dev) for _ in range(2))
+        dq, dk = (torch.empty(q.shape, dtype=q.dtype, device=dev) for _ in range(2))
+        ws, wp, wb = _scratch(lib.ia_linear_fwd_bwd_workspace_bytes(ref), dev, workspace)
+        rc = lib.ia_linear_fwd_bwd(ref, _ptr(q), _ptr(k), _ptr(v), _ptr(log_decay),
+                                   shp.d_k ** -0.5 if scale is None else scale, _ptr(dO), _ptr(o), _ptr(dq),
+                                   _ptr(dk), _ptr(dv), wp, wb, raw)
+    _check(rc, "ia_linear_fwd_bwd")
+    return {"o": o, "dq": dq, "dk": dk, "dv": dv}
+
+
+def linear_decode_step(q, k, v, log_decay, state, scale=None, state_out=None, parents=None, o=None, stream=None):
+    """One token of linear attention: q, k [B,H,d_k], v [B,H,d_v]; returns dict(o, state).
+
+    The state (flat fp32) is updated in place, or written to state_out.  With parents [B/beams, beams] int32
+    sequence g*beams + j continues from the state of sequence g*beams + parents[g, j], and state_out must be
+    another buffer."""
+    lib = load_library()
+    shp = _check_linear_args(3, q, k, v, log_decay)
+    n_state = shp.B * shp.H * shp.d_k * shp.d_v
+    _need("state", state, dtype=torch.float32, numel=n_state)
+    if state_out is not None:
+        _need("state_out", state_out, dtype=torch.float32, numel=n_state)
+    beams = 0
+    if parents is not None:
+        _need("parents", parents, dtype=torch.int32, numel=shp.B)
+        if parents.dim() != 2:
+            raise ValueError(f"parents must be [B/beams, beams], got shape {tuple(parents.shape)}")
+        beams = parents.shape[1]
+        if state_out is None:
+            raise ValueError("state_out is needed with parents: a state may have several followers")
+    if o is not None:
+        _need("o", o, v.shape, q.dtype)
+    dev = _cuda_device([("q", q), ("k", k), ("v", v), ("log_decay", log_decay), ("state", state),
+                        ("state_out", state_out), ("parents", parents), ("o", o)])
+    out = state if state_out is None else state_out
+    with _On(dev, stream) as raw:
+        if o is None:
+            o = torch.empty(v.shape, dtype=q.dtype, device=dev)
+        rc = lib.ia_linear_decode_step(ctypes.byref(shp), _ptr(q), _ptr(k), _ptr(v), _ptr(log_decay),
+                                       shp.d_k ** -0.5 if scale is None else scale, _ptr(state), _ptr(parents),
+                                       beams, _ptr(out), _ptr(o), raw)
+    _check(rc, "ia_linear_decode_step")
+    return {"o": o, "state": out}
+
+
+def _check_rows(x, weight, bias=None):
+    _need("x", x)
+    if x.dim() < 1 or x.numel() == 0:
+        raise ValueError(f"x must be [..., D] and not empty, got shape {tuple(x.shape)}")
+    D = x.shape[-1]
+    _small("x", D)
+    for name, t in (("weight", weight), ("bias", bias)):
+        if t is not None:
+            _need(name, t, (D,), torch.float32)
+    return x.numel() // D, D, _dtype_code(x)
+
+
+def layer_norm_fwd(x, weight=None, bias=None, eps=1e-5, y=None, stream=None):
+    """Layer norm over the last axis of x [..., D] (fp32 or bf16), weight and bias [D] fp32 or None.
+    Returns dict(y, mean, rstd); mean and rstd [...] fp32 are what layer_norm_bwd takes.  y may be x."""
+    lib = load_library()
+    rows, D, code = _check_rows(x, weight, bias)
+    if y is not None:
+        _need("y", y, x.shape, x.dtype)
+    dev = _cuda_device([("x", x), ("weight", weight), ("bias", bias), ("y", y)])
+    with _On(dev, stream) as raw:
+        if y is None:
+            y = torch.empty(x.shape, dtype=x.dtype, device=dev)
+        mean = torch.empty(x.shape[:-1], dtype=torch.float32, device=dev)
+        rstd = torch.empty(x.shape[:-1], dtype=torch.float32, device=dev)
+        rc = lib.ia_layer_norm_fwd(rows, D, code, _ptr(x), _ptr(weight), _ptr(bias), eps, _ptr(y), _ptr(mean),
+                                   _ptr(rstd), raw)
+    _check(rc, "ia_layer_norm_fwd")
+    return {"y": y, "mean": mean, "rstd": rstd}
+
+
+def layer_norm_bwd_workspace_bytes(rows, D, dtype) -> int:
+    code = dtype if isinstance(dtype, int) else (IA_BF16 if dtype in (torch.bfloat16, "bf16") else IA_F32)
+    return int(load_library().ia_layer_norm_bwd_workspace_bytes(int(rows), int(D), code))
+
+
+def layer_norm_bwd(dy, x, mean, rstd, weight=None, want_params=True, dx=None, workspace=None, stream=None):
+    """Gradients of layer_norm_fwd from the mean and rstd it returned: dict(dx, dweight, dbias), dx in x's dtype,
+    dweight and dbias [D] fp32 summed over the rows (None with want_params=False).  dx may be dy or x."""
+    lib = load_library()
+    rows, D, code = _check_rows(x, weight)
+    _need("dy", dy, x.shape, x.dtype)
+    for name, t in (("mean", mean), ("rstd", rstd)):
+        _need(name, t, dtype=torch.float32, numel=rows)
+    if dx is not None:
+        _need("dx", dx, x.shape, x.dtype)
+    if workspace is not None:
+        _need("workspace", workspace)
+    dev = _cuda_device([("x", x), ("dy", dy), ("mean", mean), ("rstd", rstd), ("weight", weight), ("dx", dx),
+                        ("workspace", workspace)])
+    with _On(dev, stream) as raw:
+        if dx is None:
+            dx = torch.empty(x.shape, dtype=x.dtype, device=dev)
+        dw = db = ws = wp = None
+        wb = 0
+        if want_params:
+            dw = torch.empty(D, dtype=torch.float32, device=dev)
+            db = torch.empty(D, dtype=torch.float32, device=dev)
+            ws, wp, wb = _scratch(lib.ia_layer_norm_bwd_workspace_bytes(rows, D, code), dev, workspace)
+        rc = lib.ia_layer_norm_bwd(rows, D, code, _ptr(dy), _ptr(x), _ptr(weight), _ptr(mean), _ptr(rstd), _ptr(dx),
+                                   _ptr(dw), _ptr(db), wp, wb, raw)
+    _check(rc, "ia_layer_norm_bwd")
+    return {"dx": dx, "dweight": dw, "dbias": db}
+
+
+def beam_select_workspace_bytes(G, W, V, K, dtype) -> int:
+    code = dtype if isinstance(dtype, int) else (IA_BF16 if dtype in (torch.bfloat16, "bf16") else IA_F32)
+    return int(load_library().ia_beam_select_workspace_bytes(int(G), int(W), int(V), int(K), code))
+
+
+def beam_select(logits, scores, K, finished=None, end_token=0, workspace=None, stream=None):
+    """The K best continuations of each request over its beams and the vocabulary (see ia_beam_select in
+    include/ia.h): logits [G,W,V] (fp32 or bf16), scores [G,W] fp32 the beams' summed log probabilities, finished
+    [G,W] bool or uint8 or None.  Returns dict(scores [G,K] fp32, parents [G,K] int32, tokens [G,K] int32), best
+    first; a place without a candidate holds -inf, -1, -1."""
+    lib = load_library()
+    _need("logits", logits)
+    if logits.dim() != 3:
+        raise ValueError(f"logits must be [G,W,V], got shape {tuple(logits.shape)}")
+    code = _dtype_code(logits)
+    G, W, V = logits.shape
+    _small("logits", G, W, V, K)
+    _need("scores", scores, (G, W), torch.float32)
+    if finished is not None:
+        _need("finished", finished, (G, W))
+        if finished.dtype not in (torch.bool, torch.uint8):
+            raise TypeError(f"finished has dtype {finished.dtype}, expected bool or uint8")
+    if workspace is not None:
+        _need("workspace", workspace)
+    dev = _cuda_device([("logits", logits), ("scores", scores), ("finished", finished), ("workspace", workspace)])
+    with _On(dev, stream) as raw:
+        out = torch.empty(G, K, dtype=torch.float32, device=dev)
+        parents = torch.empty(G, K, dtype=torch.int32, device=dev)
+        tokens = torch.empty(G, K, dtype=torch.int32, device=dev)
+        ws, wp, wb = _scratch(lib.ia_beam_select_workspace_bytes(G, W, V, K, code), dev, workspace)
+        rc = lib.ia_beam_select(G, W, V, K, code, _ptr(logits), _ptr(scores), _ptr(finished), int(end_token), _ptr(out),
+                                _ptr(parents), _ptr(tokens), wp, wb, raw)
+    _check(rc, "ia_beam_select")
+    return {"scores": out, "parents": parents, "tokens": tokens}
+
+
+def _reorder(call, where, shp, per, B, state, parents, out, stream):
+    _need("state", state, dtype=torch.float32, numel=per * B)
+    _need("parents", parents, dtype=torch.int32)
+    if parents.dim() != 2 or parents.numel() == 0 or B % parents.shape[0]:
+        raise ValueError(f"parents must be [requests, beams] with requests dividing B = {B}, got {tuple(parents.shape)}")
+    G, wout = parents.shape
+    if out is not None:
+        _need("out", out, dtype=torch.float32, numel=per * G * wout)
+    dev = _cuda_device([("state", state), ("parents", parents), ("out", out)])
+    with _On(dev, stream) as raw:
+        if out is None:
+            out = torch.empty(per * G * wout, dtype=torch.float32, device=dev)
+        rc = call(ctypes.byref(shp), B // G, wout, _ptr(parents), _ptr(state), _ptr(out), raw)
+    _check(rc, where)
+    return out
+
+
+def state_reorder(state, parents, B, H, M, d_xi, d_v, out=None, stream=None):
+    """The layer's states after a beam selection: sequence g*beams + j of the result is sequence g*(B/G) +
+    parents[g, j] of state (flat fp32, B sequences), parents [G, beams] int32; a parent of -1 gives a zero state.
+    Returns out (allocated here when None); out=state reorders in place, moving only the beams that change."""
+    shp = make_shape(B, H, 1, d_xi, d_v, M, IA_F32)
+    return _reorder(load_library().ia_state_reorder, "ia_state_reorder", shp, state_bytes(1, H, M, d_xi, d_v) // 4, B,
+                    state, parents, out, stream)
+
+
+def linear_state_reorder(state, parents, B, H, d_k, d_v, out=None, stream=None):
+    """state_reorder for linear attention's states [B,H,d_k,d_v]."""
+    shp = _linear_shape(B, H, 1, d_k, d_v, IA_F32)
+    return _reorder(load_library().ia_linear_state_reorder, "ia_linear_state_reorder", shp, H * d_k * d_v, B, state,
+                    parents, out, stream)
 
 
 def set_launch_events(begin=None, end=None):
