@@ -62,14 +62,13 @@ __global__ void __launch_bounds__(kThreads) lin_simt_kernel(const __grid_constan
   const int nseg = STATE_ONLY ? a.nseg - 1 : a.nseg;
   const long long stream = blockIdx.x / nseg;
   const int seg = static_cast<int>(blockIdx.x - stream * nseg);
+  const long long bh = stream / a.first[a.nprob];
+  const int block = static_cast<int>(stream - bh * a.first[a.nprob]);
   int pi = 0;
-  while (pi + 1 < a.nprob && stream >= a.first[pi + 1]) ++pi;
+  while (pi + 1 < a.nprob && block >= a.first[pi + 1]) ++pi;
   const LinProblem& pr = a.p[pi];
   const int dx = pr.dx, dz = pr.dz;
-  const int zb = (dz + kLinZB - 1) / kLinZB;
-  const long long local = stream - a.first[pi];
-  const long long bh = local / zb;
-  const int z0 = static_cast<int>(local - bh * zb) * kLinZB;
+  const int z0 = (block - a.first[pi]) * kLinZB;
   const int zw = min(kLinZB, dz - z0);
   const int h = static_cast<int>(bh % a.H);
 
@@ -274,7 +273,7 @@ __global__ void __launch_bounds__(kThreads) lin_carry_kernel(const __grid_consta
 template <int C, bool BF16>
 cudaError_t simt_launch(const LinArgs& a, int max_dx, bool state_only, cudaStream_t st) {
   const size_t bytes = sizeof(float) * simt_smem(max_dx, C).total;
-  const long long grid = static_cast<long long>(a.first[a.nprob]) * (state_only ? a.nseg - 1 : a.nseg);
+  const long long grid = static_cast<long long>(a.BH) * a.first[a.nprob] * (state_only ? a.nseg - 1 : a.nseg);
   if (grid > (1LL << 31) - 1) return cudaErrorInvalidConfiguration;
   auto kern = state_only ? lin_simt_kernel<C, BF16, true> : lin_simt_kernel<C, BF16, false>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(bytes));
@@ -367,7 +366,7 @@ size_t seg_floats(const ia_linear_shape_t& s, const LinPlan& p) {
 // Runs the problems in a: the segments' states first when there are several.
 cudaError_t run_problems(LinArgs& a, const LinPlan& p, bool bf16, cudaStream_t st) {
   a.first[0] = 0;
-  for (int i = 0; i < a.nprob; ++i) a.first[i + 1] = a.first[i] + a.BH * lin_zblocks(a.p[i].dz);
+  for (int i = 0; i < a.nprob; ++i) a.first[i + 1] = a.first[i] + lin_zblocks(a.p[i].dz);
   auto pass = [&](bool state_only) {
     return p.tc ? launch_lin_tc(a, state_only, st) : launch_lin_simt(a, bf16, p.chunk, state_only, st);
   };

@@ -28,7 +28,7 @@ struct LinProblem {
 struct LinArgs {
   LinProblem p[4];
   int nprob;
-  int first[5];             // prefix counts of streams ((b,h) x blocks of 64 columns of z) per problem
+  int first[5];             // prefix counts over the problems of a (b,h)'s blocks of 64 columns of z
   int BH, H, N;
   int nch;                  // chunks per sequence
   int nseg, cps;            // segments per sequence, chunks per segment

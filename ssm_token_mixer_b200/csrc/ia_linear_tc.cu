@@ -1,5 +1,544 @@
+// Linear attention with one decay per head on the tensor cores: the chunk
+// algebra of ia_linear.cu with C = 128 tokens per chunk, for bf16 inputs with
+// widths 64 and 128.
+//
+// One CTA carries one (b,h), one block of 64 columns of z and one segment of
+// the sequence, chunk after chunk.  Four contractions per chunk (tcgen05, bf16
+// operands, fp32 accumulators in TMEM):
+//   G1  A  = X Y^T            128 x 128 x dx   operands straight from TMA
+//   G2  O2 = P Z              128 x 64 x 128   P = decayed, masked A, from TMEM
+//   G3  O1 = X S              128 x 64 x dx    S = the entering state in bf16
+//   G4  K  = Y^T (w Z)        dx x 64 x 256    w z in two bf16 parts, stacked along tokens
+//   out = scale (O2 + lambda^(p+1) O1),  S <- lambda^L S + K in fp32 registers
+//
+// Rounding.  Decays multiply fp32 accumulators wherever they can: A before it
+// is rounded to P, O1 after the product, S in registers.  Only the weights
+// w = lambda^(L-1-p) of G4 sit on a contracted index; w z is split into hi +
+// lo bf16 parts (2^-16 of a value left over), so that the fp32 state that is
+// carried and returned keeps fp32-like accuracy.  P and the S operand are
+// rounded to bf16 once, like the output.
+//
+// Roles (448 threads, four warps at most per register file: 128 registers):
+//   warps 0-3   P: A from TMEM, decayed, back to TMEM as the A operand of G2.
+//               lambda^(t-s) = lambda^(t - e) lambda^(e - s) over groups of 32
+//               columns that end at e <= t: both factors <= 1 and constant per
+//               thread.  Groups on the other side of the diagonal are zero and
+//               not read.
+//   warps 4-7   O: O1, O2 from TMEM, out through shared memory and a TMA store
+//   warps 8-11  S: w z for G4, then the state: K from TMEM, S in registers,
+//               S in bf16 to shared memory for the next chunk's G3
+//   warp 12     TMA loads        warp 13   issues G1-G4
+// G1 of the next chunk is issued before G2 of this one, so P overlaps the
+// products.  Waits are bounded mbarrier waits with a CTA-wide abort flag.
+#include <algorithm>
+#include <cuda.h>
+
+#include "ia_device.cuh"
+#include "ia_internal.h"
 #include "ia_linear.h"
+
 namespace ia {
-bool lin_tc_supported(const ia_linear_shape_t&) { return false; }
-cudaError_t launch_lin_tc(const LinArgs&, bool, cudaStream_t) { return cudaErrorNotSupported; }
+
+using EncodeTiledFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
+                                   const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
+                                   CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+EncodeTiledFn encode_tiled();   // ia_prefill_tc.cu
+
+namespace {
+
+constexpr int C = kLinTcChunk;
+constexpr int kBox = C * 128;           // 64 bf16 columns x 128 tokens, 128-byte swizzled: 16 KB
+constexpr int kRoleThreads = 128;
+constexpr int kThreads = 3 * kRoleThreads + 64;
+constexpr uint32_t kAtom = 1024;        // 8 rows of 128 bytes
+
+// TMEM columns
+constexpr uint32_t kTA = 0, kTO1 = 256, kTO2 = 320, kTK = 384;
+
+template <int MAXDX>
+struct Cfg {
+  static constexpr int NB = MAXDX == 64 ? 3 : 2;        // stages of X, Y, Z
+  static constexpr int TX = MAXDX / 64 * kBox;
+  static constexpr int STAGE = 2 * TX + kBox;
+  static constexpr int S_ZW = NB * STAGE;               // hi, lo
+  static constexpr int S_SB = S_ZW + 2 * kBox;          // [dx][64] bf16, 128-byte swizzled
+  static constexpr int S_OUT = S_SB + MAXDX * 128;
+  static constexpr int S_BAR = S_OUT + kBox;
+  static constexpr int SMEM = S_BAR + 256 + 1024;       // + alignment of the base
+};
+
+enum Bar { kFull = 0, kFree = 3, kAFull = 6, kPReady = 8, kSReady = 10, kSFree, kZReady, kKFull, kOFull, kOFree, kDrain, kBars };
+
+struct Maps {
+  CUtensorMap m[8];    // q, k, v, dO and o, dq, dk, dv (a prefill: q, k, v and o at 4)
+};
+struct MapIdx {
+  int x, y, z, out;
+};
+struct TcParams {
+  LinArgs a;
+  MapIdx mi[4];
+};
+
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+  const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+__device__ __forceinline__ float bf_lo(uint32_t w) { return __uint_as_float(w << 16); }
+__device__ __forceinline__ float bf_hi(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
+
+// kind::f16 instruction descriptor with bf16 A and B, fp32 D.
+__host__ __device__ constexpr uint32_t idesc_bf16(int M, int N, int a_mn, int b_mn) {
+  return idesc_f16(M, N, a_mn, b_mn) | (1u << 7) | (1u << 10);
+}
+
+template <int MAXDX, bool STATE_ONLY>
+__global__ void __launch_bounds__(512, 1) lin_tc_kernel(const __grid_constant__ TcParams prm,
+                                                        const __grid_constant__ Maps maps) {
+  using K = Cfg<MAXDX>;
+  constexpr int NB = K::NB;
+  extern __shared__ uint8_t raw[];
+  uint8_t* smem = raw + ((1024u - (smem_u32(raw) & 1023u)) & 1023u);
+  const LinArgs& a = prm.a;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+
+  // (b,h), problem, block of z columns, segment
+  const int nseg = STATE_ONLY ? a.nseg - 1 : a.nseg;
+  const long long stream = blockIdx.x / nseg;
+  const int seg = static_cast<int>(blockIdx.x - stream * nseg);
+  const int per = a.first[a.nprob];
+  const int bh = static_cast<int>(stream / per);
+  const int r = static_cast<int>(stream - static_cast<long long>(bh) * per);
+  int pi = 0;
+  while (pi + 1 < a.nprob && r >= a.first[pi + 1]) ++pi;
+  const LinProblem& pr = a.p[pi];
+  const int z0 = (r - a.first[pi]) * kLinZB;
+  const int dx = pr.dx, dz = pr.dz, nbx = dx / 64;
+  const bool rev = pr.reverse != 0;
+  const int h = bh % a.H;
+  const int c0 = seg * a.cps, n = min(a.nch, c0 + a.cps) - c0;
+  auto chunk_at = [&](int c) { return rev ? a.nch - 1 - (c0 + c) : c0 + c; };
+
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + K::S_BAR);
+  uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(smem + K::S_BAR + 8 * kBars);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + K::S_BAR + 8 * kBars + 4);
+  int* bad = reinterpret_cast<int*>(smem + K::S_BAR + 8 * kBars + 8);   // [2]
+  static_assert(8 * kBars + 16 <= 256, "barriers and flags fit their slot");
+  const uint32_t sbase = smem_u32(smem);
+  auto sX = [&](int s) { return s * K::STAGE; };
+  auto sY = [&](int s) { return s * K::STAGE + K::TX; };
+  auto sZ = [&](int s) { return s * K::STAGE + 2 * K::TX; };
+
+  if (warp == 0) {
+    tmem_alloc(tmem_holder, 512);
+    tmem_relinquish();
+  }
+  if (tid == 32) {
+    for (int i = 0; i < 3; ++i) {
+      mbar_init(bars + kFull + i, 1);
+      mbar_init(bars + kFree + i, 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(bars + kAFull + i, 1);
+      mbar_init(bars + kPReady + i, 4);
+      bad[i] = C;
+    }
+    mbar_init(bars + kSReady, 4);
+    mbar_init(bars + kSFree, 1);
+    mbar_init(bars + kZReady, 4);
+    mbar_init(bars + kKFull, 1);
+    mbar_init(bars + kOFull, 1);
+    mbar_init(bars + kOFree, 4);
+    mbar_init(bars + kDrain, 1);
+    *abort_flag = 0;
+    fence_barrier_init();
+  }
+  const float graw = a.log_decay[h];
+  if (tid == 0 && !(graw <= 0.f)) atomicOr(a.err, kErrParamRange);
+  const float g = lin_log_decay(graw);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_holder;
+  auto wait = [&](int bar, uint32_t parity) { return mbar_wait_or_abort(bars + bar, parity & 1u, a.err, abort_flag); };
+  // one outcome for a warp: what follows is warp-wide
+  auto warp_wait = [&](int bar, uint32_t parity) { return __all_sync(0xffffffffu, wait(bar, parity)) != 0; };
+
+  if (warp < 4) {
+    // ------------------------------------------------------------------- P
+    if (!STATE_ONLY) {
+      const int t = tid;   // row of the chunk
+      // within group gr of 32 columns: column 32 gr + j is lambda^(e_j) from the
+      // group's near end, the row is `far` from that end
+      float e[32], dg[32];
+#pragma unroll
+      for (int j = 0; j < 32; ++j) {
+        e[j] = expf(g * (rev ? j : 31 - j));
+        const int d = rev ? j - lane : lane - j;
+        dg[j] = d >= 0 ? expf(g * d) : 0.f;
+      }
+      float rowf[4];
+#pragma unroll
+      for (int gr = 0; gr < 4; ++gr) {
+        const int far = rev ? 32 * gr - t : t - (32 * gr + 31);
+        rowf[gr] = far >= 0 ? expf(g * far) : 0.f;
+      }
+      for (int c = 0; c < n; ++c) {
+        const int b = c & 1;
+        if (!warp_wait(kAFull + b, c >> 1)) break;
+        tc_fence_after();
+        const uint32_t ta = tmem + (static_cast<uint32_t>(warp) << 21) + kTA + 128 * b;
+#pragma unroll
+        for (int gr = 0; gr < 4; ++gr) {
+          uint32_t w[16];
+          const int side = rev ? gr - warp : warp - gr;   // > 0: whole group, 0: the diagonal one, < 0: nothing
+          if (side < 0) {
+#pragma unroll
+            for (int i = 0; i < 16; ++i) w[i] = 0u;
+          } else {
+            uint32_t v0[16], v1[16];
+            tmem_ld16(ta + 32 * gr, v0);
+            tmem_ld16(ta + 32 * gr + 16, v1);
+            tmem_ld_wait16(v0);
+            tmem_ld_wait16(v1);
+            if (side > 0) {
+              const float f = rowf[gr];
+#pragma unroll
+              for (int i = 0; i < 8; ++i) {
+                w[i] = pack_bf16(__uint_as_float(v0[2 * i]) * f * e[2 * i], __uint_as_float(v0[2 * i + 1]) * f * e[2 * i + 1]);
+                w[8 + i] = pack_bf16(__uint_as_float(v1[2 * i]) * f * e[16 + 2 * i],
+                                     __uint_as_float(v1[2 * i + 1]) * f * e[17 + 2 * i]);
+              }
+            } else {
+              // select, not multiply: a masked score may be infinite or NaN
+              auto val = [&](uint32_t v, int j) {
+                return (rev ? j >= lane : j <= lane) ? __uint_as_float(v) * dg[j] : 0.f;
+              };
+#pragma unroll
+              for (int i = 0; i < 8; ++i) {
+                w[i] = pack_bf16(val(v0[2 * i], 2 * i), val(v0[2 * i + 1], 2 * i + 1));
+                w[8 + i] = pack_bf16(val(v1[2 * i], 16 + 2 * i), val(v1[2 * i + 1], 17 + 2 * i));
+              }
+            }
+          }
+          tmem_st16(ta + 16 * gr, w);   // columns of A that this lane has read already
+        }
+        tmem_st_wait();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bars + kPReady + b);
+      }
+    }
+  } else if (warp < 8) {
+    // ------------------------------------------------------------------- O
+    if (!STATE_ONLY) {
+      const int t = tid - kRoleThreads;
+      const int p = rev ? C - 1 - t : t;
+      const float scale = a.scale, hd = a.scale * expf(g * (p + 1));
+      const CUtensorMap* mo = &maps.m[prm.mi[pi].out];
+      uint8_t* row = smem + K::S_OUT + t * 128;
+      for (int c = 0; c < n; ++c) {
+        const bool ok = warp_wait(kOFull, c);
+        tc_fence_after();
+        const uint32_t to = tmem + (static_cast<uint32_t>(warp - 4) << 21);
+        uint32_t w[32];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          if (!ok) break;
+          uint32_t v1[16], v2[16];
+          tmem_ld16(to + kTO1 + 16 * q, v1);
+          tmem_ld16(to + kTO2 + 16 * q, v2);
+          tmem_ld_wait16(v1);
+          tmem_ld_wait16(v2);
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            w[8 * q + i] = pack_bf16(fmaf(hd, __uint_as_float(v1[2 * i]), scale * __uint_as_float(v2[2 * i])),
+                                     fmaf(hd, __uint_as_float(v1[2 * i + 1]), scale * __uint_as_float(v2[2 * i + 1])));
+        }
+        const int from = *reinterpret_cast<volatile int*>(bad + (c & 1));
+        if (p >= from)
+#pragma unroll
+          for (int i = 0; i < 32; ++i) w[i] = 0x7fc07fc0u;   // NaN
+        tc_fence_before();
+        if (t == 0) bulk_wait_read_0();                      // the last store has left the staging tile
+        if (named_sync_or(1, kRoleThreads, !ok)) break;      // one outcome for the role
+        if (t == 0 && from < C) bad[c & 1] = C;
+        if (lane == 0) mbar_arrive(bars + kOFree);
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+          *reinterpret_cast<uint4*>(row + ((j ^ (t & 7)) << 4)) = make_uint4(w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]);
+        fence_async_smem();
+        named_sync(1, kRoleThreads);
+        if (t == 0) {
+          tma_store_3d(mo, sbase + K::S_OUT, z0, chunk_at(c) * C, bh);
+          bulk_commit();
+        }
+      }
+      if (t == 0) bulk_wait_all();
+    }
+  } else if (warp < 12) {
+    // ------------------------------------------------------------------- S
+    const int u = tid - 2 * kRoleThreads;
+    const bool holds = u < dx;   // thread u carries row u of S
+    const long long per_state = static_cast<long long>(dx) * dz;
+    float S[64];
+    {
+      const float* s0 = seg == 0 ? (pr.state_in ? pr.state_in + bh * per_state : nullptr)
+                                 : STATE_ONLY ? nullptr : pr.seg + (static_cast<long long>(bh) * (a.nseg - 1) + seg - 1) * per_state;
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (s0 && holds) v = *reinterpret_cast<const float4*>(s0 + static_cast<long long>(u) * dz + z0 + 4 * i);
+        S[4 * i] = v.x, S[4 * i + 1] = v.y, S[4 * i + 2] = v.z, S[4 * i + 3] = v.w;
+      }
+    }
+    auto write_operand = [&]() {
+      if (holds)
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+          *reinterpret_cast<uint4*>(smem + K::S_SB + u * 128 + ((j ^ (u & 7)) << 4)) =
+              make_uint4(pack_bf16(S[8 * j], S[8 * j + 1]), pack_bf16(S[8 * j + 2], S[8 * j + 3]),
+                         pack_bf16(S[8 * j + 4], S[8 * j + 5]), pack_bf16(S[8 * j + 6], S[8 * j + 7]));
+      fence_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bars + kSReady);
+    };
+    if (!STATE_ONLY) write_operand();
+
+    // weights of this thread's rows (16 it + u / 8) of a whole chunk
+    float wf[8];
+#pragma unroll
+    for (int it = 0; it < 8; ++it) {
+      const int t = 16 * it + (u >> 3);
+      wf[it] = expf(g * (C - 1 - (rev ? C - 1 - t : t)));
+    }
+    for (int c = 0; c < n; ++c) {
+      const int s = c % NB;
+      const int L = min(C, a.N - chunk_at(c) * C);
+      const int Lw = rev ? C : L;
+      // w z, in two bf16 parts, at z's own offsets (row = token)
+      if (!warp_wait(kFull + s, c / NB)) break;
+      uint32_t top = 0u;
+#pragma unroll
+      for (int it = 0; it < 8; ++it) {
+        const uint32_t off = (it * kRoleThreads + u) * 16;
+        const int t = 16 * it + (u >> 3);
+        const uint4 z = *reinterpret_cast<const uint4*>(smem + sZ(s) + off);
+        const float w = Lw == C ? wf[it] : t < L ? expf(g * (L - 1 - t)) : 0.f;
+        const uint32_t zz[4] = {z.x, z.y, z.z, z.w};
+        uint32_t hi[4], lo[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          top = __vmaxu2(top, zz[e] & 0x7fff7fffu);
+          const float v0 = bf_lo(zz[e]) * w, v1 = bf_hi(zz[e]) * w;
+          hi[e] = pack_bf16(v0, v1);
+          lo[e] = pack_bf16(v0 - bf_lo(hi[e]), v1 - bf_hi(hi[e]));
+        }
+        *reinterpret_cast<uint4*>(smem + K::S_ZW + off) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+        *reinterpret_cast<uint4*>(smem + K::S_ZW + kBox + off) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+      }
+      if (!STATE_ONLY && ((top & 0xffffu) >= 0x7f80u || (top >> 16) >= 0x7f80u)) {
+        // A NaN or infinity in z: 0 * z of the masked half would reach the
+        // tokens before it.  G2 reads a zero instead and the output warps write
+        // NaN from its token on.
+        for (int it = 0; it < 8; ++it) {
+          uint32_t* z = reinterpret_cast<uint32_t*>(smem + sZ(s) + (it * kRoleThreads + u) * 16);
+          const int t = 16 * it + (u >> 3);
+          for (int e = 0; e < 4; ++e) {
+            uint32_t w = z[e];
+            if ((w & 0x7f80u) == 0x7f80u) w &= 0xffff0000u;
+            if ((w & 0x7f800000u) == 0x7f800000u) w &= 0x0000ffffu;
+            if (w != z[e]) {
+              z[e] = w;
+              atomicMin(bad + (c & 1), rev ? C - 1 - t : t);
+            }
+          }
+        }
+      }
+      fence_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bars + kZReady);
+
+      // S <- lambda^L S + K
+      const float dec = expm1f(g * Lw);
+      if (!warp_wait(kKFull, c)) break;
+      tc_fence_after();
+      if (32 * (warp - 8) < dx) {
+        const uint32_t tk = tmem + (static_cast<uint32_t>(warp - 8) << 21) + kTK;
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          uint32_t v[16];
+          tmem_ld16(tk + 16 * q, v);
+          tmem_ld_wait16(v);
+#pragma unroll
+          for (int i = 0; i < 16; ++i) S[16 * q + i] = fmaf(dec, S[16 * q + i], S[16 * q + i]) + __uint_as_float(v[i]);
+        }
+      }
+      tc_fence_before();
+      if (!STATE_ONLY && c + 1 < n) {
+        if (!warp_wait(kSFree, c)) break;   // G3 has read the old operand
+        write_operand();
+      }
+    }
+    float* dst = STATE_ONLY ? pr.seg + (static_cast<long long>(bh) * (a.nseg - 1) + seg) * per_state
+                            : (pr.state_out && seg == a.nseg - 1) ? pr.state_out + bh * per_state : nullptr;
+    if (dst && holds)
+#pragma unroll
+      for (int i = 0; i < 16; ++i)
+        *reinterpret_cast<float4*>(dst + static_cast<long long>(u) * dz + z0 + 4 * i) =
+            make_float4(S[4 * i], S[4 * i + 1], S[4 * i + 2], S[4 * i + 3]);
+  } else if (warp == 12) {
+    // ---------------------------------------------------------------- loads
+    if (lane == 0) {
+      const CUtensorMap *mx = &maps.m[prm.mi[pi].x], *my = &maps.m[prm.mi[pi].y], *mz = &maps.m[prm.mi[pi].z];
+      int issued = 0;
+      for (int c = 0; c < n; ++c) {
+        const int s = c % NB;
+        if (c >= NB && !wait(kFree + s, c / NB - 1)) break;
+        const int t0 = chunk_at(c) * C;
+        mbar_arrive_expect_tx(bars + kFull + s, ((STATE_ONLY ? 1 : 2) * nbx + 1) * kBox);
+        for (int x = 0; x < nbx; ++x) {
+          if (!STATE_ONLY) tma_load_3d(sbase + sX(s) + x * kBox, mx, 64 * x, t0, bh, bars + kFull + s);
+          tma_load_3d(sbase + sY(s) + x * kBox, my, 64 * x, t0, bh, bars + kFull + s);
+        }
+        tma_load_3d(sbase + sZ(s), mz, z0, t0, bh, bars + kFull + s);
+        issued = c + 1;
+      }
+      // no copy lands after the block exits
+      for (int c = max(0, issued - NB); c < issued; ++c) mbar_wait(bars + kFull + c % NB, (c / NB) & 1, a.err);
+    }
+    __syncwarp();
+  } else {
+    // ------------------------------------------------------------------ MMA
+    if (lane == 0) {
+      bool issued = false;
+      auto kstep = [](int kk) { return static_cast<uint32_t>((kk >> 2) * kBox + (kk & 3) * 32); };   // K-major, 64-column boxes
+      auto g1 = [&](int c) {
+        const int s = c % NB;
+        for (int kk = 0; kk < nbx * 4; ++kk)
+          mma_f16(tmem + kTA + 128 * (c & 1), smem_desc_sw128(sbase + sX(s) + kstep(kk), 16, kAtom),
+                  smem_desc_sw128(sbase + sY(s) + kstep(kk), 16, kAtom), idesc_bf16(128, 128, 0, 0), kk > 0);
+        mma_commit(bars + kAFull + (c & 1));
+      };
+      auto g3 = [&](int c) {
+        const int s = c % NB;
+        for (int kk = 0; kk < nbx * 4; ++kk)
+          mma_f16(tmem + kTO1, smem_desc_sw128(sbase + sX(s) + kstep(kk), 16, kAtom),
+                  smem_desc_sw128(sbase + K::S_SB + kk * 2 * kAtom, kBox, kAtom), idesc_bf16(128, 64, 0, 1), kk > 0);
+        mma_commit(bars + kSFree);
+      };
+      auto g4 = [&](int c) {
+        // rows of K past dx (a second 64-row block when dx = 64) are taken from
+        // the next tile of the stage and never read
+        const int s = c % NB;
+        for (int kk = 0; kk < 16; ++kk)
+          mma_f16(tmem + kTK, smem_desc_sw128(sbase + sY(s) + (kk & 7) * 2 * kAtom, kBox, kAtom),
+                  smem_desc_sw128(sbase + K::S_ZW + kk * 2 * kAtom, kBox, kAtom), idesc_bf16(128, 64, 1, 1), kk > 0);
+        mma_commit(bars + kKFull);
+      };
+      auto g2 = [&](int c) {
+        const int s = c % NB;
+        for (int kk = 0; kk < 8; ++kk)
+          mma_f16_ts(tmem + kTO2, tmem + kTA + 128 * (c & 1) + 8 * kk,
+                     smem_desc_sw128(sbase + sZ(s) + kk * 2 * kAtom, kBox, kAtom), idesc_bf16(128, 64, 0, 1), kk > 0);
+        mma_commit(bars + kOFull);
+      };
+      bool ok = true;
+      if (!STATE_ONLY) {
+        ok = wait(kFull, 0);
+        if (ok) {
+          tc_fence_after();
+          g1(0);
+          issued = true;
+        }
+      }
+      for (int c = 0; ok && c < n; ++c) {
+        if (!STATE_ONLY) {
+          if (!wait(kSReady, c) || (c > 0 && !wait(kOFree, c - 1))) break;
+          tc_fence_after();
+          g3(c);
+        }
+        if (!wait(kFull + c % NB, c / NB) || !wait(kZReady, c)) break;
+        tc_fence_after();
+        g4(c);
+        issued = true;
+        if (!STATE_ONLY) {
+          if (c + 1 < n) {
+            if (!wait(kFull + (c + 1) % NB, (c + 1) / NB)) break;
+            tc_fence_after();
+            g1(c + 1);
+          }
+          if (!wait(kPReady + (c & 1), c >> 1)) break;
+          tc_fence_after();
+          g2(c);
+        }
+        mma_commit(bars + kFree + c % NB);
+      }
+      if (issued) {   // every product is done before TMEM and shared memory go
+        mma_commit(bars + kDrain);
+        mbar_wait(bars + kDrain, 0, a.err);
+      }
+    }
+    __syncwarp();
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 0) tmem_dealloc(tmem, 512);
+}
+
+// [BH][N][W] bf16 as boxes of 64 columns x 128 tokens of one (b,h), 128-byte
+// swizzled; tokens past N read as zero and are not written.
+bool encode_map(CUtensorMap* m, const void* x, int BH, int N, int W) {
+  const EncodeTiledFn enc = encode_tiled();
+  if (!enc) return false;
+  const cuuint64_t dims[3] = {static_cast<cuuint64_t>(W), static_cast<cuuint64_t>(N), static_cast<cuuint64_t>(BH)};
+  const cuuint64_t strides[2] = {static_cast<cuuint64_t>(W) * 2, static_cast<cuuint64_t>(N) * W * 2};
+  const cuuint32_t box[3] = {64, C, 1};
+  const cuuint32_t estr[3] = {1, 1, 1};
+  return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(x), dims, strides, box, estr,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int MAXDX>
+cudaError_t launch(const TcParams& prm, const Maps& maps, bool state_only, cudaStream_t st) {
+  const LinArgs& a = prm.a;
+  const long long grid = static_cast<long long>(a.BH) * a.first[a.nprob] * (state_only ? a.nseg - 1 : a.nseg);
+  if (grid > (1LL << 31) - 1) return cudaErrorInvalidConfiguration;
+  auto kern = state_only ? lin_tc_kernel<MAXDX, true> : lin_tc_kernel<MAXDX, false>;
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<MAXDX>::SMEM);
+  if (e != cudaSuccess) return e;
+  kern<<<static_cast<unsigned>(grid), kThreads, Cfg<MAXDX>::SMEM, st>>>(prm, maps);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+bool lin_tc_supported(const ia_linear_shape_t& s) {
+  return s.in_dtype == IA_BF16 && (s.d_k == 64 || s.d_k == 128) && (s.d_v == 64 || s.d_v == 128);
+}
+
+cudaError_t launch_lin_tc(const LinArgs& a, bool state_only, cudaStream_t st) {
+  TcParams prm = {};
+  prm.a = a;
+  Maps maps;
+  const void* seen[8] = {};
+  int width[8] = {}, count = 0, maxdx = 0;
+  auto index = [&](const void* x, int W) {   // one map per tensor, whichever roles it has
+    for (int i = 0; i < count; ++i)
+      if (seen[i] == x && width[i] == W) return i;
+    if (count == 8 || !encode_map(&maps.m[count], x, a.BH, a.N, W)) return -1;
+    seen[count] = x;
+    width[count] = W;
+    return count++;
+  };
+  for (int i = 0; i < a.nprob; ++i) {
+    const LinProblem& p = a.p[i];
+    prm.mi[i] = {index(p.x, p.dx), index(p.y, p.dx), index(p.z, p.dz), state_only ? 0 : index(p.out, p.dz)};
+    if (prm.mi[i].x < 0 || prm.mi[i].y < 0 || prm.mi[i].z < 0 || prm.mi[i].out < 0) return cudaErrorNotSupported;
+    maxdx = std::max(maxdx, p.dx);
+  }
+  return maxdx == 64 ? launch<64>(prm, maps, state_only, st) : launch<128>(prm, maps, state_only, st);
+}
+
 }  // namespace ia
