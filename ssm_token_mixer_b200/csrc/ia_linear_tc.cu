@@ -8,7 +8,7 @@
 //   G1  A  = X Y^T            128 x 128 x dx   operands straight from TMA
 //   G2  O2 = P Z              128 x 64 x 128   P = decayed, masked A, from TMEM
 //   G3  O1 = X S              128 x 64 x dx    S = the entering state in bf16
-//   G4  K  = Y^T (w Z)        dx x 64 x 256    w z in two bf16 parts, stacked along tokens
+//   G4  K  = Y^T (w Z)        dx x 128 x 128   w z in two bf16 parts, side by side
 //   out = scale (O2 + lambda^(p+1) O1),  S <- lambda^L S + K in fp32 registers
 //
 // Rounding.  Decays multiply fp32 accumulators wherever they can: A before it
@@ -24,12 +24,17 @@
 //               columns that end at e <= t: both factors <= 1 and constant per
 //               thread.  Groups on the other side of the diagonal are zero and
 //               not read.
-//   warps 4-7   O: O1, O2 from TMEM, out through shared memory and a TMA store
-//   warps 8-11  S: w z for G4, then the state: K from TMEM, S in registers,
-//               S in bf16 to shared memory for the next chunk's G3
+//   warps 4-7   O: w z of the next chunk for G4; then O1, O2 from TMEM, out
+//               through shared memory and a TMA store
+//   warps 8-11  S: K from TMEM, S in registers, S in bf16 to shared memory for
+//               the next chunk's G3
 //   warp 12     TMA loads        warp 13   issues G1-G4
-// G1 of the next chunk is issued before G2 of this one, so P overlaps the
-// products.  Waits are bounded mbarrier waits with a CTA-wide abort flag.
+// Per chunk G4, G1 of the next chunk, G3 and G2 are issued in this order, so
+// that P and the state work while the products of the other roles run.  The
+// loops of the roles are kept short on purpose: with everything unrolled the
+// warps spent six of seven issue slots waiting for instructions (three roles
+// of straight-line code do not fit an SM's instruction caches; ncu, B8 H16
+// N2048 d64).  Waits are bounded mbarrier waits with a CTA-wide abort flag.
 #include <algorithm>
 #include <cuda.h>
 
@@ -57,17 +62,19 @@ constexpr uint32_t kTA = 0, kTO1 = 256, kTO2 = 320, kTK = 384;
 
 template <int MAXDX>
 struct Cfg {
-  static constexpr int NB = MAXDX == 64 ? 3 : 2;        // stages of X, Y, Z
+  static constexpr int NB = 2;                          // stages of X, Y, Z
   static constexpr int TX = MAXDX / 64 * kBox;
   static constexpr int STAGE = 2 * TX + kBox;
-  static constexpr int S_ZW = NB * STAGE;               // hi, lo
-  static constexpr int S_SB = S_ZW + 2 * kBox;          // [dx][64] bf16, 128-byte swizzled
+  static constexpr int NZ = MAXDX == 64 ? 2 : 1;        // buffers of w z
+  static constexpr int S_ZW = NB * STAGE;               // each: hi, lo
+  static constexpr int S_SB = S_ZW + NZ * 2 * kBox;     // [dx][64] bf16, 128-byte swizzled
   static constexpr int S_OUT = S_SB + MAXDX * 128;
   static constexpr int S_BAR = S_OUT + kBox;
-  static constexpr int SMEM = S_BAR + 256 + 1024;       // + alignment of the base
+  static constexpr int S_POW = S_BAR + 256;             // lambda^n, n = 0 .. C - 1
+  static constexpr int SMEM = S_POW + C * 4 + 1024;     // + alignment of the base
 };
 
-enum Bar { kFull = 0, kFree = 3, kAFull = 6, kPReady = 8, kSReady = 10, kSFree, kZReady, kKFull, kOFull, kOFree, kDrain, kBars };
+enum Bar { kFull = 0, kFree = 3, kAFull = 6, kPReady = 8, kZReady = 10, kZFree = 12, kSReady = 14, kSFree, kKFull, kOFull, kOFree, kDrain, kBars };
 
 struct Maps {
   CUtensorMap m[8];    // q, k, v, dO and o, dq, dk, dv (a prefill: q, k, v and o at 4)
@@ -84,8 +91,28 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
   return *reinterpret_cast<const uint32_t*>(&h);
 }
+__device__ __forceinline__ uint32_t pack2(uint64_t v) {
+  float lo, hi;
+  f2_unpack(v, lo, hi);
+  return pack_bf16(lo, hi);
+}
+__device__ __forceinline__ uint64_t f2_add(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
 __device__ __forceinline__ float bf_lo(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float bf_hi(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
+
+// True in one lane of the (converged) warp.  Unlike a test of the lane number
+// it tells the compiler that a single thread runs the branch, so the operands
+// of the tensor-core and copy instructions in it go to uniform registers at
+// once instead of through a loop over the active lanes.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+  return p != 0;
+}
 
 // kind::f16 instruction descriptor with bf16 A and B, fp32 D.
 __host__ __device__ constexpr uint32_t idesc_bf16(int M, int N, int a_mn, int b_mn) {
@@ -100,7 +127,7 @@ __global__ void __launch_bounds__(512, 1) lin_tc_kernel(const __grid_constant__ 
   extern __shared__ uint8_t raw[];
   uint8_t* smem = raw + ((1024u - (smem_u32(raw) & 1023u)) & 1023u);
   const LinArgs& a = prm.a;
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
 
   // (b,h), problem, block of z columns, segment
   const int nseg = STATE_ONLY ? a.nseg - 1 : a.nseg;
@@ -139,13 +166,14 @@ __global__ void __launch_bounds__(512, 1) lin_tc_kernel(const __grid_constant__ 
       mbar_init(bars + kFree + i, 1);
     }
     for (int i = 0; i < 2; ++i) {
+      mbar_init(bars + kZReady + i, 4);
+      mbar_init(bars + kZFree + i, 1);
       mbar_init(bars + kAFull + i, 1);
       mbar_init(bars + kPReady + i, 4);
       bad[i] = C;
     }
     mbar_init(bars + kSReady, 4);
     mbar_init(bars + kSFree, 1);
-    mbar_init(bars + kZReady, 4);
     mbar_init(bars + kKFull, 1);
     mbar_init(bars + kOFull, 1);
     mbar_init(bars + kOFree, 4);
@@ -156,6 +184,8 @@ __global__ void __launch_bounds__(512, 1) lin_tc_kernel(const __grid_constant__ 
   const float graw = a.log_decay[h];
   if (tid == 0 && !(graw <= 0.f)) atomicOr(a.err, kErrParamRange);
   const float g = lin_log_decay(graw);
+  float* pw = reinterpret_cast<float*>(smem + K::S_POW);
+  if (tid < C) pw[tid] = expf(g * tid);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -168,57 +198,46 @@ __global__ void __launch_bounds__(512, 1) lin_tc_kernel(const __grid_constant__ 
     // ------------------------------------------------------------------- P
     if (!STATE_ONLY) {
       const int t = tid;   // row of the chunk
-      // within group gr of 32 columns: column 32 gr + j is lambda^(e_j) from the
-      // group's near end, the row is `far` from that end
-      float e[32], dg[32];
+      uint64_t e[16];      // lambda^(distance of column 32 gr + j from its group's near end), pairs
 #pragma unroll
-      for (int j = 0; j < 32; ++j) {
-        e[j] = expf(g * (rev ? j : 31 - j));
-        const int d = rev ? j - lane : lane - j;
-        dg[j] = d >= 0 ? expf(g * d) : 0.f;
-      }
-      float rowf[4];
-#pragma unroll
-      for (int gr = 0; gr < 4; ++gr) {
-        const int far = rev ? 32 * gr - t : t - (32 * gr + 31);
-        rowf[gr] = far >= 0 ? expf(g * far) : 0.f;
-      }
+      for (int i = 0; i < 16; ++i)
+        e[i] = rev ? f2_pack(pw[2 * i], pw[2 * i + 1]) : f2_pack(pw[31 - 2 * i], pw[30 - 2 * i]);
       for (int c = 0; c < n; ++c) {
         const int b = c & 1;
         if (!warp_wait(kAFull + b, c >> 1)) break;
         tc_fence_after();
         const uint32_t ta = tmem + (static_cast<uint32_t>(warp) << 21) + kTA + 128 * b;
-#pragma unroll
+#pragma unroll 1
         for (int gr = 0; gr < 4; ++gr) {
-          uint32_t w[16];
           const int side = rev ? gr - warp : warp - gr;   // > 0: whole group, 0: the diagonal one, < 0: nothing
+          uint32_t w[16];
           if (side < 0) {
 #pragma unroll
             for (int i = 0; i < 16; ++i) w[i] = 0u;
           } else {
-            uint32_t v0[16], v1[16];
-            tmem_ld16(ta + 32 * gr, v0);
-            tmem_ld16(ta + 32 * gr + 16, v1);
-            tmem_ld_wait16(v0);
-            tmem_ld_wait16(v1);
+            uint32_t v[2][16];
+            tmem_ld16(ta + 32 * gr, v[0]);
+            tmem_ld16(ta + 32 * gr + 16, v[1]);
+            const float f = pw[side > 0 ? (rev ? 32 * gr - t : t - 32 * gr - 31) : 0];
+            tmem_ld_wait16(v[0]);
+            tmem_ld_wait16(v[1]);
             if (side > 0) {
-              const float f = rowf[gr];
+              const uint64_t ff = f2_pack(f, f);
 #pragma unroll
-              for (int i = 0; i < 8; ++i) {
-                w[i] = pack_bf16(__uint_as_float(v0[2 * i]) * f * e[2 * i], __uint_as_float(v0[2 * i + 1]) * f * e[2 * i + 1]);
-                w[8 + i] = pack_bf16(__uint_as_float(v1[2 * i]) * f * e[16 + 2 * i],
-                                     __uint_as_float(v1[2 * i + 1]) * f * e[17 + 2 * i]);
+              for (int i = 0; i < 16; ++i) {
+                const uint32_t* x = &v[i >> 3][2 * (i & 7)];
+                float lo, hi;
+                f2_unpack(f2_mul(f2_mul(f2_pack(__uint_as_float(x[0]), __uint_as_float(x[1])), e[i]), ff), lo, hi);
+                w[i] = pack_bf16(lo, hi);
               }
             } else {
               // select, not multiply: a masked score may be infinite or NaN
-              auto val = [&](uint32_t v, int j) {
-                return (rev ? j >= lane : j <= lane) ? __uint_as_float(v) * dg[j] : 0.f;
+              auto val = [&](int j) {
+                const int d = rev ? j - lane : lane - j;
+                return d >= 0 ? __uint_as_float(v[j >> 4][j & 15]) * pw[max(d, 0)] : 0.f;
               };
 #pragma unroll
-              for (int i = 0; i < 8; ++i) {
-                w[i] = pack_bf16(val(v0[2 * i], 2 * i), val(v0[2 * i + 1], 2 * i + 1));
-                w[8 + i] = pack_bf16(val(v1[2 * i], 16 + 2 * i), val(v1[2 * i + 1], 17 + 2 * i));
-              }
+              for (int i = 0; i < 16; ++i) w[i] = pack_bf16(val(2 * i), val(2 * i + 1));
             }
           }
           tmem_st16(ta + 16 * gr, w);   // columns of A that this lane has read already
@@ -231,57 +250,120 @@ __global__ void __launch_bounds__(512, 1) lin_tc_kernel(const __grid_constant__ 
     }
   } else if (warp < 8) {
     // ------------------------------------------------------------------- O
-    if (!STATE_ONLY) {
-      const int t = tid - kRoleThreads;
-      const int p = rev ? C - 1 - t : t;
-      const float scale = a.scale, hd = a.scale * expf(g * (p + 1));
-      const CUtensorMap* mo = &maps.m[prm.mi[pi].out];
-      uint8_t* row = smem + K::S_OUT + t * 128;
-      for (int c = 0; c < n; ++c) {
-        const bool ok = warp_wait(kOFull, c);
-        tc_fence_after();
-        const uint32_t to = tmem + (static_cast<uint32_t>(warp - 4) << 21);
-        uint32_t w[32];
+    const int u = tid - kRoleThreads;
+    // w z of chunk c in two bf16 parts, at z's own offsets (row = token)
+    auto weigh = [&](int c) -> bool {
+      const int s = c % NB;
+      const int L = min(C, a.N - chunk_at(c) * C);
+      uint8_t* zw = smem + K::S_ZW + (c % K::NZ) * 2 * kBox;
+      if (c >= K::NZ && !warp_wait(kZFree + c % K::NZ, c / K::NZ - 1)) return false;   // G4 has read the buffer
+      if (!warp_wait(kFull + s, c / NB)) return false;
+      uint32_t top = 0u;
+#pragma unroll 1
+      for (int it = 0; it < 8; it += 2) {
+        uint4 z[2];
+        float w[2];
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          if (!ok) break;
-          uint32_t v1[16], v2[16];
-          tmem_ld16(to + kTO1 + 16 * q, v1);
-          tmem_ld16(to + kTO2 + 16 * q, v2);
-          tmem_ld_wait16(v1);
-          tmem_ld_wait16(v2);
-#pragma unroll
-          for (int i = 0; i < 8; ++i)
-            w[8 * q + i] = pack_bf16(fmaf(hd, __uint_as_float(v1[2 * i]), scale * __uint_as_float(v2[2 * i])),
-                                     fmaf(hd, __uint_as_float(v1[2 * i + 1]), scale * __uint_as_float(v2[2 * i + 1])));
+        for (int k = 0; k < 2; ++k) {
+          const int t = 16 * (it + k) + (u >> 3);
+          z[k] = *reinterpret_cast<const uint4*>(smem + sZ(s) + ((it + k) * kRoleThreads + u) * 16);
+          w[k] = t < L ? pw[rev ? t : L - 1 - t] : 0.f;
         }
-        const int from = *reinterpret_cast<volatile int*>(bad + (c & 1));
-        if (p >= from)
 #pragma unroll
-          for (int i = 0; i < 32; ++i) w[i] = 0x7fc07fc0u;   // NaN
-        tc_fence_before();
-        if (t == 0) bulk_wait_read_0();                      // the last store has left the staging tile
-        if (named_sync_or(1, kRoleThreads, !ok)) break;      // one outcome for the role
-        if (t == 0 && from < C) bad[c & 1] = C;
-        if (lane == 0) mbar_arrive(bars + kOFree);
+        for (int k = 0; k < 2; ++k) {
+          const uint32_t off = ((it + k) * kRoleThreads + u) * 16;
+          const uint32_t zz[4] = {z[k].x, z[k].y, z[k].z, z[k].w};
+          uint32_t hi[4], lo[4];
 #pragma unroll
-        for (int j = 0; j < 8; ++j)
-          *reinterpret_cast<uint4*>(row + ((j ^ (t & 7)) << 4)) = make_uint4(w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]);
-        fence_async_smem();
-        named_sync(1, kRoleThreads);
-        if (t == 0) {
-          tma_store_3d(mo, sbase + K::S_OUT, z0, chunk_at(c) * C, bh);
-          bulk_commit();
+          for (int e = 0; e < 4; ++e) {
+            top = __vmaxu2(top, zz[e] & 0x7fff7fffu);
+            const float v0 = bf_lo(zz[e]) * w[k], v1 = bf_hi(zz[e]) * w[k];
+            hi[e] = pack_bf16(v0, v1);
+            lo[e] = pack_bf16(v0 - bf_lo(hi[e]), v1 - bf_hi(hi[e]));
+          }
+          *reinterpret_cast<uint4*>(zw + off) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+          *reinterpret_cast<uint4*>(zw + kBox + off) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
         }
       }
-      if (t == 0) bulk_wait_all();
+      if (!STATE_ONLY && ((top & 0xffffu) >= 0x7f80u || (top >> 16) >= 0x7f80u)) {
+        // A NaN or infinity in z: 0 * z of the masked half would reach the
+        // tokens before it.  G2 reads a zero instead and the output warps write
+        // NaN from its token on.
+#pragma unroll 1
+        for (int i = 0; i < 32; ++i) {
+          const int it = i >> 2, t = 16 * it + (u >> 3);
+          uint32_t* z = reinterpret_cast<uint32_t*>(smem + sZ(s) + (it * kRoleThreads + u) * 16) + (i & 3);
+          uint32_t w = *z;
+          if ((w & 0x7f80u) == 0x7f80u) w &= 0xffff0000u;
+          if ((w & 0x7f800000u) == 0x7f800000u) w &= 0x0000ffffu;
+          if (w != *z) {
+            *z = w;
+            atomicMin(bad + (c & 1), rev ? C - 1 - t : t);
+          }
+        }
+      }
+      fence_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bars + kZReady + c % K::NZ);
+      return true;
+    };
+    const bool alive = weigh(0);
+    const int p = rev ? C - 1 - u : u;
+    const float hd = a.scale * expf(g * (p + 1));
+    const uint64_t scale2 = f2_pack(a.scale, a.scale), hd2 = f2_pack(hd, hd);
+    const CUtensorMap* mo = &maps.m[prm.mi[pi].out];
+    uint8_t* row = smem + K::S_OUT + u * 128;
+#pragma unroll 1
+    for (int c = 0; c < n; ++c) {
+      bool ok = alive && (c + 1 == n || weigh(c + 1));
+      if (STATE_ONLY) {
+        if (!ok) break;
+        continue;
+      }
+      ok = ok && warp_wait(kOFull, c);
+      const int from = *reinterpret_cast<volatile int*>(bad + (c & 1));
+      if (u == 0) bulk_wait_read_0();                      // the last store has left the staging tile
+      if (named_sync_or(1, kRoleThreads, !ok)) break;      // one outcome for the role
+      tc_fence_after();
+      if (u == 0 && from < C) bad[c & 1] = C;              // all have read it; weigh(c + 2) comes after the next barrier
+      const uint32_t to = tmem + (static_cast<uint32_t>(warp - 4) << 21);
+#pragma unroll 1
+      for (int q = 0; q < 4; ++q) {
+        uint32_t v1[16], v2[16], w[8];
+        tmem_ld16(to + kTO1 + 16 * q, v1);
+        tmem_ld16(to + kTO2 + 16 * q, v2);
+        tmem_ld_wait16(v1);
+        tmem_ld_wait16(v2);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          float lo, hi;
+          f2_unpack(f2_fma(hd2, f2_pack(__uint_as_float(v1[2 * i]), __uint_as_float(v1[2 * i + 1])),
+                           f2_mul(scale2, f2_pack(__uint_as_float(v2[2 * i]), __uint_as_float(v2[2 * i + 1])))), lo, hi);
+          w[i] = pack_bf16(lo, hi);
+        }
+        if (p >= from)
+#pragma unroll
+          for (int i = 0; i < 8; ++i) w[i] = 0x7fc07fc0u;   // NaN
+        *reinterpret_cast<uint4*>(row + (((2 * q) ^ (u & 7)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
+        *reinterpret_cast<uint4*>(row + (((2 * q + 1) ^ (u & 7)) << 4)) = make_uint4(w[4], w[5], w[6], w[7]);
+      }
+      tc_fence_before();
+      fence_async_smem();
+      named_sync(1, kRoleThreads);
+      if (u == 0) {
+        tma_store_3d(mo, sbase + K::S_OUT, z0, chunk_at(c) * C, bh);
+        bulk_commit();
+      }
+      if (lane == 0) mbar_arrive(bars + kOFree);
     }
+    if (u == 0) bulk_wait_all();
   } else if (warp < 12) {
     // ------------------------------------------------------------------- S
     const int u = tid - 2 * kRoleThreads;
     const bool holds = u < dx;   // thread u carries row u of S
     const long long per_state = static_cast<long long>(dx) * dz;
-    float S[64];
+    uint64_t S[32];              // its 64 columns in pairs
+    const float dec_full = expm1f(g * C);
     {
       const float* s0 = seg == 0 ? (pr.state_in ? pr.state_in + bh * per_state : nullptr)
                                  : STATE_ONLY ? nullptr : pr.seg + (static_cast<long long>(bh) * (a.nseg - 1) + seg - 1) * per_state;
@@ -289,94 +371,48 @@ __global__ void __launch_bounds__(512, 1) lin_tc_kernel(const __grid_constant__ 
       for (int i = 0; i < 16; ++i) {
         float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
         if (s0 && holds) v = *reinterpret_cast<const float4*>(s0 + static_cast<long long>(u) * dz + z0 + 4 * i);
-        S[4 * i] = v.x, S[4 * i + 1] = v.y, S[4 * i + 2] = v.z, S[4 * i + 3] = v.w;
+        S[2 * i] = f2_pack(v.x, v.y), S[2 * i + 1] = f2_pack(v.z, v.w);
       }
     }
-    auto write_operand = [&]() {
-      if (holds)
+    auto write_operand = [&]() {   // and K has been read: the next G4 may overwrite it
+      if (!STATE_ONLY && holds)
 #pragma unroll
         for (int j = 0; j < 8; ++j)
           *reinterpret_cast<uint4*>(smem + K::S_SB + u * 128 + ((j ^ (u & 7)) << 4)) =
-              make_uint4(pack_bf16(S[8 * j], S[8 * j + 1]), pack_bf16(S[8 * j + 2], S[8 * j + 3]),
-                         pack_bf16(S[8 * j + 4], S[8 * j + 5]), pack_bf16(S[8 * j + 6], S[8 * j + 7]));
+              make_uint4(pack2(S[4 * j]), pack2(S[4 * j + 1]), pack2(S[4 * j + 2]), pack2(S[4 * j + 3]));
       fence_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(bars + kSReady);
     };
-    if (!STATE_ONLY) write_operand();
+    write_operand();
 
-    // weights of this thread's rows (16 it + u / 8) of a whole chunk
-    float wf[8];
-#pragma unroll
-    for (int it = 0; it < 8; ++it) {
-      const int t = 16 * it + (u >> 3);
-      wf[it] = expf(g * (C - 1 - (rev ? C - 1 - t : t)));
-    }
     for (int c = 0; c < n; ++c) {
-      const int s = c % NB;
       const int L = min(C, a.N - chunk_at(c) * C);
-      const int Lw = rev ? C : L;
-      // w z, in two bf16 parts, at z's own offsets (row = token)
-      if (!warp_wait(kFull + s, c / NB)) break;
-      uint32_t top = 0u;
-#pragma unroll
-      for (int it = 0; it < 8; ++it) {
-        const uint32_t off = (it * kRoleThreads + u) * 16;
-        const int t = 16 * it + (u >> 3);
-        const uint4 z = *reinterpret_cast<const uint4*>(smem + sZ(s) + off);
-        const float w = Lw == C ? wf[it] : t < L ? expf(g * (L - 1 - t)) : 0.f;
-        const uint32_t zz[4] = {z.x, z.y, z.z, z.w};
-        uint32_t hi[4], lo[4];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          top = __vmaxu2(top, zz[e] & 0x7fff7fffu);
-          const float v0 = bf_lo(zz[e]) * w, v1 = bf_hi(zz[e]) * w;
-          hi[e] = pack_bf16(v0, v1);
-          lo[e] = pack_bf16(v0 - bf_lo(hi[e]), v1 - bf_hi(hi[e]));
-        }
-        *reinterpret_cast<uint4*>(smem + K::S_ZW + off) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-        *reinterpret_cast<uint4*>(smem + K::S_ZW + kBox + off) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
-      }
-      if (!STATE_ONLY && ((top & 0xffffu) >= 0x7f80u || (top >> 16) >= 0x7f80u)) {
-        // A NaN or infinity in z: 0 * z of the masked half would reach the
-        // tokens before it.  G2 reads a zero instead and the output warps write
-        // NaN from its token on.
-        for (int it = 0; it < 8; ++it) {
-          uint32_t* z = reinterpret_cast<uint32_t*>(smem + sZ(s) + (it * kRoleThreads + u) * 16);
-          const int t = 16 * it + (u >> 3);
-          for (int e = 0; e < 4; ++e) {
-            uint32_t w = z[e];
-            if ((w & 0x7f80u) == 0x7f80u) w &= 0xffff0000u;
-            if ((w & 0x7f800000u) == 0x7f800000u) w &= 0x0000ffffu;
-            if (w != z[e]) {
-              z[e] = w;
-              atomicMin(bad + (c & 1), rev ? C - 1 - t : t);
-            }
-          }
-        }
-      }
-      fence_async_smem();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(bars + kZReady);
-
-      // S <- lambda^L S + K
-      const float dec = expm1f(g * Lw);
+      const float dec = L == C || rev ? dec_full : expm1f(g * L);
+      const uint64_t dec2 = f2_pack(dec, dec);
       if (!warp_wait(kKFull, c)) break;
       tc_fence_after();
       if (32 * (warp - 8) < dx) {
         const uint32_t tk = tmem + (static_cast<uint32_t>(warp - 8) << 21) + kTK;
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
-          uint32_t v[16];
+          uint32_t v[16], w[16];
           tmem_ld16(tk + 16 * q, v);
+          tmem_ld16(tk + 64 + 16 * q, w);
           tmem_ld_wait16(v);
+          tmem_ld_wait16(w);
 #pragma unroll
-          for (int i = 0; i < 16; ++i) S[16 * q + i] = fmaf(dec, S[16 * q + i], S[16 * q + i]) + __uint_as_float(v[i]);
+          for (int i = 0; i < 8; ++i) {
+            const uint64_t hi = f2_pack(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1]));
+            const uint64_t lo = f2_pack(__uint_as_float(w[2 * i]), __uint_as_float(w[2 * i + 1]));
+            uint64_t& S2 = S[8 * q + i];
+            S2 = f2_add(f2_fma(dec2, S2, S2), f2_add(hi, lo));
+          }
         }
       }
       tc_fence_before();
-      if (!STATE_ONLY && c + 1 < n) {
-        if (!warp_wait(kSFree, c)) break;   // G3 has read the old operand
+      if (c + 1 < n) {
+        if (!STATE_ONLY && !warp_wait(kSFree, c)) break;   // G3 has read the old operand
         write_operand();
       }
     }
@@ -384,12 +420,15 @@ __global__ void __launch_bounds__(512, 1) lin_tc_kernel(const __grid_constant__ 
                             : (pr.state_out && seg == a.nseg - 1) ? pr.state_out + bh * per_state : nullptr;
     if (dst && holds)
 #pragma unroll
-      for (int i = 0; i < 16; ++i)
-        *reinterpret_cast<float4*>(dst + static_cast<long long>(u) * dz + z0 + 4 * i) =
-            make_float4(S[4 * i], S[4 * i + 1], S[4 * i + 2], S[4 * i + 3]);
+      for (int i = 0; i < 16; ++i) {
+        float4 v;
+        f2_unpack(S[2 * i], v.x, v.y);
+        f2_unpack(S[2 * i + 1], v.z, v.w);
+        *reinterpret_cast<float4*>(dst + static_cast<long long>(u) * dz + z0 + 4 * i) = v;
+      }
   } else if (warp == 12) {
     // ---------------------------------------------------------------- loads
-    if (lane == 0) {
+    if (elect_one()) {
       const CUtensorMap *mx = &maps.m[prm.mi[pi].x], *my = &maps.m[prm.mi[pi].y], *mz = &maps.m[prm.mi[pi].z];
       int issued = 0;
       for (int c = 0; c < n; ++c) {
@@ -410,37 +449,50 @@ __global__ void __launch_bounds__(512, 1) lin_tc_kernel(const __grid_constant__ 
     __syncwarp();
   } else {
     // ------------------------------------------------------------------ MMA
-    if (lane == 0) {
+    if (elect_one()) {
       bool issued = false;
-      auto kstep = [](int kk) { return static_cast<uint32_t>((kk >> 2) * kBox + (kk & 3) * 32); };   // K-major, 64-column boxes
+      // descriptors of a stage's tiles: K-major for G1 and G3's X, MN-major
+      // (the token index contracted) for G2 and G4
+      auto kmajor = [&](int off) { return smem_desc_sw128(sbase + off, 16, kAtom); };
+      auto mnmajor = [&](int off) { return smem_desc_sw128(sbase + off, kBox, kAtom); };
+      constexpr uint64_t kTok = (2 * kAtom) >> 4;   // 16 tokens (or rows of S) further
       auto g1 = [&](int c) {
         const int s = c % NB;
-        for (int kk = 0; kk < nbx * 4; ++kk)
-          mma_f16(tmem + kTA + 128 * (c & 1), smem_desc_sw128(sbase + sX(s) + kstep(kk), 16, kAtom),
-                  smem_desc_sw128(sbase + sY(s) + kstep(kk), 16, kAtom), idesc_bf16(128, 128, 0, 0), kk > 0);
+        const uint64_t x = kmajor(sX(s)), y = kmajor(sY(s));
+#pragma unroll 1
+        for (int b = 0; b < nbx; ++b)
+#pragma unroll
+          for (int kk = 0; kk < 4; ++kk) {
+            const uint64_t step = (b * kBox + kk * 32) >> 4;
+            mma_f16(tmem + kTA + 128 * (c & 1), x + step, y + step, idesc_bf16(128, 128, 0, 0), b + kk > 0);
+          }
         mma_commit(bars + kAFull + (c & 1));
       };
       auto g3 = [&](int c) {
-        const int s = c % NB;
-        for (int kk = 0; kk < nbx * 4; ++kk)
-          mma_f16(tmem + kTO1, smem_desc_sw128(sbase + sX(s) + kstep(kk), 16, kAtom),
-                  smem_desc_sw128(sbase + K::S_SB + kk * 2 * kAtom, kBox, kAtom), idesc_bf16(128, 64, 0, 1), kk > 0);
+        const uint64_t x = kmajor(sX(c % NB)), sb = mnmajor(K::S_SB);
+#pragma unroll 1
+        for (int b = 0; b < nbx; ++b)
+#pragma unroll
+          for (int kk = 0; kk < 4; ++kk)
+            mma_f16(tmem + kTO1, x + ((b * kBox + kk * 32) >> 4), sb + (4 * b + kk) * kTok, idesc_bf16(128, 64, 0, 1), b + kk > 0);
         mma_commit(bars + kSFree);
       };
       auto g4 = [&](int c) {
         // rows of K past dx (a second 64-row block when dx = 64) are taken from
         // the next tile of the stage and never read
-        const int s = c % NB;
-        for (int kk = 0; kk < 16; ++kk)
-          mma_f16(tmem + kTK, smem_desc_sw128(sbase + sY(s) + (kk & 7) * 2 * kAtom, kBox, kAtom),
-                  smem_desc_sw128(sbase + K::S_ZW + kk * 2 * kAtom, kBox, kAtom), idesc_bf16(128, 64, 1, 1), kk > 0);
+        const int zb = c % K::NZ;
+        const uint64_t y = mnmajor(sY(c % NB)), zw = mnmajor(K::S_ZW + zb * 2 * kBox);
+#pragma unroll 4
+        for (int kk = 0; kk < 8; ++kk)
+          mma_f16(tmem + kTK, y + kk * kTok, zw + kk * kTok, idesc_bf16(128, 128, 1, 1), kk > 0);
         mma_commit(bars + kKFull);
+        mma_commit(bars + kZFree + zb);
       };
       auto g2 = [&](int c) {
-        const int s = c % NB;
+        const uint64_t z = mnmajor(sZ(c % NB));
+#pragma unroll 4
         for (int kk = 0; kk < 8; ++kk)
-          mma_f16_ts(tmem + kTO2, tmem + kTA + 128 * (c & 1) + 8 * kk,
-                     smem_desc_sw128(sbase + sZ(s) + kk * 2 * kAtom, kBox, kAtom), idesc_bf16(128, 64, 0, 1), kk > 0);
+          mma_f16_ts(tmem + kTO2, tmem + kTA + 128 * (c & 1) + 8 * kk, z + kk * kTok, idesc_bf16(128, 64, 0, 1), kk > 0);
         mma_commit(bars + kOFull);
       };
       bool ok = true;
@@ -452,13 +504,10 @@ __global__ void __launch_bounds__(512, 1) lin_tc_kernel(const __grid_constant__ 
           issued = true;
         }
       }
+#pragma unroll 1
       for (int c = 0; ok && c < n; ++c) {
-        if (!STATE_ONLY) {
-          if (!wait(kSReady, c) || (c > 0 && !wait(kOFree, c - 1))) break;
-          tc_fence_after();
-          g3(c);
-        }
-        if (!wait(kFull + c % NB, c / NB) || !wait(kZReady, c)) break;
+        // K is free once the state has taken it (which also made S's operand)
+        if (!wait(kSReady, c) || !wait(kFull + c % NB, c / NB) || !wait(kZReady + c % K::NZ, c / K::NZ)) break;
         tc_fence_after();
         g4(c);
         issued = true;
@@ -468,6 +517,9 @@ __global__ void __launch_bounds__(512, 1) lin_tc_kernel(const __grid_constant__ 
             tc_fence_after();
             g1(c + 1);
           }
+          if (c > 0 && !wait(kOFree, c - 1)) break;
+          tc_fence_after();
+          g3(c);
           if (!wait(kPReady + (c & 1), c >> 1)) break;
           tc_fence_after();
           g2(c);
