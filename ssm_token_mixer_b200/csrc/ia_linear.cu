@@ -15,6 +15,7 @@
 #include <algorithm>
 #include <cmath>
 #include <cstdint>
+#include <cstdlib>
 
 #include "ia_device.cuh"
 #include "ia_internal.h"
@@ -342,6 +343,14 @@ LinPlan lin_plan(const ia_linear_shape_t& s, bool train) {
   const long long streams = train ? bh * (2LL * lin_zblocks(s.d_v) + 2LL * lin_zblocks(s.d_k)) : bh * lin_zblocks(s.d_v);
   const long long slots = static_cast<long long>(num_sms()) * (p.tc ? 1 : std::max(s.d_k, s.d_v) <= 64 ? 2 : 1);
   const double f = p.tc ? 0.6 : 0.45, launches = p.tc ? 5.0 : 2.0;
+  if (const char* env = std::getenv("IA_LINEAR_SEGMENTS")) {   // forced count (tuning and tests)
+    const int want = std::atoi(env);
+    if (want >= 1) {
+      p.cps = (p.nch + std::min(want, p.nch) - 1) / std::min(want, p.nch);
+      p.nseg = (p.nch + p.cps - 1) / p.cps;
+      return p;
+    }
+  }
   double best = 0.0;
   p.nseg = 1;
   p.cps = p.nch;

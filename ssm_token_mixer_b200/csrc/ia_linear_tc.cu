@@ -62,11 +62,12 @@ constexpr uint32_t kTA = 0, kTO1 = 256, kTO2 = 320, kTK = 384;
 
 template <int MAXDX>
 struct Cfg {
-  static constexpr int NB = 2;                          // stages of X, Y, Z
-  static constexpr int TX = MAXDX / 64 * kBox;
-  static constexpr int STAGE = 2 * TX + kBox;
+  static constexpr int NS = 2;                          // stages of X and Y
+  static constexpr int NT = MAXDX == 64 ? 3 : 2;        // stages of Z, needed first and released last
   static constexpr int NZ = MAXDX == 64 ? 2 : 1;        // buffers of w z
-  static constexpr int S_ZW = NB * STAGE;               // each: hi, lo
+  static constexpr int TX = MAXDX / 64 * kBox;
+  static constexpr int S_Z = NS * 2 * TX;
+  static constexpr int S_ZW = S_Z + NT * kBox;          // each: hi, lo
   static constexpr int S_SB = S_ZW + NZ * 2 * kBox;     // [dx][64] bf16, 128-byte swizzled
   static constexpr int S_OUT = S_SB + MAXDX * 128;
   static constexpr int S_BAR = S_OUT + kBox;
@@ -74,7 +75,10 @@ struct Cfg {
   static constexpr int SMEM = S_POW + C * 4 + 1024;     // + alignment of the base
 };
 
-enum Bar { kFull = 0, kFree = 3, kAFull = 6, kPReady = 8, kZReady = 10, kZFree = 12, kSReady = 14, kSFree, kKFull, kOFull, kOFree, kDrain, kBars };
+enum Bar {
+  kFullXY = 0, kFullZ = 2, kFreeX = 5, kFreeY = 7, kFreeZ = 9, kAFull = 12, kPReady = 14, kZReady = 16, kZFree = 18,
+  kSReady = 20, kSFree, kKFull, kOFull, kOFree, kDrain, kBars
+};
 
 struct Maps {
   CUtensorMap m[8];    // q, k, v, dO and o, dq, dk, dv (a prefill: q, k, v and o at 4)
@@ -123,7 +127,7 @@ template <int MAXDX, bool STATE_ONLY>
 __global__ void __launch_bounds__(512, 1) lin_tc_kernel(const __grid_constant__ TcParams prm,
                                                         const __grid_constant__ Maps maps) {
   using K = Cfg<MAXDX>;
-  constexpr int NB = K::NB;
+  constexpr int NS = K::NS, NT = K::NT;
   extern __shared__ uint8_t raw[];
   uint8_t* smem = raw + ((1024u - (smem_u32(raw) & 1023u)) & 1023u);
   const LinArgs& a = prm.a;
@@ -152,32 +156,20 @@ __global__ void __launch_bounds__(512, 1) lin_tc_kernel(const __grid_constant__ 
   int* bad = reinterpret_cast<int*>(smem + K::S_BAR + 8 * kBars + 8);   // [2]
   static_assert(8 * kBars + 16 <= 256, "barriers and flags fit their slot");
   const uint32_t sbase = smem_u32(smem);
-  auto sX = [&](int s) { return s * K::STAGE; };
-  auto sY = [&](int s) { return s * K::STAGE + K::TX; };
-  auto sZ = [&](int s) { return s * K::STAGE + 2 * K::TX; };
+  auto sX = [&](int c) { return (c % NS) * 2 * K::TX; };
+  auto sY = [&](int c) { return (c % NS) * 2 * K::TX + K::TX; };
+  auto sZ = [&](int c) { return K::S_Z + (c % NT) * kBox; };
 
   if (warp == 0) {
     tmem_alloc(tmem_holder, 512);
     tmem_relinquish();
   }
   if (tid == 32) {
-    for (int i = 0; i < 3; ++i) {
-      mbar_init(bars + kFull + i, 1);
-      mbar_init(bars + kFree + i, 1);
+    for (int i = 0; i < kBars; ++i) {   // arrivals: one, or one per warp of the role that fills the buffer
+      const bool warps = i == kPReady || i == kPReady + 1 || i == kZReady || i == kZReady + 1 || i == kSReady || i == kOFree;
+      mbar_init(bars + i, warps ? 4 : 1);
     }
-    for (int i = 0; i < 2; ++i) {
-      mbar_init(bars + kZReady + i, 4);
-      mbar_init(bars + kZFree + i, 1);
-      mbar_init(bars + kAFull + i, 1);
-      mbar_init(bars + kPReady + i, 4);
-      bad[i] = C;
-    }
-    mbar_init(bars + kSReady, 4);
-    mbar_init(bars + kSFree, 1);
-    mbar_init(bars + kKFull, 1);
-    mbar_init(bars + kOFull, 1);
-    mbar_init(bars + kOFree, 4);
-    mbar_init(bars + kDrain, 1);
+    bad[0] = bad[1] = C;
     *abort_flag = 0;
     fence_barrier_init();
   }
@@ -253,52 +245,49 @@ __global__ void __launch_bounds__(512, 1) lin_tc_kernel(const __grid_constant__ 
     const int u = tid - kRoleThreads;
     // w z of chunk c in two bf16 parts, at z's own offsets (row = token)
     auto weigh = [&](int c) -> bool {
-      const int s = c % NB;
       const int L = min(C, a.N - chunk_at(c) * C);
       uint8_t* zw = smem + K::S_ZW + (c % K::NZ) * 2 * kBox;
+      const uint8_t* zs = smem + sZ(c);
       if (c >= K::NZ && !warp_wait(kZFree + c % K::NZ, c / K::NZ - 1)) return false;   // G4 has read the buffer
-      if (!warp_wait(kFull + s, c / NB)) return false;
-      uint32_t top = 0u;
+      if (!warp_wait(kFullZ + c % NT, c / NT)) return false;
+      const __nv_bfloat162 zero = __float2bfloat162_rn(0.f);
+      __nv_bfloat162 probe = zero;   // 0 * z: NaN if any z is not finite
+      uint32_t off = u * 16;
+      int t = u >> 3;
+      uint4 zn = *reinterpret_cast<const uint4*>(zs + off);
 #pragma unroll 1
-      for (int it = 0; it < 8; it += 2) {
-        uint4 z[2];
-        float w[2];
+      for (int i = 0; i < 8; ++i) {
+        const uint32_t zz[4] = {zn.x, zn.y, zn.z, zn.w};
+        if (i < 7) zn = *reinterpret_cast<const uint4*>(zs + off + 16 * kRoleThreads);
+        const float wt = t < L ? pw[rev ? t : L - 1 - t] : 0.f;
+        const uint64_t w2 = f2_pack(wt, wt), minus = f2_pack(-1.f, -1.f);
+        uint32_t hi[4], lo[4];
 #pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          const int t = 16 * (it + k) + (u >> 3);
-          z[k] = *reinterpret_cast<const uint4*>(smem + sZ(s) + ((it + k) * kRoleThreads + u) * 16);
-          w[k] = t < L ? pw[rev ? t : L - 1 - t] : 0.f;
+        for (int e = 0; e < 4; ++e) {
+          probe = __hfma2(*reinterpret_cast<const __nv_bfloat162*>(&zz[e]), zero, probe);
+          const uint64_t v = f2_mul(f2_pack(bf_lo(zz[e]), bf_hi(zz[e])), w2);
+          hi[e] = pack2(v);
+          lo[e] = pack2(f2_fma(f2_pack(bf_lo(hi[e]), bf_hi(hi[e])), minus, v));
         }
-#pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          const uint32_t off = ((it + k) * kRoleThreads + u) * 16;
-          const uint32_t zz[4] = {z[k].x, z[k].y, z[k].z, z[k].w};
-          uint32_t hi[4], lo[4];
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            top = __vmaxu2(top, zz[e] & 0x7fff7fffu);
-            const float v0 = bf_lo(zz[e]) * w[k], v1 = bf_hi(zz[e]) * w[k];
-            hi[e] = pack_bf16(v0, v1);
-            lo[e] = pack_bf16(v0 - bf_lo(hi[e]), v1 - bf_hi(hi[e]));
-          }
-          *reinterpret_cast<uint4*>(zw + off) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-          *reinterpret_cast<uint4*>(zw + kBox + off) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
-        }
+        *reinterpret_cast<uint4*>(zw + off) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+        *reinterpret_cast<uint4*>(zw + kBox + off) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+        off += 16 * kRoleThreads;
+        t += 16;
       }
-      if (!STATE_ONLY && ((top & 0xffffu) >= 0x7f80u || (top >> 16) >= 0x7f80u)) {
+      if (!STATE_ONLY && !__hbeq2(probe, zero)) {
         // A NaN or infinity in z: 0 * z of the masked half would reach the
         // tokens before it.  G2 reads a zero instead and the output warps write
         // NaN from its token on.
 #pragma unroll 1
         for (int i = 0; i < 32; ++i) {
-          const int it = i >> 2, t = 16 * it + (u >> 3);
-          uint32_t* z = reinterpret_cast<uint32_t*>(smem + sZ(s) + (it * kRoleThreads + u) * 16) + (i & 3);
-          uint32_t w = *z;
-          if ((w & 0x7f80u) == 0x7f80u) w &= 0xffff0000u;
-          if ((w & 0x7f800000u) == 0x7f800000u) w &= 0x0000ffffu;
-          if (w != *z) {
-            *z = w;
-            atomicMin(bad + (c & 1), rev ? C - 1 - t : t);
+          const int it = i >> 2, tt = 16 * it + (u >> 3);
+          uint32_t* z = reinterpret_cast<uint32_t*>(smem + sZ(c) + (it * kRoleThreads + u) * 16) + (i & 3);
+          uint32_t x = *z;
+          if ((x & 0x7f80u) == 0x7f80u) x &= 0xffff0000u;
+          if ((x & 0x7f800000u) == 0x7f800000u) x &= 0x0000ffffu;
+          if (x != *z) {
+            *z = x;
+            atomicMin(bad + (c & 1), rev ? C - 1 - tt : tt);
           }
         }
       }
@@ -307,20 +296,21 @@ __global__ void __launch_bounds__(512, 1) lin_tc_kernel(const __grid_constant__ 
       if (lane == 0) mbar_arrive(bars + kZReady + c % K::NZ);
       return true;
     };
-    const bool alive = weigh(0);
+    bool alive = true;
     const int p = rev ? C - 1 - u : u;
     const float hd = a.scale * expf(g * (p + 1));
     const uint64_t scale2 = f2_pack(a.scale, a.scale), hd2 = f2_pack(hd, hd);
     const CUtensorMap* mo = &maps.m[prm.mi[pi].out];
     uint8_t* row = smem + K::S_OUT + u * 128;
 #pragma unroll 1
-    for (int c = 0; c < n; ++c) {
-      bool ok = alive && (c + 1 == n || weigh(c + 1));
+    for (int c = -1; c < n; ++c) {
+      if (c + 1 < n) alive = alive && weigh(c + 1);
+      if (c < 0) continue;           // the first chunk is weighed before the first output
       if (STATE_ONLY) {
-        if (!ok) break;
+        if (!alive) break;
         continue;
       }
-      ok = ok && warp_wait(kOFull, c);
+      const bool ok = alive && warp_wait(kOFull, c);
       const int from = *reinterpret_cast<volatile int*>(bad + (c & 1));
       if (u == 0) bulk_wait_read_0();                      // the last store has left the staging tile
       if (named_sync_or(1, kRoleThreads, !ok)) break;      // one outcome for the role
@@ -430,21 +420,33 @@ __global__ void __launch_bounds__(512, 1) lin_tc_kernel(const __grid_constant__ 
     // ---------------------------------------------------------------- loads
     if (elect_one()) {
       const CUtensorMap *mx = &maps.m[prm.mi[pi].x], *my = &maps.m[prm.mi[pi].y], *mz = &maps.m[prm.mi[pi].z];
-      int issued = 0;
+      int issued_z = 0, issued_y = 0, issued_x = 0;
+#pragma unroll 1
       for (int c = 0; c < n; ++c) {
-        const int s = c % NB;
-        if (c >= NB && !wait(kFree + s, c / NB - 1)) break;
         const int t0 = chunk_at(c) * C;
-        mbar_arrive_expect_tx(bars + kFull + s, ((STATE_ONLY ? 1 : 2) * nbx + 1) * kBox);
-        for (int x = 0; x < nbx; ++x) {
-          if (!STATE_ONLY) tma_load_3d(sbase + sX(s) + x * kBox, mx, 64 * x, t0, bh, bars + kFull + s);
-          tma_load_3d(sbase + sY(s) + x * kBox, my, 64 * x, t0, bh, bars + kFull + s);
+        if (c >= NT && !wait(kFreeZ + c % NT, c / NT - 1)) break;
+        mbar_arrive_expect_tx(bars + kFullZ + c % NT, kBox);
+        tma_load_3d(sbase + sZ(c), mz, z0, t0, bh, bars + kFullZ + c % NT);
+        issued_z = c + 1;
+        uint64_t* full = bars + kFullXY + c % NS;
+        if (c >= NS && !wait(kFreeY + c % NS, c / NS - 1)) break;
+        mbar_arrive_expect_tx(full, (STATE_ONLY ? 1 : 2) * nbx * kBox);
+        for (int x = 0; x < nbx; ++x) tma_load_3d(sbase + sY(c) + x * kBox, my, 64 * x, t0, bh, full);
+        issued_y = c + 1;
+        if (!STATE_ONLY) {
+          if (c >= NS && !wait(kFreeX + c % NS, c / NS - 1)) break;
+          for (int x = 0; x < nbx; ++x) tma_load_3d(sbase + sX(c) + x * kBox, mx, 64 * x, t0, bh, full);
         }
-        tma_load_3d(sbase + sZ(s), mz, z0, t0, bh, bars + kFull + s);
-        issued = c + 1;
+        issued_x = c + 1;
       }
       // no copy lands after the block exits
-      for (int c = max(0, issued - NB); c < issued; ++c) mbar_wait(bars + kFull + c % NB, (c / NB) & 1, a.err);
+      for (int c = max(0, issued_z - NT); c < issued_z; ++c) mbar_wait(bars + kFullZ + c % NT, (c / NT) & 1, a.err);
+      for (int c = max(0, issued_y - NS); c < issued_x; ++c) mbar_wait(bars + kFullXY + c % NS, (c / NS) & 1, a.err);
+      if (issued_x < issued_y) {
+        // aborted between Y and X of a chunk: its barrier cannot complete; its Y gets a millisecond to land
+        const unsigned long long t = global_ns();
+        while (global_ns() - t < 1000000ull) __nanosleep(1000);
+      }
     }
     __syncwarp();
   } else {
@@ -457,8 +459,7 @@ __global__ void __launch_bounds__(512, 1) lin_tc_kernel(const __grid_constant__ 
       auto mnmajor = [&](int off) { return smem_desc_sw128(sbase + off, kBox, kAtom); };
       constexpr uint64_t kTok = (2 * kAtom) >> 4;   // 16 tokens (or rows of S) further
       auto g1 = [&](int c) {
-        const int s = c % NB;
-        const uint64_t x = kmajor(sX(s)), y = kmajor(sY(s));
+        const uint64_t x = kmajor(sX(c)), y = kmajor(sY(c));
 #pragma unroll 1
         for (int b = 0; b < nbx; ++b)
 #pragma unroll
@@ -469,35 +470,39 @@ __global__ void __launch_bounds__(512, 1) lin_tc_kernel(const __grid_constant__ 
         mma_commit(bars + kAFull + (c & 1));
       };
       auto g3 = [&](int c) {
-        const uint64_t x = kmajor(sX(c % NB)), sb = mnmajor(K::S_SB);
+        const uint64_t x = kmajor(sX(c)), sb = mnmajor(K::S_SB);
 #pragma unroll 1
         for (int b = 0; b < nbx; ++b)
 #pragma unroll
           for (int kk = 0; kk < 4; ++kk)
             mma_f16(tmem + kTO1, x + ((b * kBox + kk * 32) >> 4), sb + (4 * b + kk) * kTok, idesc_bf16(128, 64, 0, 1), b + kk > 0);
         mma_commit(bars + kSFree);
+        mma_commit(bars + kFreeX + c % NS);
       };
       auto g4 = [&](int c) {
         // rows of K past dx (a second 64-row block when dx = 64) are taken from
         // the next tile of the stage and never read
         const int zb = c % K::NZ;
-        const uint64_t y = mnmajor(sY(c % NB)), zw = mnmajor(K::S_ZW + zb * 2 * kBox);
+        const uint64_t y = mnmajor(sY(c)), zw = mnmajor(K::S_ZW + zb * 2 * kBox);
 #pragma unroll 4
         for (int kk = 0; kk < 8; ++kk)
           mma_f16(tmem + kTK, y + kk * kTok, zw + kk * kTok, idesc_bf16(128, 128, 1, 1), kk > 0);
         mma_commit(bars + kKFull);
         mma_commit(bars + kZFree + zb);
+        mma_commit(bars + kFreeY + c % NS);   // G1 of this chunk came before
+        if (STATE_ONLY) mma_commit(bars + kFreeZ + c % NT);
       };
       auto g2 = [&](int c) {
-        const uint64_t z = mnmajor(sZ(c % NB));
+        const uint64_t z = mnmajor(sZ(c));
 #pragma unroll 4
         for (int kk = 0; kk < 8; ++kk)
           mma_f16_ts(tmem + kTO2, tmem + kTA + 128 * (c & 1) + 8 * kk, z + kk * kTok, idesc_bf16(128, 64, 0, 1), kk > 0);
         mma_commit(bars + kOFull);
+        mma_commit(bars + kFreeZ + c % NT);
       };
       bool ok = true;
       if (!STATE_ONLY) {
-        ok = wait(kFull, 0);
+        ok = wait(kFullXY, 0);
         if (ok) {
           tc_fence_after();
           g1(0);
@@ -507,13 +512,13 @@ __global__ void __launch_bounds__(512, 1) lin_tc_kernel(const __grid_constant__ 
 #pragma unroll 1
       for (int c = 0; ok && c < n; ++c) {
         // K is free once the state has taken it (which also made S's operand)
-        if (!wait(kSReady, c) || !wait(kFull + c % NB, c / NB) || !wait(kZReady + c % K::NZ, c / K::NZ)) break;
+        if (!wait(kSReady, c) || !wait(kFullXY + c % NS, c / NS) || !wait(kZReady + c % K::NZ, c / K::NZ)) break;
         tc_fence_after();
         g4(c);
         issued = true;
         if (!STATE_ONLY) {
           if (c + 1 < n) {
-            if (!wait(kFull + (c + 1) % NB, (c + 1) / NB)) break;
+            if (!wait(kFullXY + (c + 1) % NS, (c + 1) / NS)) break;
             tc_fence_after();
             g1(c + 1);
           }
@@ -524,7 +529,6 @@ __global__ void __launch_bounds__(512, 1) lin_tc_kernel(const __grid_constant__ 
           tc_fence_after();
           g2(c);
         }
-        mma_commit(bars + kFree + c % NB);
       }
       if (issued) {   // every product is done before TMEM and shared memory go
         mma_commit(bars + kDrain);
