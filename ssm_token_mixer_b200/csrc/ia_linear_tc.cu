@@ -27,7 +27,7 @@
 //   warps 4-7   O: w z of the next chunk for G4; then O1, O2 from TMEM, out
 //               through shared memory and a TMA store
 //   warps 8-11  S: K from TMEM, S in registers, S in bf16 to shared memory for
-//               the next chunk's G3
+//               the next chunk's G3; half of w z when there are two buffers
 //   warp 12     TMA loads        warp 13   issues G1-G4
 // Per chunk G4, G1 of the next chunk, G3 and G2 are issued in this order, so
 // that P and the state work while the products of the other roles run.  The
@@ -65,6 +65,11 @@ struct Cfg {
   static constexpr int NS = 2;                          // stages of X and Y
   static constexpr int NT = MAXDX == 64 ? 3 : 2;        // stages of Z, needed first and released last
   static constexpr int NZ = MAXDX == 64 ? 2 : 1;        // buffers of w z
+  // Who weighs z.  With two buffers the state's warps take half of it off the
+  // output warps, which carry the longest chain (training step of B8 H16 N2048,
+  // d = 64: 126 us without, 118 us with); with one buffer it would hold up the
+  // state instead (d = 128: 140 us without, 150 us with).
+  static constexpr bool kSplit = NZ == 2;
   static constexpr int TX = MAXDX / 64 * kBox;
   static constexpr int S_Z = NS * 2 * TX;
   static constexpr int S_ZW = S_Z + NT * kBox;          // each: hi, lo
@@ -153,8 +158,8 @@ __global__ void __launch_bounds__(512, 1) lin_tc_kernel(const __grid_constant__ 
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + K::S_BAR);
   uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(smem + K::S_BAR + 8 * kBars);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + K::S_BAR + 8 * kBars + 4);
-  int* bad = reinterpret_cast<int*>(smem + K::S_BAR + 8 * kBars + 8);   // [2]
-  static_assert(8 * kBars + 16 <= 256, "barriers and flags fit their slot");
+  int* bad = reinterpret_cast<int*>(smem + K::S_BAR + 8 * kBars + 8);   // [4]
+  static_assert(8 * kBars + 24 <= 256, "barriers and flags fit their slot");
   const uint32_t sbase = smem_u32(smem);
   auto sX = [&](int c) { return (c % NS) * 2 * K::TX; };
   auto sY = [&](int c) { return (c % NS) * 2 * K::TX + K::TX; };
@@ -165,11 +170,12 @@ __global__ void __launch_bounds__(512, 1) lin_tc_kernel(const __grid_constant__ 
     tmem_relinquish();
   }
   if (tid == 32) {
-    for (int i = 0; i < kBars; ++i) {   // arrivals: one, or one per warp of the role that fills the buffer
-      const bool warps = i == kPReady || i == kPReady + 1 || i == kZReady || i == kZReady + 1 || i == kSReady || i == kOFree;
-      mbar_init(bars + i, warps ? 4 : 1);
+    for (int i = 0; i < kBars; ++i) {   // arrivals: one, or one per warp of the roles that fill the buffer
+      const bool warps4 = i == kPReady || i == kPReady + 1 || i == kSReady || i == kOFree ||
+                          i == kZReady || i == kZReady + 1;
+      mbar_init(bars + i, K::kSplit && (i == kZReady || i == kZReady + 1) ? 8 : warps4 ? 4 : 1);
     }
-    bad[0] = bad[1] = C;
+    for (int i = 0; i < 4; ++i) bad[i] = C;
     *abort_flag = 0;
     fence_barrier_init();
   }
@@ -185,6 +191,62 @@ __global__ void __launch_bounds__(512, 1) lin_tc_kernel(const __grid_constant__ 
   auto wait = [&](int bar, uint32_t parity) { return mbar_wait_or_abort(bars + bar, parity & 1u, a.err, abort_flag); };
   // one outcome for a warp: what follows is warp-wide
   auto warp_wait = [&](int bar, uint32_t parity) { return __all_sync(0xffffffffu, wait(bar, parity)) != 0; };
+
+  // w z of chunk c (of half of it if split) in two bf16 parts, at z's own
+  // offsets (row = token); u: the thread among its role's 128
+  auto weigh = [&](int c, int half, int u) -> bool {
+    constexpr int kIter = K::kSplit ? 4 : 8;
+    const int L = min(C, a.N - chunk_at(c) * C);
+    uint8_t* zw = smem + K::S_ZW + (c % K::NZ) * 2 * kBox;
+    const uint8_t* zs = smem + sZ(c);
+    if (c >= K::NZ && !warp_wait(kZFree + c % K::NZ, c / K::NZ - 1)) return false;   // G4 has read the buffer
+    if (!warp_wait(kFullZ + c % NT, c / NT)) return false;
+    const __nv_bfloat162 zero = __float2bfloat162_rn(0.f);
+    __nv_bfloat162 probe = zero;   // 0 * z: NaN if any z is not finite
+    uint32_t off = (4 * half * kRoleThreads + u) * 16;
+    int t = 64 * half + (u >> 3);
+    uint4 zn = *reinterpret_cast<const uint4*>(zs + off);
+#pragma unroll 1
+    for (int i = 0; i < kIter; ++i) {
+      const uint32_t zz[4] = {zn.x, zn.y, zn.z, zn.w};
+      if (i + 1 < kIter) zn = *reinterpret_cast<const uint4*>(zs + off + 16 * kRoleThreads);
+      const float wt = t < L ? pw[rev ? t : L - 1 - t] : 0.f;
+      const uint64_t w2 = f2_pack(wt, wt), minus = f2_pack(-1.f, -1.f);
+      uint32_t hi[4], lo[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        probe = __hfma2(*reinterpret_cast<const __nv_bfloat162*>(&zz[e]), zero, probe);
+        const uint64_t v = f2_mul(f2_pack(bf_lo(zz[e]), bf_hi(zz[e])), w2);
+        hi[e] = pack2(v);
+        lo[e] = pack2(f2_fma(f2_pack(bf_lo(hi[e]), bf_hi(hi[e])), minus, v));
+      }
+      *reinterpret_cast<uint4*>(zw + off) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+      *reinterpret_cast<uint4*>(zw + kBox + off) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+      off += 16 * kRoleThreads;
+      t += 16;
+    }
+    if (!STATE_ONLY && !__hbeq2(probe, zero)) {
+      // A NaN or infinity in z: 0 * z of the masked half would reach the
+      // tokens before it.  G2 reads a zero instead and the output warps write
+      // NaN from its token on.
+#pragma unroll 1
+      for (int i = 16 * half; i < 16 * half + 4 * kIter; ++i) {
+        const int it = i >> 2, tt = 16 * it + (u >> 3);
+        uint32_t* z = reinterpret_cast<uint32_t*>(smem + sZ(c) + (it * kRoleThreads + u) * 16) + (i & 3);
+        uint32_t x = *z;
+        if ((x & 0x7f80u) == 0x7f80u) x &= 0xffff0000u;
+        if ((x & 0x7f800000u) == 0x7f800000u) x &= 0x0000ffffu;
+        if (x != *z) {
+          *z = x;
+          atomicMin(bad + (c & 3), rev ? C - 1 - tt : tt);
+        }
+      }
+    }
+    fence_async_smem();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(bars + kZReady + c % K::NZ);
+    return true;
+  };
 
   if (warp < 4) {
     // ------------------------------------------------------------------- P
@@ -243,59 +305,6 @@ __global__ void __launch_bounds__(512, 1) lin_tc_kernel(const __grid_constant__ 
   } else if (warp < 8) {
     // ------------------------------------------------------------------- O
     const int u = tid - kRoleThreads;
-    // w z of chunk c in two bf16 parts, at z's own offsets (row = token)
-    auto weigh = [&](int c) -> bool {
-      const int L = min(C, a.N - chunk_at(c) * C);
-      uint8_t* zw = smem + K::S_ZW + (c % K::NZ) * 2 * kBox;
-      const uint8_t* zs = smem + sZ(c);
-      if (c >= K::NZ && !warp_wait(kZFree + c % K::NZ, c / K::NZ - 1)) return false;   // G4 has read the buffer
-      if (!warp_wait(kFullZ + c % NT, c / NT)) return false;
-      const __nv_bfloat162 zero = __float2bfloat162_rn(0.f);
-      __nv_bfloat162 probe = zero;   // 0 * z: NaN if any z is not finite
-      uint32_t off = u * 16;
-      int t = u >> 3;
-      uint4 zn = *reinterpret_cast<const uint4*>(zs + off);
-#pragma unroll 1
-      for (int i = 0; i < 8; ++i) {
-        const uint32_t zz[4] = {zn.x, zn.y, zn.z, zn.w};
-        if (i < 7) zn = *reinterpret_cast<const uint4*>(zs + off + 16 * kRoleThreads);
-        const float wt = t < L ? pw[rev ? t : L - 1 - t] : 0.f;
-        const uint64_t w2 = f2_pack(wt, wt), minus = f2_pack(-1.f, -1.f);
-        uint32_t hi[4], lo[4];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          probe = __hfma2(*reinterpret_cast<const __nv_bfloat162*>(&zz[e]), zero, probe);
-          const uint64_t v = f2_mul(f2_pack(bf_lo(zz[e]), bf_hi(zz[e])), w2);
-          hi[e] = pack2(v);
-          lo[e] = pack2(f2_fma(f2_pack(bf_lo(hi[e]), bf_hi(hi[e])), minus, v));
-        }
-        *reinterpret_cast<uint4*>(zw + off) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-        *reinterpret_cast<uint4*>(zw + kBox + off) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
-        off += 16 * kRoleThreads;
-        t += 16;
-      }
-      if (!STATE_ONLY && !__hbeq2(probe, zero)) {
-        // A NaN or infinity in z: 0 * z of the masked half would reach the
-        // tokens before it.  G2 reads a zero instead and the output warps write
-        // NaN from its token on.
-#pragma unroll 1
-        for (int i = 0; i < 32; ++i) {
-          const int it = i >> 2, tt = 16 * it + (u >> 3);
-          uint32_t* z = reinterpret_cast<uint32_t*>(smem + sZ(c) + (it * kRoleThreads + u) * 16) + (i & 3);
-          uint32_t x = *z;
-          if ((x & 0x7f80u) == 0x7f80u) x &= 0xffff0000u;
-          if ((x & 0x7f800000u) == 0x7f800000u) x &= 0x0000ffffu;
-          if (x != *z) {
-            *z = x;
-            atomicMin(bad + (c & 1), rev ? C - 1 - tt : tt);
-          }
-        }
-      }
-      fence_async_smem();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(bars + kZReady + c % K::NZ);
-      return true;
-    };
     bool alive = true;
     const int p = rev ? C - 1 - u : u;
     const float hd = a.scale * expf(g * (p + 1));
@@ -304,18 +313,18 @@ __global__ void __launch_bounds__(512, 1) lin_tc_kernel(const __grid_constant__ 
     uint8_t* row = smem + K::S_OUT + u * 128;
 #pragma unroll 1
     for (int c = -1; c < n; ++c) {
-      if (c + 1 < n) alive = alive && weigh(c + 1);
+      if (c + 1 < n) alive = alive && weigh(c + 1, 0, u);
       if (c < 0) continue;           // the first chunk is weighed before the first output
       if (STATE_ONLY) {
         if (!alive) break;
         continue;
       }
       const bool ok = alive && warp_wait(kOFull, c);
-      const int from = *reinterpret_cast<volatile int*>(bad + (c & 1));
+      const int from = *reinterpret_cast<volatile int*>(bad + (c & 3));
       if (u == 0) bulk_wait_read_0();                      // the last store has left the staging tile
       if (named_sync_or(1, kRoleThreads, !ok)) break;      // one outcome for the role
       tc_fence_after();
-      if (u == 0 && from < C) bad[c & 1] = C;              // all have read it; weigh(c + 2) comes after the next barrier
+      if (u == 0 && from < C) bad[c & 3] = C;              // all have read it; its next use follows this chunk's kOFree
       const uint32_t to = tmem + (static_cast<uint32_t>(warp - 4) << 21);
 #pragma unroll 1
       for (int q = 0; q < 4; ++q) {
@@ -376,7 +385,10 @@ __global__ void __launch_bounds__(512, 1) lin_tc_kernel(const __grid_constant__ 
     };
     write_operand();
 
-    for (int c = 0; c < n; ++c) {
+#pragma unroll 1
+    for (int c = -1; c < n; ++c) {
+      if (K::kSplit && c + 1 < n && !weigh(c + 1, 1, u)) break;
+      if (c < 0) continue;
       const int L = min(C, a.N - chunk_at(c) * C);
       const float dec = L == C || rev ? dec_full : expm1f(g * L);
       const uint64_t dec2 = f2_pack(dec, dec);
