@@ -566,21 +566,48 @@ def decode_step_ex(q, k, v, state, M, delta=None, A=None, delta_t=None, gain=Non
 
 
 # ------------------------------------------------- linear attention, norm, beams
+# These calls are short enough for the checks to show in a decoding loop, so
+# the common case is tested with few operations and the wordy helpers above
+# only say what was wrong.
+def _ok(t, shape, dtype):
+    return isinstance(t, torch.Tensor) and t.dtype is dtype and (shape is None or t.shape == shape)
+
+
+def _ad(t):
+    """Address of a contiguous tensor (None for None)."""
+    if t is None:
+        return None
+    if not t.is_contiguous():
+        raise ValueError("tensors must be contiguous")
+    return t.data_ptr()
+
+
+def _place(*named):
+    """The index of the one CUDA device that the named tensors (None skipped) live on."""
+    idx = named[0][1].get_device()
+    for _, t in named:
+        if t is not None and t.get_device() != idx:
+            idx = -1
+    return idx if idx >= 0 else _cuda_device(named).index
+
+
 class _On:
     """Makes a call's device and stream current while outputs and scratch are
     allocated and the kernels are launched, so that a tensor of another device
     than the current one works and memory allocated for another stream belongs
-    to that stream's pool.  `raw` is the stream's handle."""
+    to that stream's pool.  Gives the stream's handle."""
 
-    def __init__(self, dev, stream):
+    def __init__(self, idx, stream):
+        self.ctx = None
         if stream is not None:
-            if stream.device != dev:
-                raise ValueError(f"stream is on {stream.device}, the tensors on {dev}")
+            if stream.device_index != idx:
+                raise ValueError(f"stream is on cuda:{stream.device_index}, the tensors on cuda:{idx}")
             self.ctx = torch.cuda.stream(stream)   # makes its device current too
             self.raw = stream.cuda_stream
         else:
-            self.ctx = torch.cuda.device(dev) if dev.index != torch.cuda.current_device() else None
-            self.raw = torch.cuda.current_stream(dev).cuda_stream
+            if idx != torch.cuda.current_device():
+                self.ctx = torch.cuda.device(idx)
+            self.raw = torch.cuda.current_stream(idx).cuda_stream
 
     def __enter__(self):
         if self.ctx is not None:
@@ -631,18 +658,21 @@ def _small(name, *sizes):
 
 def _check_linear_args(dim, q, k, v, log_decay):
     """q, k [B,H,(N,)d_k], v [B,H,(N,)d_v] in one input dtype, log_decay [H] fp32.  Returns the C shape."""
-    names = "[B,H,N,d_k]" if dim == 4 else "[B,H,d_k]"
     _need("q", q)
-    if q.dim() != dim:
-        raise ValueError(f"q must be {names}, got shape {tuple(q.shape)}")
     code = _dtype_code(q)
-    _need("k", k, q.shape, q.dtype)
-    _need("v", v, dtype=q.dtype)
-    if v.dim() != dim or v.shape[:-1] != q.shape[:-1]:
-        raise ValueError(f"v must be {names.replace('d_k', 'd_v')} with q's leading sizes, got {tuple(v.shape)}")
-    _need("log_decay", log_decay, (q.shape[1],), torch.float32)
-    _small("q, v", *q.shape, *v.shape)
-    return IALinearShape(q.shape[0], q.shape[1], q.shape[2] if dim == 4 else 1, q.shape[-1], v.shape[-1], code)
+    size, vsize = q.shape, v.shape if isinstance(v, torch.Tensor) else ()
+    if not (len(size) == dim == len(vsize) and _ok(k, size, q.dtype) and v.dtype is q.dtype and vsize[:-1] == size[:-1]
+            and _ok(log_decay, size[1:2], torch.float32)):
+        names = "[B,H,N,d_k]" if dim == 4 else "[B,H,d_k]"
+        if len(size) != dim:
+            raise ValueError(f"q must be {names}, got shape {tuple(size)}")
+        _need("k", k, size, q.dtype)
+        _need("v", v, dtype=q.dtype)
+        if len(vsize) != dim or vsize[:-1] != size[:-1]:
+            raise ValueError(f"v must be {names.replace('d_k', 'd_v')} with q's leading sizes, got {tuple(vsize)}")
+        _need("log_decay", log_decay, (size[1],), torch.float32)
+    _small("q, v", *size, vsize[-1])
+    return IALinearShape(size[0], size[1], size[2] if dim == 4 else 1, size[-1], vsize[-1], code)
 
 
 def _scratch(nbytes, dev, workspace):
@@ -651,7 +681,8 @@ def _scratch(nbytes, dev, workspace):
         if nbytes == 0:
             return None, None, 0
         workspace = torch.empty(nbytes, dtype=torch.uint8, device=dev)
-    return workspace, _ptr(workspace), _nbytes(workspace)
+        return workspace, workspace.data_ptr(), nbytes
+    return workspace, _ad(workspace), _nbytes(workspace)
 
 
 def linear_prefill_fwd(q, k, v, log_decay, scale=None, state_in=None, want_state=False, o=None, workspace=None,
@@ -671,17 +702,17 @@ def linear_prefill_fwd(q, k, v, log_decay, scale=None, state_in=None, want_state
         _need("o", o, v.shape, q.dtype)
     if workspace is not None:
         _need("workspace", workspace)
-    dev = _cuda_device([("q", q), ("k", k), ("v", v), ("log_decay", log_decay), ("state_in", state_in), ("o", o),
-                        ("workspace", workspace)])
+    dev = _place(("q", q), ("k", k), ("v", v), ("log_decay", log_decay), ("state_in", state_in), ("o", o),
+                        ("workspace", workspace))
     ref = ctypes.byref(shp)
     with _On(dev, stream) as raw:
         if o is None:
             o = torch.empty(v.shape, dtype=q.dtype, device=dev)
         st = torch.empty(n_state, dtype=torch.float32, device=dev) if want_state else None
         ws, wp, wb = _scratch(lib.ia_linear_prefill_workspace_bytes(ref), dev, workspace)
-        rc = lib.ia_linear_prefill_fwd(ref, _ptr(q), _ptr(k), _ptr(v), _ptr(log_decay),
-                                       shp.d_k ** -0.5 if scale is None else scale, _ptr(state_in), _ptr(o),
-                                       _ptr(st), wp, wb, raw)
+        rc = lib.ia_linear_prefill_fwd(ref, _ad(q), _ad(k), _ad(v), _ad(log_decay),
+                                       shp.d_k ** -0.5 if scale is None else scale, _ad(state_in), _ad(o),
+                                       _ad(st), wp, wb, raw)
     _check(rc, "ia_linear_prefill_fwd")
     return {"o": o, "state": st}
 
@@ -694,15 +725,15 @@ def linear_fwd_bwd(q, k, v, log_decay, dO, scale=None, workspace=None, stream=No
     _need("dO", dO, v.shape, q.dtype)
     if workspace is not None:
         _need("workspace", workspace)
-    dev = _cuda_device([("q", q), ("k", k), ("v", v), ("log_decay", log_decay), ("dO", dO), ("workspace", workspace)])
+    dev = _place(("q", q), ("k", k), ("v", v), ("log_decay", log_decay), ("dO", dO), ("workspace", workspace))
     ref = ctypes.byref(shp)
     with _On(dev, stream) as raw:
         o, dv = (torch.empty(v.shape, dtype=q.dtype, device=dev) for _ in range(2))
         dq, dk = (torch.empty(q.shape, dtype=q.dtype, device=dev) for _ in range(2))
         ws, wp, wb = _scratch(lib.ia_linear_fwd_bwd_workspace_bytes(ref), dev, workspace)
-        rc = lib.ia_linear_fwd_bwd(ref, _ptr(q), _ptr(k), _ptr(v), _ptr(log_decay),
-                                   shp.d_k ** -0.5 if scale is None else scale, _ptr(dO), _ptr(o), _ptr(dq),
-                                   _ptr(dk), _ptr(dv), wp, wb, raw)
+        rc = lib.ia_linear_fwd_bwd(ref, _ad(q), _ad(k), _ad(v), _ad(log_decay),
+                                   shp.d_k ** -0.5 if scale is None else scale, _ad(dO), _ad(o), _ad(dq),
+                                   _ad(dk), _ad(dv), wp, wb, raw)
     _check(rc, "ia_linear_fwd_bwd")
     return {"o": o, "dq": dq, "dk": dk, "dv": dv}
 
@@ -729,15 +760,15 @@ def linear_decode_step(q, k, v, log_decay, state, scale=None, state_out=None, pa
             raise ValueError("state_out is needed with parents: a state may have several followers")
     if o is not None:
         _need("o", o, v.shape, q.dtype)
-    dev = _cuda_device([("q", q), ("k", k), ("v", v), ("log_decay", log_decay), ("state", state),
-                        ("state_out", state_out), ("parents", parents), ("o", o)])
+    dev = _place(("q", q), ("k", k), ("v", v), ("log_decay", log_decay), ("state", state),
+                        ("state_out", state_out), ("parents", parents), ("o", o))
     out = state if state_out is None else state_out
     with _On(dev, stream) as raw:
         if o is None:
             o = torch.empty(v.shape, dtype=q.dtype, device=dev)
-        rc = lib.ia_linear_decode_step(ctypes.byref(shp), _ptr(q), _ptr(k), _ptr(v), _ptr(log_decay),
-                                       shp.d_k ** -0.5 if scale is None else scale, _ptr(state), _ptr(parents),
-                                       beams, _ptr(out), _ptr(o), raw)
+        rc = lib.ia_linear_decode_step(ctypes.byref(shp), _ad(q), _ad(k), _ad(v), _ad(log_decay),
+                                       shp.d_k ** -0.5 if scale is None else scale, _ad(state), _ad(parents),
+                                       beams, _ad(out), _ad(o), raw)
     _check(rc, "ia_linear_decode_step")
     return {"o": o, "state": out}
 
@@ -761,14 +792,14 @@ def layer_norm_fwd(x, weight=None, bias=None, eps=1e-5, y=None, stream=None):
     rows, D, code = _check_rows(x, weight, bias)
     if y is not None:
         _need("y", y, x.shape, x.dtype)
-    dev = _cuda_device([("x", x), ("weight", weight), ("bias", bias), ("y", y)])
+    dev = _place(("x", x), ("weight", weight), ("bias", bias), ("y", y))
     with _On(dev, stream) as raw:
         if y is None:
             y = torch.empty(x.shape, dtype=x.dtype, device=dev)
         mean = torch.empty(x.shape[:-1], dtype=torch.float32, device=dev)
         rstd = torch.empty(x.shape[:-1], dtype=torch.float32, device=dev)
-        rc = lib.ia_layer_norm_fwd(rows, D, code, _ptr(x), _ptr(weight), _ptr(bias), eps, _ptr(y), _ptr(mean),
-                                   _ptr(rstd), raw)
+        rc = lib.ia_layer_norm_fwd(rows, D, code, _ad(x), _ad(weight), _ad(bias), eps, _ad(y), _ad(mean),
+                                   _ad(rstd), raw)
     _check(rc, "ia_layer_norm_fwd")
     return {"y": y, "mean": mean, "rstd": rstd}
 
@@ -790,8 +821,8 @@ def layer_norm_bwd(dy, x, mean, rstd, weight=None, want_params=True, dx=None, wo
         _need("dx", dx, x.shape, x.dtype)
     if workspace is not None:
         _need("workspace", workspace)
-    dev = _cuda_device([("x", x), ("dy", dy), ("mean", mean), ("rstd", rstd), ("weight", weight), ("dx", dx),
-                        ("workspace", workspace)])
+    dev = _place(("x", x), ("dy", dy), ("mean", mean), ("rstd", rstd), ("weight", weight), ("dx", dx),
+                        ("workspace", workspace))
     with _On(dev, stream) as raw:
         if dx is None:
             dx = torch.empty(x.shape, dtype=x.dtype, device=dev)
@@ -801,8 +832,8 @@ def layer_norm_bwd(dy, x, mean, rstd, weight=None, want_params=True, dx=None, wo
             dw = torch.empty(D, dtype=torch.float32, device=dev)
             db = torch.empty(D, dtype=torch.float32, device=dev)
             ws, wp, wb = _scratch(lib.ia_layer_norm_bwd_workspace_bytes(rows, D, code), dev, workspace)
-        rc = lib.ia_layer_norm_bwd(rows, D, code, _ptr(dy), _ptr(x), _ptr(weight), _ptr(mean), _ptr(rstd), _ptr(dx),
-                                   _ptr(dw), _ptr(db), wp, wb, raw)
+        rc = lib.ia_layer_norm_bwd(rows, D, code, _ad(dy), _ad(x), _ad(weight), _ad(mean), _ad(rstd), _ad(dx),
+                                   _ad(dw), _ad(db), wp, wb, raw)
     _check(rc, "ia_layer_norm_bwd")
     return {"dx": dx, "dweight": dw, "dbias": db}
 
@@ -831,14 +862,14 @@ def beam_select(logits, scores, K, finished=None, end_token=0, workspace=None, s
             raise TypeError(f"finished has dtype {finished.dtype}, expected bool or uint8")
     if workspace is not None:
         _need("workspace", workspace)
-    dev = _cuda_device([("logits", logits), ("scores", scores), ("finished", finished), ("workspace", workspace)])
+    dev = _place(("logits", logits), ("scores", scores), ("finished", finished), ("workspace", workspace))
     with _On(dev, stream) as raw:
         out = torch.empty(G, K, dtype=torch.float32, device=dev)
         parents = torch.empty(G, K, dtype=torch.int32, device=dev)
         tokens = torch.empty(G, K, dtype=torch.int32, device=dev)
         ws, wp, wb = _scratch(lib.ia_beam_select_workspace_bytes(G, W, V, K, code), dev, workspace)
-        rc = lib.ia_beam_select(G, W, V, K, code, _ptr(logits), _ptr(scores), _ptr(finished), int(end_token), _ptr(out),
-                                _ptr(parents), _ptr(tokens), wp, wb, raw)
+        rc = lib.ia_beam_select(G, W, V, K, code, _ad(logits), _ad(scores), _ad(finished), int(end_token), _ad(out),
+                                _ad(parents), _ad(tokens), wp, wb, raw)
     _check(rc, "ia_beam_select")
     return {"scores": out, "parents": parents, "tokens": tokens}
 
@@ -851,11 +882,11 @@ def _reorder(call, where, shp, per, B, state, parents, out, stream):
     G, wout = parents.shape
     if out is not None:
         _need("out", out, dtype=torch.float32, numel=per * G * wout)
-    dev = _cuda_device([("state", state), ("parents", parents), ("out", out)])
+    dev = _place(("state", state), ("parents", parents), ("out", out))
     with _On(dev, stream) as raw:
         if out is None:
             out = torch.empty(per * G * wout, dtype=torch.float32, device=dev)
-        rc = call(ctypes.byref(shp), B // G, wout, _ptr(parents), _ptr(state), _ptr(out), raw)
+        rc = call(ctypes.byref(shp), B // G, wout, _ad(parents), _ad(state), _ad(out), raw)
     _check(rc, where)
     return out
 

@@ -58,7 +58,8 @@ __host__ __device__ inline SimtSmem simt_smem(int dx, int C) {
 template <int C, bool BF16, bool STATE_ONLY>
 __global__ void __launch_bounds__(kThreads) lin_simt_kernel(const __grid_constant__ LinArgs a) {
   extern __shared__ __align__(16) float sm[];
-  __shared__ int bad;   // least position in the chunk whose z holds a NaN or an infinity, C if none
+  __shared__ int bad;          // least position in the chunk whose z holds a NaN or an infinity, C if none
+  __shared__ float pw[C + 1];  // lambda^n
   const int tid = threadIdx.x;
   const int nseg = STATE_ONLY ? a.nseg - 1 : a.nseg;
   const long long stream = blockIdx.x / nseg;
@@ -81,6 +82,8 @@ __global__ void __launch_bounds__(kThreads) lin_simt_kernel(const __grid_constan
   const float graw = a.log_decay[h];
   if (!(graw <= 0.f) && tid == 0) atomicOr(a.err, kErrParamRange);
   const float g = lin_log_decay(graw);
+  if (tid <= C) pw[tid] = expf(g * tid);
+  const int warp = tid >> 5, lane = tid & 31;
 
   // entering state
   const float* s0 = seg == 0 ? pr.state_in : STATE_ONLY ? nullptr : pr.seg;
@@ -101,20 +104,25 @@ __global__ void __launch_bounds__(kThreads) lin_simt_kernel(const __grid_constan
     if (tid == 0) bad = C;
     __syncthreads();
     const long long row0 = bh * a.N + t0;
-    for (int e = tid; e < C * dx4; e += kThreads) {
-      const int t = e / dx4, i = e - t * dx4;
-      const bool in = t < L && i < dx;
-      if (!STATE_ONLY) X[t * dxs + i] = in ? lin_load(pr.x, (row0 + t) * dx + i, BF16) : 0.f;
-      Y[t * dxs + i] = in ? lin_load(pr.y, (row0 + t) * dx + i, BF16) : 0.f;
-    }
-    for (int e = tid; e < C * zw4; e += kThreads) {
-      const int t = e / zw4, j = e - t * zw4;
-      float z = (t < L && j < zw) ? lin_load(pr.z, (row0 + t) * dz + z0 + j, BF16) : 0.f;
-      if (!isfinite(z)) {   // 0 * z of the masked half would reach the tokens before it
-        atomicMin(&bad, pr.reverse ? C - 1 - t : t);
-        z = 0.f;
+    // a warp per row, its lanes along the columns
+    for (int i = lane; i < dx4; i += 32) {
+#pragma unroll 4
+      for (int t = warp; t < C; t += kThreads / 32) {
+        const bool in = t < L && i < dx;
+        if (!STATE_ONLY) X[t * dxs + i] = in ? lin_load(pr.x, (row0 + t) * dx + i, BF16) : 0.f;
+        Y[t * dxs + i] = in ? lin_load(pr.y, (row0 + t) * dx + i, BF16) : 0.f;
       }
-      Z[t * zs + j] = z;
+    }
+    for (int j = lane; j < zw4; j += 32) {
+#pragma unroll 4
+      for (int t = warp; t < C; t += kThreads / 32) {
+        float z = (t < L && j < zw) ? lin_load(pr.z, (row0 + t) * dz + z0 + j, BF16) : 0.f;
+        if (!isfinite(z)) {   // 0 * z of the masked half would reach the tokens before it
+          atomicMin(&bad, pr.reverse ? C - 1 - t : t);
+          z = 0.f;
+        }
+        Z[t * zs + j] = z;
+      }
     }
     __syncthreads();
     if (!STATE_ONLY) {
@@ -147,7 +155,7 @@ __global__ void __launch_bounds__(kThreads) lin_simt_kernel(const __grid_constan
           for (int s = 0; s < 4; ++s) {
             const int t = tr + r * Q, u = tc + s * Q;
             const int far = pr.reverse ? u - t : t - u;
-            A[t * as + u] = far < 0 ? 0.f : acc[r][s] * expf(g * far);
+            A[t * as + u] = far < 0 ? 0.f : acc[r][s] * pw[far];
           }
       }
       __syncthreads();
@@ -183,7 +191,7 @@ __global__ void __launch_bounds__(kThreads) lin_simt_kernel(const __grid_constan
         for (int r = 0; r < 4; ++r) {
           const int t = tr + r * Q;
           if (t >= L) continue;
-          const float hd = expf(g * ((pr.reverse ? C - 1 - t : t) + 1));
+          const float hd = pw[(pr.reverse ? C - 1 - t : t) + 1];
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
             if (j0 + j >= zw) continue;
@@ -198,10 +206,9 @@ __global__ void __launch_bounds__(kThreads) lin_simt_kernel(const __grid_constan
       __syncthreads();
     }
     // S <- lambda^L S + sum_s (lambda^(L-1-p_s) y_s) z_s^T
-    for (int e = tid; e < C * dx4; e += kThreads) {
-      const int t = e / dx4, i = e - t * dx4;
-      const int p = pr.reverse ? C - 1 - t : t;
-      Y[t * dxs + i] = t < L ? Y[t * dxs + i] * expf(g * (Lw - 1 - p)) : 0.f;
+    for (int t = warp; t < C; t += kThreads / 32) {
+      const float w = t < L ? pw[Lw - 1 - (pr.reverse ? C - 1 - t : t)] : 0.f;
+      for (int i = lane; i < dx4; i += 32) Y[t * dxs + i] *= w;
     }
     __syncthreads();
     const float dec = bad < C ? __int_as_float(0x7fc00000) : expm1f(g * Lw);
@@ -265,9 +272,17 @@ __global__ void __launch_bounds__(kThreads) lin_carry_kernel(const __grid_consta
   const float decf = static_cast<float>(dec);
   float* s = pr.seg + bh * (a.nseg - 1) * per + e;
   float run = s[0];
-  for (int i = 1; i < a.nseg - 1; ++i) {
-    run = fmaf(decf, run, run) + s[i * per];
-    s[i * per] = run;
+  constexpr int kBatch = 8;   // loads in flight
+  for (int i = 1; i < a.nseg - 1; i += kBatch) {
+    float v[kBatch];
+#pragma unroll
+    for (int j = 0; j < kBatch; ++j) v[j] = i + j < a.nseg - 1 ? s[(i + j) * per] : 0.f;
+#pragma unroll
+    for (int j = 0; j < kBatch; ++j)
+      if (i + j < a.nseg - 1) {
+        run = fmaf(decf, run, run) + v[j];
+        s[(i + j) * per] = run;
+      }
   }
 }
 
@@ -342,7 +357,14 @@ LinPlan lin_plan(const ia_linear_shape_t& s, bool train) {
   const long long bh = static_cast<long long>(s.B) * s.H;
   const long long streams = train ? bh * (2LL * lin_zblocks(s.d_v) + 2LL * lin_zblocks(s.d_k)) : bh * lin_zblocks(s.d_v);
   const long long slots = static_cast<long long>(num_sms()) * (p.tc ? 1 : std::max(s.d_k, s.d_v) <= 64 ? 2 : 1);
-  const double f = p.tc ? 0.6 : 0.45, launches = p.tc ? 5.0 : 2.0;
+  // In microseconds on a B200: a chunk of the full pass and of the state-only
+  // pass, what a wave of CTAs costs beside its chunks, and the launches of the
+  // state-only pass and of the carry.  (d = 64: a sequence of 56 chunks alone
+  // takes 88.6 us whole, 78.7 in 2 segments, 31.7 in 8; d = 128: 119, 101, 71.)
+  const bool wide = std::max(s.d_k, s.d_v) > 64;
+  const double full = p.tc ? (wide ? 2.1 : 1.5) : (wide ? 40.0 : 20.0);
+  const double state = p.tc ? (wide ? 1.2 : 1.0) : 0.45 * full;
+  const double wave = 3.5, extra = 2.0, carry = 3.0;
   if (const char* env = std::getenv("IA_LINEAR_SEGMENTS")) {   // forced count (tuning and tests)
     const int want = std::atoi(env);
     if (want >= 1) {
@@ -354,11 +376,15 @@ LinPlan lin_plan(const ia_linear_shape_t& s, bool train) {
   double best = 0.0;
   p.nseg = 1;
   p.cps = p.nch;
-  for (int n = 1; n <= std::min(p.nch, 64); ++n) {
+  // (more segments than fill the slots twice only add chunks' waves)
+  const int most = static_cast<int>(std::min<long long>({p.nch, 64, 2 * slots / streams + 1}));
+  for (int n = 1; n <= most; ++n) {
     const int cps = (p.nch + n - 1) / n, nseg = (p.nch + cps - 1) / cps;
     if (nseg != n) continue;
     auto waves = [&](long long ctas) { return static_cast<double>((ctas + slots - 1) / slots); };
-    const double t = waves(streams * n) * cps + (n > 1 ? waves(streams * (n - 1)) * cps * f + launches : 0.0);
+    double t = waves(streams * n) * (cps * full + wave);
+    if (n > 1) t += waves(streams * (n - 1)) * (cps * state + wave) + extra;
+    if (n > 2) t += carry;
     if (n == 1 || t < best) {
       best = t;
       p.nseg = n;
