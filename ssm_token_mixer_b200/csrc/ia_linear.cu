@@ -24,10 +24,19 @@
 namespace ia {
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 128;
+constexpr int C = 32;   // tokens per chunk: fewer operations per token than 64, and more CTAs per SM
 
-__device__ __forceinline__ float lin_load(const void* p, long long i, bool bf16) {
-  return bf16 ? __bfloat162float(static_cast<const __nv_bfloat16*>(p)[i]) : static_cast<const float*>(p)[i];
+// Element i of p as fp32 to shared memory, 0 outside: an asynchronous copy for
+// fp32 (complete after cp.async.wait_all of the same thread).
+template <bool BF16>
+__device__ __forceinline__ void fetch(float* dst, const void* p, long long i, bool in) {
+  if constexpr (BF16) {
+    *dst = in ? __bfloat162float(static_cast<const __nv_bfloat16*>(p)[i]) : 0.f;
+  } else {
+    const float* src = static_cast<const float*>(p) + (in ? i : 0);
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(smem_u32(dst)), "l"(src), "r"(in ? 4 : 0) : "memory");
+  }
 }
 
 // Row stride in floats of a shared tile of `w` columns: a multiple of 4 whose
@@ -38,7 +47,7 @@ __host__ __device__ inline int lin_pad(int w) { return ((w + 3) / 4 | 1) * 4; }
 struct SimtSmem {
   int X, Y, S, Z, A, total;   // float offsets
 };
-__host__ __device__ inline SimtSmem simt_smem(int dx, int C) {
+__host__ __device__ inline SimtSmem simt_smem(int dx) {
   SimtSmem s;
   const int dxs = lin_pad(dx);
   s.X = 0;
@@ -54,9 +63,10 @@ __host__ __device__ inline SimtSmem simt_smem(int dx, int C) {
 // (b,h, block of 64 z columns, segment), 4 x 4 outputs per thread and step.
 // It reads 16 bytes of shared memory per 8 multiply-adds of a lane, about
 // what an SM can supply, so it is bound by the FP32 pipe and shared memory
-// together.
-template <int C, bool BF16, bool STATE_ONLY>
-__global__ void __launch_bounds__(kThreads) lin_simt_kernel(const __grid_constant__ LinArgs a) {
+// together.  Small CTAs (four per SM at widths up to 64) let one compute
+// while another loads or waits at a barrier.
+template <bool BF16, bool STATE_ONLY>
+__global__ void __launch_bounds__(kThreads, 4) lin_simt_kernel(const __grid_constant__ LinArgs a) {
   extern __shared__ __align__(16) float sm[];
   __shared__ int bad;          // least position in the chunk whose z holds a NaN or an infinity, C if none
   __shared__ float pw[C + 1];  // lambda^n
@@ -74,7 +84,7 @@ __global__ void __launch_bounds__(kThreads) lin_simt_kernel(const __grid_constan
   const int zw = min(kLinZB, dz - z0);
   const int h = static_cast<int>(bh % a.H);
 
-  const SimtSmem o = simt_smem(dx, C);
+  const SimtSmem o = simt_smem(dx);
   const int dxs = lin_pad(dx), zs = lin_pad(kLinZB), as = lin_pad(C);
   const int dx4 = (dx + 3) / 4 * 4, zw4 = (zw + 3) / 4 * 4;
   float *X = sm + o.X, *Y = sm + o.Y, *S = sm + o.S, *Z = sm + o.Z, *A = sm + o.A;
@@ -104,26 +114,29 @@ __global__ void __launch_bounds__(kThreads) lin_simt_kernel(const __grid_constan
     if (tid == 0) bad = C;
     __syncthreads();
     const long long row0 = bh * a.N + t0;
-    // a warp per row, its lanes along the columns
+    // A warp per row, its lanes along the columns; every copy is in flight
+    // before the first is waited for (a chunk cost six DRAM round trips with
+    // plain loads, half of its 10 us).
     for (int i = lane; i < dx4; i += 32) {
-#pragma unroll 4
+#pragma unroll 8
       for (int t = warp; t < C; t += kThreads / 32) {
         const bool in = t < L && i < dx;
-        if (!STATE_ONLY) X[t * dxs + i] = in ? lin_load(pr.x, (row0 + t) * dx + i, BF16) : 0.f;
-        Y[t * dxs + i] = in ? lin_load(pr.y, (row0 + t) * dx + i, BF16) : 0.f;
+        if (!STATE_ONLY) fetch<BF16>(X + t * dxs + i, pr.x, (row0 + t) * dx + i, in);
+        fetch<BF16>(Y + t * dxs + i, pr.y, (row0 + t) * dx + i, in);
       }
     }
     for (int j = lane; j < zw4; j += 32) {
-#pragma unroll 4
-      for (int t = warp; t < C; t += kThreads / 32) {
-        float z = (t < L && j < zw) ? lin_load(pr.z, (row0 + t) * dz + z0 + j, BF16) : 0.f;
-        if (!isfinite(z)) {   // 0 * z of the masked half would reach the tokens before it
-          atomicMin(&bad, pr.reverse ? C - 1 - t : t);
-          z = 0.f;
-        }
-        Z[t * zs + j] = z;
-      }
+#pragma unroll 8
+      for (int t = warp; t < C; t += kThreads / 32)
+        fetch<BF16>(Z + t * zs + j, pr.z, (row0 + t) * dz + z0 + j, t < L && j < zw);
     }
+    if (!BF16) asm volatile("cp.async.wait_all;" ::: "memory");
+    for (int j = lane; j < zw4; j += 32)
+      for (int t = warp; t < C; t += kThreads / 32)
+        if (!isfinite(Z[t * zs + j])) {   // 0 * z of the masked half would reach the tokens before it
+          atomicMin(&bad, pr.reverse ? C - 1 - t : t);
+          Z[t * zs + j] = 0.f;
+        }
     __syncthreads();
     if (!STATE_ONLY) {
       // A = X Y^T, masked and decayed; thread rows t, t + C/4, .. so that the
@@ -132,6 +145,7 @@ __global__ void __launch_bounds__(kThreads) lin_simt_kernel(const __grid_constan
       for (int tile = tid; tile < Q * Q; tile += kThreads) {
         const int tr = tile / Q, tc = tile % Q;
         float acc[4][4] = {};
+#pragma unroll 2
         for (int i = 0; i < dx4; i += 4) {
           float4 xv[4], yv[4];
 #pragma unroll
@@ -165,6 +179,7 @@ __global__ void __launch_bounds__(kThreads) lin_simt_kernel(const __grid_constan
         const int tr = tile / jt, j0 = (tile - tr * jt) * 4;
         float acc[4][4] = {}, acc2[4][4] = {};
         auto gemm = [&](const float* lhs, int ls, const float* rhs, int K, float (&c4)[4][4]) {
+#pragma unroll 2
           for (int i = 0; i < K; i += 4) {
             float4 xv[4], sv[4];
 #pragma unroll
@@ -216,6 +231,7 @@ __global__ void __launch_bounds__(kThreads) lin_simt_kernel(const __grid_constan
     for (int tile = tid; tile < (dx4 / 4) * jt; tile += kThreads) {
       const int i0 = (tile / jt) * 4, j0 = (tile % jt) * 4;
       float acc[4][4] = {};
+#pragma unroll 8
       for (int s = 0; s < C; ++s) {
         const float4 y = *reinterpret_cast<const float4*>(Y + s * dxs + i0);
         const float4 z = *reinterpret_cast<const float4*>(Z + s * zs + j0);
@@ -286,12 +302,12 @@ __global__ void __launch_bounds__(kThreads) lin_carry_kernel(const __grid_consta
   }
 }
 
-template <int C, bool BF16>
+template <bool BF16>
 cudaError_t simt_launch(const LinArgs& a, int max_dx, bool state_only, cudaStream_t st) {
-  const size_t bytes = sizeof(float) * simt_smem(max_dx, C).total;
+  const size_t bytes = sizeof(float) * simt_smem(max_dx).total;
   const long long grid = static_cast<long long>(a.BH) * a.first[a.nprob] * (state_only ? a.nseg - 1 : a.nseg);
   if (grid > (1LL << 31) - 1) return cudaErrorInvalidConfiguration;
-  auto kern = state_only ? lin_simt_kernel<C, BF16, true> : lin_simt_kernel<C, BF16, false>;
+  auto kern = state_only ? lin_simt_kernel<BF16, true> : lin_simt_kernel<BF16, false>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(bytes));
   if (e != cudaSuccess) return e;
   kern<<<static_cast<unsigned>(grid), kThreads, bytes, st>>>(a);
@@ -300,13 +316,10 @@ cudaError_t simt_launch(const LinArgs& a, int max_dx, bool state_only, cudaStrea
 
 }  // namespace
 
-int lin_simt_chunk(int d_k, int d_v) { return std::max(d_k, d_v) <= 128 ? 64 : 32; }
-
-cudaError_t launch_lin_simt(const LinArgs& a, bool bf16, int chunk, bool state_only, cudaStream_t st) {
+cudaError_t launch_lin_simt(const LinArgs& a, bool bf16, bool state_only, cudaStream_t st) {
   int dx = 0;
   for (int i = 0; i < a.nprob; ++i) dx = std::max(dx, a.p[i].dx);
-  if (chunk == 64) return bf16 ? simt_launch<64, true>(a, dx, state_only, st) : simt_launch<64, false>(a, dx, state_only, st);
-  return bf16 ? simt_launch<32, true>(a, dx, state_only, st) : simt_launch<32, false>(a, dx, state_only, st);
+  return bf16 ? simt_launch<true>(a, dx, state_only, st) : simt_launch<false>(a, dx, state_only, st);
 }
 
 cudaError_t launch_lin_carry(const LinArgs& a, int chunk, cudaStream_t st) {
@@ -352,16 +365,17 @@ struct LinPlan {
 LinPlan lin_plan(const ia_linear_shape_t& s, bool train) {
   LinPlan p;
   p.tc = lin_tc_supported(s);
-  p.chunk = p.tc ? kLinTcChunk : lin_simt_chunk(s.d_k, s.d_v);
+  p.chunk = p.tc ? kLinTcChunk : C;
   p.nch = (s.N - 1) / p.chunk + 1;
   const long long bh = static_cast<long long>(s.B) * s.H;
   const long long streams = train ? bh * (2LL * lin_zblocks(s.d_v) + 2LL * lin_zblocks(s.d_k)) : bh * lin_zblocks(s.d_v);
-  const long long slots = static_cast<long long>(num_sms()) * (p.tc ? 1 : std::max(s.d_k, s.d_v) <= 64 ? 2 : 1);
+  const int width = std::max(s.d_k, s.d_v);
+  const long long slots = static_cast<long long>(num_sms()) * (p.tc || width > 128 ? 1 : width > 64 ? 2 : 4);
   // In microseconds on a B200: a chunk of the full pass and of the state-only
   // pass, what a wave of CTAs costs beside its chunks, and the launches of the
   // state-only pass and of the carry.  (d = 64: a sequence of 56 chunks alone
   // takes 88.6 us whole, 78.7 in 2 segments, 31.7 in 8; d = 128: 119, 101, 71.)
-  const bool wide = std::max(s.d_k, s.d_v) > 64;
+  const bool wide = width > 64;
   const double full = p.tc ? (wide ? 2.1 : 1.5) : (wide ? 40.0 : 20.0);
   const double state = p.tc ? (wide ? 1.2 : 1.0) : 0.45 * full;
   const double wave = 3.5, extra = 2.0, carry = 3.0;
@@ -403,7 +417,7 @@ cudaError_t run_problems(LinArgs& a, const LinPlan& p, bool bf16, cudaStream_t s
   a.first[0] = 0;
   for (int i = 0; i < a.nprob; ++i) a.first[i + 1] = a.first[i] + lin_zblocks(a.p[i].dz);
   auto pass = [&](bool state_only) {
-    return p.tc ? launch_lin_tc(a, state_only, st) : launch_lin_simt(a, bf16, p.chunk, state_only, st);
+    return p.tc ? launch_lin_tc(a, state_only, st) : launch_lin_simt(a, bf16, state_only, st);
   };
   mark_launch_begin(st);
   cudaError_t e = cudaSuccess;

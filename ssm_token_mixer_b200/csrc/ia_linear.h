@@ -46,11 +46,10 @@ inline int lin_zblocks(int dz) { return (dz + kLinZB - 1) / kLinZB; }
 __host__ __device__ inline float lin_log_decay(float g) { return g > -1e30f ? g : -1e30f; }
 
 bool lin_tc_supported(const ia_linear_shape_t& s);
-int lin_simt_chunk(int d_k, int d_v);                  // tokens per chunk of the CUDA-core kernel
 constexpr int kLinTcChunk = 128;
 
 // state_only: run every segment but the last from its start for its end state.
-cudaError_t launch_lin_simt(const LinArgs& a, bool bf16, int chunk, bool state_only, cudaStream_t st);
+cudaError_t launch_lin_simt(const LinArgs& a, bool bf16, bool state_only, cudaStream_t st);
 cudaError_t launch_lin_tc(const LinArgs& a, bool state_only, cudaStream_t st);
 // Composes the segments' end states into running ones, in place.
 cudaError_t launch_lin_carry(const LinArgs& a, int chunk, cudaStream_t st);
