@@ -30,7 +30,7 @@
 
 #include "ia_device.cuh"
 #include "ia_internal.h"
-#include "ia_linear.h"
+#include "ia_launch.h"
 
 namespace ia {
 namespace {
@@ -147,6 +147,7 @@ __global__ void __launch_bounds__(kThreads) beam_scan_kernel(const T* __restrict
   const int tid = threadIdx.x;
   const long long at = blockIdx.x, row = at / splits;
   const int split = static_cast<int>(at - row * splits);
+  griddep_launch_dependents();
   if (!live(scores[row], finished && finished[row])) return;   // the merge does not read this row's lists
   if (tid == 0) sm.thr = 0, sm.count = 0;
   __syncthreads();
@@ -297,6 +298,7 @@ __global__ void __launch_bounds__(kThreads) beam_merge_kernel(
   const int tid = threadIdx.x;
   const long long g = blockIdx.x;
   const double nan = __longlong_as_double(0x7ff8000000000000ll);
+  griddep_wait();
 
   for (int w = tid; w < W; w += kThreads) {
     const long long row = g * W + w;
@@ -441,9 +443,8 @@ cudaError_t run_select(int G, int W, int V, int K, const void* logits, const flo
   beam_scan_kernel<T><<<static_cast<unsigned>(rows * splits), kThreads, 0, st>>>(x, scores, fin, V, K, splits, keys, ms, sums);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  beam_merge_kernel<T><<<static_cast<unsigned>(G), kThreads, 0, st>>>(x, scores, fin, end_token, W, V, K, splits, keys,
-                                                                     ms, sums, os, op, ot);
-  return cudaGetLastError();
+  return launch_after(beam_merge_kernel<T>, static_cast<unsigned>(G), kThreads, 0, st, true, x, scores, fin, end_token, W, V, K,
+                      splits, keys, ms, sums, os, op, ot);
 }
 
 // ------------------------------------------------------------- state reorder

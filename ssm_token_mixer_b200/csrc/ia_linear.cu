@@ -19,6 +19,7 @@
 
 #include "ia_device.cuh"
 #include "ia_internal.h"
+#include "ia_launch.h"
 #include "ia_linear.h"
 
 namespace ia {
@@ -94,6 +95,8 @@ __global__ void __launch_bounds__(kThreads, 4) lin_simt_kernel(const __grid_cons
   const float g = lin_log_decay(graw);
   if (tid <= C) pw[tid] = expf(g * tid);
   const int warp = tid >> 5, lane = tid & 31;
+  griddep_launch_dependents();
+  griddep_wait();   // the segments' states, when a pass before this one built them
 
   // entering state
   const float* s0 = seg == 0 ? pr.state_in : STATE_ONLY ? nullptr : pr.seg;
@@ -279,6 +282,8 @@ __global__ void __launch_bounds__(kThreads, 4) lin_simt_kernel(const __grid_cons
 // Every segment but a direction's first holds only whole chunks, and the
 // first one's own length does not matter as nothing enters it.
 __global__ void __launch_bounds__(kThreads) lin_carry_kernel(const __grid_constant__ LinArgs a, int chunk) {
+  griddep_launch_dependents();
+  griddep_wait();
   const LinProblem& pr = a.p[blockIdx.z];
   const long long per = static_cast<long long>(pr.dx) * pr.dz;
   const long long e = static_cast<long long>(blockIdx.y) * kThreads + threadIdx.x;
@@ -310,8 +315,7 @@ cudaError_t simt_launch(const LinArgs& a, int max_dx, bool state_only, cudaStrea
   auto kern = state_only ? lin_simt_kernel<BF16, true> : lin_simt_kernel<BF16, false>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(bytes));
   if (e != cudaSuccess) return e;
-  kern<<<static_cast<unsigned>(grid), kThreads, bytes, st>>>(a);
-  return cudaGetLastError();
+  return launch_after(kern, static_cast<unsigned>(grid), kThreads, bytes, st, a.nseg > 1 && !state_only, a);
 }
 
 }  // namespace
@@ -327,8 +331,7 @@ cudaError_t launch_lin_carry(const LinArgs& a, int chunk, cudaStream_t st) {
   for (int i = 0; i < a.nprob; ++i) per = std::max(per, static_cast<long long>(a.p[i].dx) * a.p[i].dz);
   const dim3 grid(static_cast<unsigned>(a.BH), static_cast<unsigned>((per + kThreads - 1) / kThreads),
                   static_cast<unsigned>(a.nprob));
-  lin_carry_kernel<<<grid, kThreads, 0, st>>>(a, chunk);
-  return cudaGetLastError();
+  return launch_after(lin_carry_kernel, grid, kThreads, 0, st, true, a, chunk);
 }
 
 namespace {

@@ -40,6 +40,7 @@
 
 #include "ia_device.cuh"
 #include "ia_internal.h"
+#include "ia_launch.h"
 #include "ia_linear.h"
 
 namespace ia {
@@ -184,6 +185,8 @@ __global__ void __launch_bounds__(512, 1) lin_tc_kernel(const __grid_constant__ 
   const float g = lin_log_decay(graw);
   float* pw = reinterpret_cast<float*>(smem + K::S_POW);
   if (tid < C) pw[tid] = expf(g * tid);
+  griddep_launch_dependents();
+  griddep_wait();   // the segments' states, when a pass before this one built them
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -576,8 +579,7 @@ cudaError_t launch(const TcParams& prm, const Maps& maps, bool state_only, cudaS
   auto kern = state_only ? lin_tc_kernel<MAXDX, true> : lin_tc_kernel<MAXDX, false>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<MAXDX>::SMEM);
   if (e != cudaSuccess) return e;
-  kern<<<static_cast<unsigned>(grid), kThreads, Cfg<MAXDX>::SMEM, st>>>(prm, maps);
-  return cudaGetLastError();
+  return launch_after(kern, static_cast<unsigned>(grid), kThreads, Cfg<MAXDX>::SMEM, st, a.nseg > 1 && !state_only, prm, maps);
 }
 
 }  // namespace

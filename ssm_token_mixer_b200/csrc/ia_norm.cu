@@ -21,6 +21,7 @@
 
 #include "ia_device.cuh"
 #include "ia_internal.h"
+#include "ia_launch.h"
 
 namespace ia {
 namespace {
@@ -176,6 +177,7 @@ __global__ void __launch_bounds__(512) ln_bwd_kernel(long long rows, int D, int 
   extern __shared__ float acc_sm[];   // [2][D] when the block has several groups
   const int group = threadIdx.x / tpr, gt = threadIdx.x - group * tpr, groups = blockDim.x / tpr;
   const float inv = 1.f / static_cast<float>(D);
+  griddep_launch_dependents();
   float aw[E], ab[E];
 #pragma unroll
   for (int e = 0; e < E; ++e) aw[e] = ab[e] = 0.f;
@@ -349,6 +351,7 @@ __global__ void __launch_bounds__(512) ln_bwd_wide_kernel(long long rows, int D,
 __global__ void __launch_bounds__(256) ln_reduce_kernel(int D, int nparts, const float* __restrict__ part,
                                                         float* __restrict__ dw, float* __restrict__ db) {
   __shared__ float sm[8][33];
+  griddep_wait();
   const int c = blockIdx.x * 32 + (threadIdx.x & 31), r = threadIdx.x >> 5;   // columns of [2 D]
   float t = 0.f;
   if (c < 2 * D)
@@ -457,8 +460,8 @@ cudaError_t ln_bwd(long long rows, int D, const void* dy, const void* x, const f
     });
   }
   if (e != cudaSuccess || !part) return e;
-  ln_reduce_kernel<<<(2 * D + 31) / 32, 256, 0, st>>>(D, static_cast<int>(blocks), part, dw, db);
-  return cudaGetLastError();
+  // (the wide form's last kernel does not write the partial rows: no overlap there)
+  return launch_after(ln_reduce_kernel, (2 * D + 31) / 32, 256, 0, st, D <= kMaxHeld, D, static_cast<int>(blocks), part, dw, db);
 }
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
