@@ -5,25 +5,31 @@
 //   scores[w] + x[w][t] - lse_w,   lse_w = log sum_t exp(x[w][t]).
 // Within a beam the order is that of x, so a beam's K best tokens need no
 // lse, and the scan kernel finds both in one pass over the logits (which HBM
-// bounds): each CTA takes a span of one row, keeps a running maximum and sum
-// of exponentials per thread, and a shared buffer of the values that reach
-// the K-th best seen so far.  The merge kernel, one CTA per request, adds the
-// spans' sums and picks the K best of the rows' lists.
+// bounds): a CTA takes a span of one row, its warps interleaved.  A warp
+// appends the values that reach a threshold to a list in shared memory, by
+// ballot and without a barrier.  The threshold costs next to nothing: every
+// lane keeps the largest value it has seen, a warp takes the r-th largest of
+// its lanes' (of the first round before any is listed, then after 2, 4, 8, ... rounds) and the least of the eight warps'
+// is reached by at least 8 r >= K values of the span.  About 40 (1 + ln n)
+// values of n rounds reach it for K = 16.  A list that grows past 128 all the
+// same (ties, ascending rows) is cut back to its K best.  The merge kernel,
+// one CTA per request, adds the spans' sums and picks the K best of the rows'
+// lists.
 //
 // Order keys.  (value, lower index first) is one 64-bit number: the fp32 value
 // mapped to an order-preserving integer above the complement of the index.
-// All keys differ, which bounds every buffer: of n keys spread over 256
-// threads the K-th largest of the threads' maxima is at most the K-th largest
-// key, and only K threads hold keys that reach it, so at most K * ceil(n/256)
-// keys do.
+// All keys differ, so ranks by counting give a sorted list.
+//
+// Sums.  A warp's terms are exp(x - m) with one m, which follows the maximum
+// only when that has risen by more than 8: no rescaling in the common round.
 //
 // Exactness.  Scores of one beam differ exactly as their logits do; across
-// beams the order hangs on lse_w, whose fp32 sums are off by at most kLseEps/2
-// (a term: 2 ulp of ex2.approx, |t| 2^-24 1.5 ln 2 from the argument, which
-// weighs at most 16 e^-11 for the terms below 2^-16; 7 additions inside a tile;
-// the tiles add up in fp64).  Where two neighbours in the chosen order come
-// from different beams and lie closer than that, the CTA takes those beams'
-// sums again in fp64 and orders once more.
+// beams the order hangs on lse_w, whose fp32 sums are off by at most kLseEps/2:
+// a term by 2 ulp of ex2.approx and by |t| 2^-24 1.5 ln 2 from its argument t
+// (at most 12 above m, and below it the weight 2^-t makes up for it), 7
+// additions inside a lane's 8 values; these add up in fp64.  Where two
+// neighbours in the chosen order come from different beams and lie closer than
+// kLseEps, the CTA takes those beams' sums again in fp64 and orders once more.
 #include <algorithm>
 #include <cmath>
 #include <cstdint>
@@ -37,10 +43,13 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kMaxW = 64, kMaxK = 64;
-constexpr int kPer = 8;                       // values per thread and tile
-constexpr int kTile = kThreads * kPer;        // 2048
-constexpr int kCap = kTile + 512;             // candidate buffer: a tile on top of 512 kept ones
-constexpr int kMergeMost = 4096;              // entries one merge takes
+constexpr int kPer = 8;                       // values per lane and round
+constexpr int kWarps = kThreads / 32;
+constexpr int kKeep = 128;                    // a warp's list is cut back to K when it is longer
+constexpr int kCap = kKeep + 32 * kPer;       // and grows by at most this much in a round
+constexpr int kSlots = kCap / 32;
+constexpr float kSlack = 8.f;
+constexpr int kMergeMost = 2048;              // entries one merge takes (or one per beam and place, if more)
 constexpr double kLseEps = 4e-6;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kInf = __builtin_huge_valf();
@@ -64,52 +73,75 @@ __device__ __forceinline__ float ex2(float x) {
   return y;
 }
 
-// Shared memory of the scan kernel.
+// The K best of n keys in `buf` (n <= kCap), sorted, in buf[0 .. min(n, K));
+// returns that count.  One warp.
+__device__ __forceinline__ int cut_back(uint64_t* buf, int n, int K, int lane) {
+  const unsigned full = 0xffffffffu;
+  uint64_t key[kSlots];
+  uint64_t a = 0, b = 0;   // the lane's largest and second
+#pragma unroll
+  for (int i = 0; i < kSlots; ++i) {
+    const int j = 32 * i + lane;
+    key[i] = j < n ? buf[j] : 0;
+    if (key[i] > a) b = a, a = key[i];
+    else if (key[i] > b) b = key[i];
+  }
+  // A key that at least K keys reach: the K-th largest of the lanes' largest,
+  // or for K > 32 the least of the lanes' second largest.
+  uint64_t thr;
+  if (K <= 32) {
+    int rank = 0;
+#pragma unroll 4
+    for (int l = 0; l < 32; ++l) rank += __shfl_sync(full, a, l) > a;
+    const unsigned who = __ballot_sync(full, a && rank == K - 1);
+    thr = who ? __shfl_sync(full, a, __ffs(who) - 1) : 0;
+  } else {
+    thr = b;
+#pragma unroll
+    for (int o = 16; o; o >>= 1) {
+      const uint64_t other = __shfl_xor_sync(full, thr, o);
+      thr = other < thr ? other : thr;
+    }
+  }
+  __syncwarp();
+  int m = 0;
+#pragma unroll
+  for (int i = 0; i < kSlots; ++i) {
+    const bool in = key[i] && key[i] >= thr;
+    const unsigned who = __ballot_sync(full, in);
+    if (in) buf[m + __popc(who & ((1u << lane) - 1))] = key[i];
+    m += __popc(who);
+  }
+  __syncwarp();
+  int rank[kSlots];
+#pragma unroll
+  for (int i = 0; i < kSlots; ++i) {
+    rank[i] = K;
+    if (32 * i >= m) continue;
+    const int j = 32 * i + lane;
+    key[i] = j < m ? buf[j] : 0;
+    int r = 0;
+#pragma unroll 4
+    for (int l = 0; l < m; ++l) r += buf[l] > key[i];
+    if (j < m) rank[i] = r;
+  }
+  __syncwarp();
+#pragma unroll
+  for (int i = 0; i < kSlots; ++i)
+    if (rank[i] < K) buf[rank[i]] = key[i];
+  __syncwarp();
+  return min(m, K);
+}
+
+constexpr int kAll = kWarps * kMaxK;   // keys the CTA's merge takes
 struct ScanSmem {
-  uint64_t buf[kCap];
-  uint64_t few[kMaxK * ((kCap + kThreads - 1) / kThreads)];
-  uint64_t tmax[kThreads];
-  uint64_t thr;      // no key below this one can be among the K best
-  int count, nfew;
-  float m[kThreads / 32];
-  double s[kThreads / 32];
+  uint64_t buf[kWarps][kCap];
+  uint64_t all[kAll];
+  volatile float lead[kWarps];   // r-th largest of the lanes' largest values, per warp
+  int count[kWarps];
+  float m[kWarps];
+  double s[kWarps];
 };
-
-// The K-th largest of the threads' values (0 if fewer than K are not 0), in
-// sm.thr if it is larger than what stands there.  All threads call it.
-__device__ __forceinline__ void raise_threshold(ScanSmem& sm, uint64_t mine, int K) {
-  sm.tmax[threadIdx.x] = mine;
-  __syncthreads();
-  if (mine) {
-    int rank = 0;
-    for (int i = 0; i < kThreads; ++i) rank += sm.tmax[i] > mine;
-    if (rank == K - 1 && mine > sm.thr) sm.thr = mine;
-  }
-  __syncthreads();
-}
-
-// Keeps the K best keys of the buffer, sorted, in buf[0 .. count).
-__device__ __forceinline__ void compact(ScanSmem& sm, int K) {
-  const int n = sm.count;
-  uint64_t best = 0;
-  for (int i = threadIdx.x; i < n; i += kThreads) best = max(best, sm.buf[i]);
-  if (threadIdx.x == 0) sm.nfew = 0;
-  raise_threshold(sm, best, K);
-  const uint64_t thr = sm.thr;
-  for (int i = threadIdx.x; i < n; i += kThreads)
-    if (sm.buf[i] >= thr) sm.few[atomicAdd(&sm.nfew, 1)] = sm.buf[i];
-  __syncthreads();
-  const int m = sm.nfew;
-  for (int i = threadIdx.x; i < m; i += kThreads) {
-    const uint64_t key = sm.few[i];
-    int rank = 0;
-    for (int j = 0; j < m; ++j) rank += sm.few[j] > key;
-    if (rank < K) sm.buf[rank] = key;
-    if (rank == K - 1) sm.thr = key;   // only this thread writes; the value is at least the old one
-  }
-  if (threadIdx.x == 0) sm.count = min(m, K);
-  __syncthreads();
-}
 
 template <typename T>
 __device__ __forceinline__ float to_f(T x) {
@@ -144,13 +176,12 @@ __global__ void __launch_bounds__(kThreads) beam_scan_kernel(const T* __restrict
                                                              int splits, uint64_t* __restrict__ keys, float* __restrict__ ms,
                                                              double* __restrict__ sums) {
   __shared__ ScanSmem sm;
-  const int tid = threadIdx.x;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const unsigned full = 0xffffffffu;
   const long long at = blockIdx.x, row = at / splits;
   const int split = static_cast<int>(at - row * splits);
   griddep_launch_dependents();
   if (!live(scores[row], finished && finished[row])) return;   // the merge does not read this row's lists
-  if (tid == 0) sm.thr = 0, sm.count = 0;
-  __syncthreads();
 
   const T* x = logits + row * V;
   // values before the first 16-byte boundary, then whole vectors of kPer, then the rest
@@ -159,85 +190,141 @@ __global__ void __launch_bounds__(kThreads) beam_scan_kernel(const T* __restrict
   const int v0 = static_cast<int>(static_cast<long long>(nvec) * split / splits);
   const int v1 = static_cast<int>(static_cast<long long>(nvec) * (split + 1) / splits);
 
-  float m = -kInf;
-  double s = 0.0;
-  auto take = [&](const float (&f)[kPer], int idx, bool first) {   // idx: index of f[0]; unused places hold -inf
+  uint64_t* buf = sm.buf[warp];
+  const int r = (K + kWarps - 1) / kWarps;
+  int count = 0;           // of the warp's list
+  uint64_t own = 0;        // K keys of the warp's list reach it
+  float tv = -kInf;        // smaller values are not wanted
+  float best = -kInf;      // the lane's largest value
+  float m = -kInf;         // the warp's reference
+  double s = 0.0;          // the lane's sum
+  auto announce = [&]() {
+    uint32_t o = ordered(best), M = 0;
+    for (int i = 0; i < r; ++i) {
+      M = __reduce_max_sync(full, o);
+      if (lane == __ffs(__ballot_sync(full, o == M)) - 1) o = 0;
+    }
+    if (lane == 0) sm.lead[warp] = unordered(M);
+  };
+  auto take = [&](const float (&f)[kPer], int idx, int round) {   // idx: index of f[0]; unused places hold -inf
     float tm = f[0];
 #pragma unroll
     for (int i = 1; i < kPer; ++i) tm = fmaxf(tm, f[i]);
-    if (tm > m) {
-      s *= exp(static_cast<double>(m) - static_cast<double>(tm));
-      m = tm;
+    if (__any_sync(full, tm > m + kSlack)) {
+      float M = tm;
+#pragma unroll
+      for (int o = 16; o; o >>= 1) M = fmaxf(M, __shfl_xor_sync(full, M, o));
+      s *= exp(static_cast<double>(m) - static_cast<double>(M));   // m = -inf: 0 * 0
+      m = M;
     }
-    float e[kPer];
     const float base = m == -kInf ? 0.f : m;   // nothing above -inf yet: every term is 0 (or NaN)
+    float e[kPer];
 #pragma unroll
     for (int i = 0; i < kPer; ++i) e[i] = ex2((f[i] - base) * kLog2e);
     s += static_cast<double>(((e[0] + e[1]) + (e[2] + e[3])) + ((e[4] + e[5]) + (e[6] + e[7])));
-    if (first) {   // no threshold yet: it comes from the threads' best
-      uint64_t best = 0;
+    best = fmaxf(best, tm);
+    if ((round & (round + 1)) == 0) {   // rounds 0, 1, 3, 7, ...
+      if (round > 0) announce();
+      float least = sm.lead[0];
 #pragma unroll
-      for (int i = 0; i < kPer; ++i)
-        if (f[i] > -kInf) best = max(best, make_key(f[i], idx + i));
-      raise_threshold(sm, best, K);
+      for (int w = 1; w < kWarps; ++w) least = fminf(least, sm.lead[w]);
+      tv = fmaxf(tv, least);
     }
-    const uint64_t thr = sm.thr;
-    const float tv = thr ? key_value(thr) : -kInf;
-    if (tm >= tv && tm > -kInf) {
+    if (__any_sync(full, tm >= tv && tm > -kInf)) {
+      const unsigned below = (1u << lane) - 1;
 #pragma unroll
-      for (int i = 0; i < kPer; ++i)
-        if (f[i] >= tv && f[i] > -kInf) {
-          const uint64_t key = make_key(f[i], idx + i);
-          if (key >= thr) sm.buf[atomicAdd(&sm.count, 1)] = key;
+      for (int i = 0; i < kPer; ++i) {
+        const bool in = f[i] > -kInf && f[i] >= tv;
+        const unsigned who = __ballot_sync(full, in);
+        if (who == 0) continue;
+        const uint64_t key = make_key(f[i], idx + i);
+        const unsigned keep = __ballot_sync(full, in && key >= own);
+        if (in && key >= own) buf[count + __popc(keep & below)] = key;
+        count += __popc(keep);
+      }
+      __syncwarp();
+      if (count > kKeep) {
+        count = cut_back(buf, count, K, lane);
+        if (count == K) {
+          own = buf[K - 1];
+          tv = fmaxf(tv, key_value(own));
         }
+        __syncwarp();
+      }
     }
-    __syncthreads();
-    if (sm.count > kCap - kTile) compact(sm, K);
-    else __syncthreads();
   };
 
-  const int ntile = (v1 - v0 + kThreads - 1) / kThreads;
-  for (int t = 0; t < ntile; ++t) {
-    const int vec = v0 + t * kThreads + tid;
-    float f[kPer];
-    if (vec < v1) load8(x + head + static_cast<long long>(vec) * kPer, f);
+  float f[kPer], g[kPer];
+  auto load = [&](int vec, float (&d)[kPer]) {
+    if (vec < v1) load8(x + head + static_cast<long long>(vec) * kPer, d);
     else
 #pragma unroll
-      for (int i = 0; i < kPer; ++i) f[i] = -kInf;
-    take(f, head + vec * kPer, t == 0);
+      for (int i = 0; i < kPer; ++i) d[i] = -kInf;
+  };
+  const int first = v0 + warp * 32;
+  load(first + lane, f);
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) best = fmaxf(best, f[i]);
+  announce();              // of the first round's values, so that few of them are listed
+  __syncthreads();
+  int round = 0;
+#pragma unroll 1
+  for (int vec = first; vec < v1; vec += kThreads, ++round) {
+    load(vec + kThreads + lane, g);   // the next round's values are on their way meanwhile
+    take(f, head + (vec + lane) * kPer, round);
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) f[i] = g[i];
   }
-  {   // the ends: head values by the first span, tail values by the last (each fewer than one vector)
+  if (warp == 0) {   // the ends: head values by the first span, tail values by the last (each fewer than one vector)
     const int tail0 = head + nvec * kPer;
     const int n_head = split == 0 ? head : 0, n_tail = split == splits - 1 ? V - tail0 : 0;
-    const int idx = tid < n_head ? tid : tid - n_head < n_tail ? tail0 + tid - n_head : -1;
-    float f[kPer];
+    const int idx = lane < n_head ? lane : lane - n_head < n_tail ? tail0 + lane - n_head : -1;
 #pragma unroll
     for (int i = 0; i < kPer; ++i) f[i] = -kInf;
     if (idx >= 0) f[0] = to_f(x[idx]);
-    take(f, idx, ntile == 0);
+    if (n_head + n_tail > 0) take(f, idx, round);
   }
-  compact(sm, K);
-  if (tid < K) keys[at * K + tid] = tid < sm.count ? sm.buf[tid] : 0;
+  // the CTA's list from the warps' lists
+  if (count > kMaxK) count = cut_back(buf, count, K, lane);
+#pragma unroll
+  for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(full, s, o);
+  if (lane == 0) {
+    sm.count[warp] = count;
+    sm.m[warp] = m;
+    sm.s[warp] = s;
+  }
+  __syncthreads();
+  int base = 0, total = 0;
+#pragma unroll
+  for (int w = 0; w < kWarps; ++w) {
+    if (w < warp) base += sm.count[w];
+    total += sm.count[w];
+  }
+  for (int i = lane; i < count; i += 32) sm.all[base + i] = buf[i];
+  __syncthreads();
+  for (int i = tid; i < total; i += kThreads) {
+    const uint64_t key = sm.all[i];
+    int rank = 0;
+#pragma unroll 4
+    for (int j = 0; j < total; ++j) rank += sm.all[j] > key;
+    if (rank < K) keys[at * K + rank] = key;
+  }
+  for (int i = total + tid; i < K; i += kThreads) keys[at * K + i] = 0;
 
-  // maximum and sum of the CTA.  A NaN logit made its thread's sum NaN; +inf made inf - inf.
-  const unsigned full = 0xffffffffu;
-  float M = m;
+  // maximum and sum of the CTA.  A NaN logit made its lane's sum NaN; +inf made inf - inf.
+  if (warp == 0) {
+    const float mw = lane < kWarps ? sm.m[lane] : -kInf;
+    float M = mw;
 #pragma unroll
-  for (int o = 16; o; o >>= 1) M = fmaxf(M, __shfl_xor_sync(full, M, o));
-  if ((tid & 31) == 0) sm.m[tid >> 5] = M;
-  __syncthreads();
-#pragma unroll
-  for (int w = 0; w < kThreads / 32; ++w) M = fmaxf(M, sm.m[w]);
-  double part = m == -kInf ? s : s * exp(static_cast<double>(m) - static_cast<double>(M));
-#pragma unroll
-  for (int o = 16; o; o >>= 1) part += __shfl_xor_sync(full, part, o);
-  if ((tid & 31) == 0) sm.s[tid >> 5] = part;
-  __syncthreads();
-  if (tid == 0) {
+    for (int o = 4; o; o >>= 1) M = fmaxf(M, __shfl_xor_sync(full, M, o));
     double t = 0.0;
-    for (int w = 0; w < kThreads / 32; ++w) t += sm.s[w];
-    ms[at] = M;
-    sums[at] = t;
+    if (lane < kWarps) t = mw == -kInf ? sm.s[lane] : sm.s[lane] * exp(static_cast<double>(mw) - static_cast<double>(M));
+#pragma unroll
+    for (int o = 4; o; o >>= 1) t += __shfl_xor_sync(full, t, o);
+    if (lane == 0) {
+      ms[at] = M;
+      sums[at] = t;
+    }
   }
 }
 
@@ -249,15 +336,24 @@ __device__ __forceinline__ bool better(const Cand& a, const Cand& b) {
   return a.score > b.score || (a.score == b.score && a.at < b.at);
 }
 
+constexpr int kMergeEntries = kMergeMost > kMaxW * kMaxK ? kMergeMost : kMaxW * kMaxK;
+// of n candidates spread over the threads, the K1-th best of the threads' best
+// is reached by at most K1 ceil(n / threads)
+constexpr int kFew = (kMaxK + 1) * (kMergeEntries / kThreads);
+static_assert(kFew >= kThreads, "one entry per thread fits without narrowing");
+// fp32 and finite: scores below the type's range count as its lowest
+__device__ __forceinline__ float as_float(double s) { return fmaxf(static_cast<float>(s), -3.402823466e38f); }
+
 struct MergeSmem {
-  Cand few[(kMaxK + 1) * (kMergeMost / kThreads)];
+  Cand few[kFew];
   Cand best[kMaxK + 1];
-  double tscore[kThreads];
-  uint64_t tat[kThreads];
+  float tbest[kThreads];
+  float span_m[kMergeMost];
+  double span_s[kMergeMost];
   double lse[kMaxW];      // NaN: no candidates
   double red[kThreads / 32];
   float redm[kThreads / 32];
-  Cand thr;
+  unsigned thr;
   int nfew, again;
   unsigned char redo[kMaxW];
 };
@@ -300,21 +396,27 @@ __global__ void __launch_bounds__(kThreads) beam_merge_kernel(
   const double nan = __longlong_as_double(0x7ff8000000000000ll);
   griddep_wait();
 
+  // the spans' maxima and sums, then one thread per beam
+  for (int i = tid; i < W * splits; i += kThreads) {
+    const long long at = g * W * splits + i;
+    const long long row = g * W + i / splits;
+    const bool in = live(scores[row], finished && finished[row]);
+    sm.span_m[i] = in ? ms[at] : 0.f;
+    sm.span_s[i] = in ? sums[at] : nan;
+  }
+  __syncthreads();
   for (int w = tid; w < W; w += kThreads) {
-    const long long row = g * W + w;
     double lse = nan;
-    if (live(scores[row], finished && finished[row])) {
-      float M = -kInf;
-      for (int p = 0; p < splits; ++p) M = fmaxf(M, ms[row * splits + p]);
-      if (M > -kInf && M < kInf) {
-        double t = 0.0;
-        for (int p = 0; p < splits; ++p) {
-          const float mp = ms[row * splits + p];
-          // a span of nothing but -inf has sum 0 (NaN if it holds one)
-          t += sums[row * splits + p] * (mp == -kInf ? 1.0 : exp(static_cast<double>(mp) - static_cast<double>(M)));
-        }
-        lse = M + log(t);
+    float M = -kInf;
+    for (int p = 0; p < splits; ++p) M = fmaxf(M, sm.span_m[w * splits + p]);
+    if (M > -kInf && M < kInf) {
+      double t = 0.0;
+      for (int p = 0; p < splits; ++p) {
+        const float mp = sm.span_m[w * splits + p];
+        // a span of nothing but -inf has sum 0 (NaN if it holds one)
+        t += sm.span_s[w * splits + p] * (mp == M || mp == -kInf ? 1.0 : exp(static_cast<double>(mp) - static_cast<double>(M)));
       }
+      lse = M + log(t);
     }
     sm.lse[w] = lse;
     sm.redo[w] = 0;
@@ -349,26 +451,53 @@ __global__ void __launch_bounds__(kThreads) beam_merge_kernel(
     if (tid == 0) {
       sm.nfew = 0;
       sm.again = 0;
-      sm.thr = none;
+      sm.thr = 0;
     }
-    Cand mine = none;
+    // A bound that at least K1 candidates reach: the K1-th largest of the
+    // threads' best in fp32 (rounding keeps the order)
+    float mine = -kInf;
+    Cand top = none;
     for (int i = tid; i < n; i += kThreads) {
       Cand c;
-      if (entry(i, c) && better(c, mine)) mine = c;
+      if (entry(i, c) && better(c, top)) top = c, mine = as_float(c.score);
     }
-    sm.tscore[tid] = mine.score;
-    sm.tat[tid] = mine.at;
+    sm.tbest[tid] = mine;
     __syncthreads();
-    if (mine.at != ~0ull) {
+    if (mine > -kInf) {
+      int reach = 0;
+#pragma unroll 4
+      for (int i = 0; i < kThreads; i += 4) {
+        const float4 o = *reinterpret_cast<const float4*>(sm.tbest + i);
+        reach += (o.x >= mine) + (o.y >= mine) + (o.z >= mine) + (o.w >= mine);
+      }
+      if (reach >= K1) atomicMax(&sm.thr, ordered(mine));
+    }
+    __syncthreads();
+    const unsigned thr = sm.thr;
+    for (int i = tid; i < n; i += kThreads) {
+      Cand c;
+      if (!entry(i, c) || ordered(as_float(c.score)) < thr) continue;
+      const int at = atomicAdd(&sm.nfew, 1);
+      if (at < kFew) sm.few[at] = c;
+    }
+    __syncthreads();
+    if (sm.nfew > kFew) {   // more ties in fp32 than fit: the bound from exact scores, through the same list
+      __syncthreads();
+      if (tid == 0) {
+        sm.nfew = 0;
+        sm.best[0] = none;
+      }
+      sm.few[tid] = top;
+      __syncthreads();
       int rank = 0;
-      for (int i = 0; i < kThreads; ++i) rank += better(Cand{sm.tscore[i], sm.tat[i]}, mine);
-      if (rank == K1 - 1) sm.thr = mine;
-    }
-    __syncthreads();
-    const Cand thr = sm.thr;
-    for (int i = tid; i < n; i += kThreads) {
-      Cand c;
-      if (entry(i, c) && !better(thr, c)) sm.few[atomicAdd(&sm.nfew, 1)] = c;
+      for (int i = 0; i < kThreads; ++i) rank += better(sm.few[i], top);
+      if (rank == K1 - 1 && top.at != ~0ull) sm.best[0] = top;
+      __syncthreads();
+      const Cand bound = sm.best[0];
+      for (int i = tid; i < n; i += kThreads) {
+        Cand c;
+        if (entry(i, c) && !better(bound, c)) sm.few[atomicAdd(&sm.nfew, 1)] = c;
+      }
     }
     __syncthreads();
     const int m = sm.nfew;
@@ -409,11 +538,11 @@ __global__ void __launch_bounds__(kThreads) beam_merge_kernel(
   }
 }
 
-// Spans per row: enough CTAs for every SM to hold several, spans of at least
-// four tiles, and no more list entries per request than one merge takes.
+// Spans per row: about six CTAs for every SM, spans of at least two rounds of
+// every warp, and no more list entries per request than one merge takes.
 int beam_splits(long long rows, int W, int V, int K) {
-  const long long want = (static_cast<long long>(num_sms()) * 4 + rows - 1) / rows;
-  const long long by_len = std::max(1, V / (4 * kTile));
+  const long long want = (static_cast<long long>(num_sms()) * 6 + rows - 1) / rows;
+  const long long by_len = std::max(1, V / (2 * kThreads * kPer));
   const long long by_merge = std::max(1, kMergeMost / (W * K));
   return static_cast<int>(std::max(1LL, std::min({want, by_len, by_merge})));
 }
