@@ -22,12 +22,13 @@
 //
 // Sums.  A warp's terms are exp(x - m) with one m, which follows the maximum
 // only when that has risen by more than 8: no rescaling in the common round.
+// (x - m is formed first: x log2 e would overflow for logits of the type's
+// lowest value.)
 //
 // Exactness.  Scores of one beam differ exactly as their logits do; across
 // beams the order hangs on lse_w, whose fp32 sums are off by at most kLseEps/2:
 // a term by 2 ulp of ex2.approx and by |t| 2^-24 1.5 ln 2 from its argument t
-// (at most 12 above m, and below it the weight 2^-t makes up for it), 7
-// additions inside a lane's 8 values; these add up in fp64.  Where two
+// (at most 12 above 0, and below it the weight 2^t makes up for it), 7 additions inside a lane's 8 values; these add up in fp64.  Where two
 // neighbours in the chosen order come from different beams and lie closer than
 // kLseEps, the CTA takes those beams' sums again in fp64 and orders once more.
 #include <algorithm>
@@ -67,6 +68,11 @@ __device__ __forceinline__ uint64_t make_key(float x, uint32_t idx) {
 __device__ __forceinline__ float key_value(uint64_t k) { return unordered(static_cast<uint32_t>(k >> 32)); }
 __device__ __forceinline__ uint32_t key_index(uint64_t k) { return 0xffffffffu - static_cast<uint32_t>(k); }
 
+__device__ __forceinline__ uint64_t f2_add(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
 __device__ __forceinline__ float ex2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -138,7 +144,7 @@ struct ScanSmem {
   uint64_t buf[kWarps][kCap];
   uint64_t all[kAll];
   volatile float lead[kWarps];   // r-th largest of the lanes' largest values, per warp
-  int count[kWarps];
+  int total;
   float m[kWarps];
   double s[kWarps];
 };
@@ -169,7 +175,8 @@ __device__ __forceinline__ void load8(const T* p, float (&f)[kPer]) {
 __device__ __forceinline__ bool live(float score, bool fin) { return !fin && isfinite(score); }
 
 // One CTA per (row, span).  keys [rows][splits][K] (0: none), ms [rows][splits]
-// maxima, sums [rows][splits] of exp(x - max) in fp64 (NaN: no distribution).
+// references m (-inf: nothing above -inf), sums [rows][splits] of exp(x - m) in
+// fp64 (NaN: no distribution).
 template <typename T>
 __global__ void __launch_bounds__(kThreads) beam_scan_kernel(const T* __restrict__ logits, const float* __restrict__ scores,
                                                              const unsigned char* __restrict__ finished, int V, int K,
@@ -193,10 +200,10 @@ __global__ void __launch_bounds__(kThreads) beam_scan_kernel(const T* __restrict
   uint64_t* buf = sm.buf[warp];
   const int r = (K + kWarps - 1) / kWarps;
   int count = 0;           // of the warp's list
-  uint64_t own = 0;        // K keys of the warp's list reach it
   float tv = -kInf;        // smaller values are not wanted
   float best = -kInf;      // the lane's largest value
   float m = -kInf;         // the warp's reference
+  uint64_t minus_m = 0;    // -m twice
   double s = 0.0;          // the lane's sum
   auto announce = [&]() {
     uint32_t o = ordered(best), M = 0;
@@ -214,14 +221,21 @@ __global__ void __launch_bounds__(kThreads) beam_scan_kernel(const T* __restrict
       float M = tm;
 #pragma unroll
       for (int o = 16; o; o >>= 1) M = fmaxf(M, __shfl_xor_sync(full, M, o));
-      s *= exp(static_cast<double>(m) - static_cast<double>(M));   // m = -inf: 0 * 0
+      s *= exp(static_cast<double>(m) - static_cast<double>(M));   // the first time: 0 * 0
       m = M;
+      minus_m = f2_pack(-m, -m);
     }
-    const float base = m == -kInf ? 0.f : m;   // nothing above -inf yet: every term is 0 (or NaN)
-    float e[kPer];
+    // (nothing above -inf yet: every term is 0, or NaN)
+    uint64_t e2[kPer / 2];
 #pragma unroll
-    for (int i = 0; i < kPer; ++i) e[i] = ex2((f[i] - base) * kLog2e);
-    s += static_cast<double>(((e[0] + e[1]) + (e[2] + e[3])) + ((e[4] + e[5]) + (e[6] + e[7])));
+    for (int i = 0; i < kPer / 2; ++i) {
+      float lo, hi;
+      f2_unpack(f2_mul(f2_add(f2_pack(f[2 * i], f[2 * i + 1]), minus_m), f2_pack(kLog2e, kLog2e)), lo, hi);
+      e2[i] = f2_pack(ex2(lo), ex2(hi));
+    }
+    float lo, hi;
+    f2_unpack(f2_add(f2_add(e2[0], e2[1]), f2_add(e2[2], e2[3])), lo, hi);
+    s += static_cast<double>(lo + hi);
     best = fmaxf(best, tm);
     if ((round & (round + 1)) == 0) {   // rounds 0, 1, 3, 7, ...
       if (round > 0) announce();
@@ -237,18 +251,15 @@ __global__ void __launch_bounds__(kThreads) beam_scan_kernel(const T* __restrict
         const bool in = f[i] > -kInf && f[i] >= tv;
         const unsigned who = __ballot_sync(full, in);
         if (who == 0) continue;
-        const uint64_t key = make_key(f[i], idx + i);
-        const unsigned keep = __ballot_sync(full, in && key >= own);
-        if (in && key >= own) buf[count + __popc(keep & below)] = key;
-        count += __popc(keep);
+        if (in) buf[count + __popc(who & below)] = make_key(f[i], idx + i);
+        count += __popc(who);
       }
       __syncwarp();
       if (count > kKeep) {
         count = cut_back(buf, count, K, lane);
-        if (count == K) {
-          own = buf[K - 1];
-          tv = fmaxf(tv, key_value(own));
-        }
+        // (later values that tie with the K-th lose to it, but another warp's
+        // K best may hold fewer of the tied ones: they are listed all the same)
+        if (count == K) tv = fmaxf(tv, key_value(buf[K - 1]));
         __syncwarp();
       }
     }
@@ -284,24 +295,24 @@ __global__ void __launch_bounds__(kThreads) beam_scan_kernel(const T* __restrict
     if (idx >= 0) f[0] = to_f(x[idx]);
     if (n_head + n_tail > 0) take(f, idx, round);
   }
-  // the CTA's list from the warps' lists
+  // the CTA's list from what the warps' lists hold above the last threshold
+  announce();
   if (count > kMaxK) count = cut_back(buf, count, K, lane);
 #pragma unroll
   for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(full, s, o);
   if (lane == 0) {
-    sm.count[warp] = count;
     sm.m[warp] = m;
     sm.s[warp] = s;
   }
+  if (tid == 0) sm.total = 0;
   __syncthreads();
-  int base = 0, total = 0;
+  float least = sm.lead[0];
 #pragma unroll
-  for (int w = 0; w < kWarps; ++w) {
-    if (w < warp) base += sm.count[w];
-    total += sm.count[w];
-  }
-  for (int i = lane; i < count; i += 32) sm.all[base + i] = buf[i];
+  for (int w = 1; w < kWarps; ++w) least = fminf(least, sm.lead[w]);
+  for (int i = lane; i < count; i += 32)
+    if (key_value(buf[i]) >= least) sm.all[atomicAdd(&sm.total, 1)] = buf[i];
   __syncthreads();
+  const int total = sm.total;
   for (int i = tid; i < total; i += kThreads) {
     const uint64_t key = sm.all[i];
     int rank = 0;

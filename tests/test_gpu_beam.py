@@ -50,6 +50,7 @@ def test_ties_go_to_the_lowest_index(dt):
     y, s = data(2, 1, 5000, dt)
     y, s = y.expand(2, 4, 5000).contiguous(), s.expand(2, 4).contiguous()   # four equal beams
     check(y, s, 12)
+    check(torch.zeros(2, 64, 500, dtype=dt, device="cuda"), torch.full((2, 64), -1.0, device="cuda"), 64)
     z = torch.tensor([[[0.0, -0.0, 1.0, -0.0]]], dtype=dt, device="cuda")   # both zeros are one value
     assert check(z, torch.zeros(1, 1, device="cuda"), 4)["tokens"].tolist() == [[2, 0, 1, 3]]
 
