@@ -6,8 +6,8 @@
 // Within a beam the order is that of x, so a beam's K best tokens need no
 // lse, and the scan kernel finds both in one pass over the logits (which HBM
 // bounds): a CTA takes a span of one row, its warps interleaved.  A warp
-// appends the values that reach a threshold to a list in shared memory, by
-// ballot and without a barrier.  The threshold costs next to nothing: every
+// appends the values that reach a threshold to its list in shared memory,
+// without a barrier.  The threshold costs next to nothing: every
 // lane keeps the largest value it has seen, a warp takes the r-th largest of
 // its lanes' (of the first round before any is listed, then after 2, 4, 8, ... rounds) and the least of the eight warps'
 // is reached by at least 8 r >= K values of the span.  About 40 (1 + ln n)
@@ -21,16 +21,19 @@
 // All keys differ, so ranks by counting give a sorted list.
 //
 // Sums.  A warp's terms are exp(x - m) with one m, which follows the maximum
-// only when that has risen by more than 8: no rescaling in the common round.
+// only when that has risen by more than 2: no rescaling in the common round.
 // (x - m is formed first: x log2 e would overflow for logits of the type's
 // lowest value.)
 //
 // Exactness.  Scores of one beam differ exactly as their logits do; across
-// beams the order hangs on lse_w, whose fp32 sums are off by at most kLseEps/2:
-// a term by 2 ulp of ex2.approx and by |t| 2^-24 1.5 ln 2 from its argument t
-// (at most 12 above 0, and below it the weight 2^t makes up for it), 7 additions inside a lane's 8 values; these add up in fp64.  Where two
-// neighbours in the chosen order come from different beams and lie closer than
-// kLseEps, the CTA takes those beams' sums again in fp64 and orders once more.
+// beams the order hangs on lse_w.  A term 2^t of a row's fp32 sum is off by 2
+// ulp of ex2.approx (2^-22) and by ln 2 |t| (2^-24 + 2^-24 + 2^-26) from x - m,
+// the product and log2 e, a lane's tree of 8 adds 3 2^-24, and these add up in
+// fp64.  t is at most 3 above 0; below it the terms' weights keep their mean
+// |t| under log2 V.  So a lse is off by at most 4.2e-7 + 9.3e-8 log2 V, and
+// where two neighbours in the chosen order come from different beams and lie
+// within twice that, the CTA takes those beams' sums again in fp64 and orders
+// once more (4 % of calls at 64 x 8 x 50257, K = 16, normal logits).
 #include <algorithm>
 #include <cmath>
 #include <cstdint>
@@ -49,9 +52,8 @@ constexpr int kWarps = kThreads / 32;
 constexpr int kKeep = 128;                    // a warp's list is cut back to K when it is longer
 constexpr int kCap = kKeep + 32 * kPer;       // and grows by at most this much in a round
 constexpr int kSlots = kCap / 32;
-constexpr float kSlack = 8.f;
+constexpr float kSlack = 2.f;
 constexpr int kMergeMost = 2048;              // entries one merge takes (or one per beam and place, if more)
-constexpr double kLseEps = 4e-6;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kInf = __builtin_huge_valf();
 
@@ -80,8 +82,9 @@ __device__ __forceinline__ float ex2(float x) {
 }
 
 // The K best of n keys in `buf` (n <= kCap), sorted, in buf[0 .. min(n, K));
-// returns that count.  One warp.
-__device__ __forceinline__ int cut_back(uint64_t* buf, int n, int K, int lane) {
+// returns that count.  One warp.  Out of line: it is rare, and its registers
+// would cost the scan one of four CTAs per SM.
+__device__ __noinline__ int cut_back(uint64_t* buf, int n, int K, int lane) {
   const unsigned full = 0xffffffffu;
   uint64_t key[kSlots];
   uint64_t a = 0, b = 0;   // the lane's largest and second
@@ -144,6 +147,7 @@ struct ScanSmem {
   uint64_t buf[kWarps][kCap];
   uint64_t all[kAll];
   volatile float lead[kWarps];   // r-th largest of the lanes' largest values, per warp
+  int count[kWarps];        // of the warps' lists
   int total;
   float m[kWarps];
   double s[kWarps];
@@ -178,28 +182,27 @@ __device__ __forceinline__ bool live(float score, bool fin) { return !fin && isf
 // references m (-inf: nothing above -inf), sums [rows][splits] of exp(x - m) in
 // fp64 (NaN: no distribution).
 template <typename T>
-__global__ void __launch_bounds__(kThreads) beam_scan_kernel(const T* __restrict__ logits, const float* __restrict__ scores,
+__global__ void __launch_bounds__(kThreads, 4) beam_scan_kernel(const T* __restrict__ logits, const float* __restrict__ scores,
                                                              const unsigned char* __restrict__ finished, int V, int K,
                                                              int splits, uint64_t* __restrict__ keys, float* __restrict__ ms,
                                                              double* __restrict__ sums) {
   __shared__ ScanSmem sm;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const unsigned full = 0xffffffffu;
-  const long long at = blockIdx.x, row = at / splits;
+  const unsigned at = blockIdx.x, row = at / static_cast<unsigned>(splits);
   const int split = static_cast<int>(at - row * splits);
   griddep_launch_dependents();
   if (!live(scores[row], finished && finished[row])) return;   // the merge does not read this row's lists
 
-  const T* x = logits + row * V;
+  const T* x = logits + static_cast<long long>(row) * V;
   // values before the first 16-byte boundary, then whole vectors of kPer, then the rest
   const int head = min(V, static_cast<int>(((16 - (reinterpret_cast<uintptr_t>(x) & 15)) & 15) / sizeof(T)));
   const int nvec = (V - head) / kPer;
-  const int v0 = static_cast<int>(static_cast<long long>(nvec) * split / splits);
-  const int v1 = static_cast<int>(static_cast<long long>(nvec) * (split + 1) / splits);
+  const int span = nvec / splits + 1;
+  const int v0 = min(nvec, split * span), v1 = min(nvec, v0 + span);
 
   uint64_t* buf = sm.buf[warp];
   const int r = (K + kWarps - 1) / kWarps;
-  int count = 0;           // of the warp's list
   float tv = -kInf;        // smaller values are not wanted
   float best = -kInf;      // the lane's largest value
   float m = -kInf;         // the warp's reference
@@ -245,21 +248,16 @@ __global__ void __launch_bounds__(kThreads) beam_scan_kernel(const T* __restrict
       tv = fmaxf(tv, least);
     }
     if (__any_sync(full, tm >= tv && tm > -kInf)) {
-      const unsigned below = (1u << lane) - 1;
+      if (tm >= tv)   // few lanes: each appends its own
 #pragma unroll
-      for (int i = 0; i < kPer; ++i) {
-        const bool in = f[i] > -kInf && f[i] >= tv;
-        const unsigned who = __ballot_sync(full, in);
-        if (who == 0) continue;
-        if (in) buf[count + __popc(who & below)] = make_key(f[i], idx + i);
-        count += __popc(who);
-      }
+        for (int i = 0; i < kPer; ++i)
+          if (f[i] >= tv && f[i] > -kInf) buf[atomicAdd(&sm.count[warp], 1)] = make_key(f[i], idx + i);
       __syncwarp();
+      const int count = sm.count[warp];
       if (count > kKeep) {
-        count = cut_back(buf, count, K, lane);
-        // (later values that tie with the K-th lose to it, but another warp's
-        // K best may hold fewer of the tied ones: they are listed all the same)
-        if (count == K) tv = fmaxf(tv, key_value(buf[K - 1]));
+        const int left = cut_back(buf, count, K, lane);
+        if (lane == 0) sm.count[warp] = left;
+        if (left == K) tv = fmaxf(tv, key_value(buf[K - 1]));
         __syncwarp();
       }
     }
@@ -276,6 +274,7 @@ __global__ void __launch_bounds__(kThreads) beam_scan_kernel(const T* __restrict
   load(first + lane, f);
 #pragma unroll
   for (int i = 0; i < kPer; ++i) best = fmaxf(best, f[i]);
+  if (lane == 0) sm.count[warp] = 0;
   announce();              // of the first round's values, so that few of them are listed
   __syncthreads();
   int round = 0;
@@ -297,6 +296,7 @@ __global__ void __launch_bounds__(kThreads) beam_scan_kernel(const T* __restrict
   }
   // the CTA's list from what the warps' lists hold above the last threshold
   announce();
+  int count = sm.count[warp];
   if (count > kMaxK) count = cut_back(buf, count, K, lane);
 #pragma unroll
   for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(full, s, o);
@@ -347,6 +347,7 @@ __device__ __forceinline__ bool better(const Cand& a, const Cand& b) {
   return a.score > b.score || (a.score == b.score && a.at < b.at);
 }
 
+constexpr int kHeld = (kMergeMost > kMaxW * kMaxK ? kMergeMost : kMaxW * kMaxK) / kThreads;   // entries per thread of the merge
 constexpr int kMergeEntries = kMergeMost > kMaxW * kMaxK ? kMergeMost : kMaxW * kMaxK;
 // of n candidates spread over the threads, the K1-th best of the threads' best
 // is reached by at most K1 ceil(n / threads)
@@ -371,10 +372,11 @@ struct MergeSmem {
 
 // lse of one row in fp64, by the whole CTA.
 template <typename T>
-__device__ double exact_lse(const T* x, int V, MergeSmem& sm) {
+__device__ __noinline__ double exact_lse(const T* x, int V, MergeSmem& sm) {
   const unsigned full = 0xffffffffu;
   const int tid = threadIdx.x;
   float m = -kInf;
+#pragma unroll 8
   for (int i = tid; i < V; i += kThreads) m = fmaxf(m, to_f(x[i]));
 #pragma unroll
   for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(full, m, o));
@@ -382,8 +384,14 @@ __device__ double exact_lse(const T* x, int V, MergeSmem& sm) {
   if ((tid & 31) == 0) sm.redm[tid >> 5] = m;
   __syncthreads();
   for (int w = 0; w < kThreads / 32; ++w) m = fmaxf(m, sm.redm[w]);
-  double s = 0.0;
-  for (int i = tid; i < V; i += kThreads) s += exp(static_cast<double>(to_f(x[i])) - m);
+  double part[4] = {0.0, 0.0, 0.0, 0.0};   // four in flight; a fixed order
+  int i = tid;
+  for (; i + 3 * kThreads < V; i += 4 * kThreads) {
+#pragma unroll
+    for (int k = 0; k < 4; ++k) part[k] += exp(static_cast<double>(to_f(x[i + k * kThreads])) - m);
+  }
+  for (; i < V; i += kThreads) part[0] += exp(static_cast<double>(to_f(x[i])) - m);
+  double s = (part[0] + part[1]) + (part[2] + part[3]);
 #pragma unroll
   for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(full, s, o);
   if ((tid & 31) == 0) sm.red[tid >> 5] = s;
@@ -398,7 +406,7 @@ __device__ double exact_lse(const T* x, int V, MergeSmem& sm) {
 template <typename T>
 __global__ void __launch_bounds__(kThreads) beam_merge_kernel(
     const T* __restrict__ logits, const float* __restrict__ scores, const unsigned char* __restrict__ finished,
-    int end_token, int W, int V, int K, int splits, const uint64_t* __restrict__ keys, const float* __restrict__ ms,
+    int end_token, int W, int V, int K, int splits, double eps, const uint64_t* __restrict__ keys, const float* __restrict__ ms,
     const double* __restrict__ sums, float* __restrict__ out_scores, int* __restrict__ out_parents,
     int* __restrict__ out_tokens) {
   __shared__ MergeSmem sm;
@@ -407,6 +415,14 @@ __global__ void __launch_bounds__(kThreads) beam_merge_kernel(
   const double nan = __longlong_as_double(0x7ff8000000000000ll);
   griddep_wait();
 
+  const int per_row = splits * K;
+  const int n = W * per_row;
+  uint64_t key[kHeld];   // this thread's entries tid, tid + kThreads, .. of the rows' lists
+#pragma unroll
+  for (int j = 0; j < kHeld; ++j) {
+    const int i = tid + j * kThreads;
+    key[j] = i < n ? keys[g * n + i] : 0;   // (a finished or dead beam's are not looked at)
+  }
   // the spans' maxima and sums, then one thread per beam
   for (int i = tid; i < W * splits; i += kThreads) {
     const long long at = g * W * splits + i;
@@ -434,25 +450,23 @@ __global__ void __launch_bounds__(kThreads) beam_merge_kernel(
   }
   __syncthreads();
 
-  const int per_row = splits * K;
-  const int n = W * per_row;
-  // entry i of the rows' lists as a candidate; false if it is none
-  auto entry = [&](int i, Cand& c) -> bool {
-    const int w = i / per_row, j = i - w * per_row;
+  // entry tid + j kThreads as a candidate; false if it is none
+  auto entry = [&](int j, Cand& c) -> bool {
+    const int i = tid + j * kThreads;
+    if (i >= n) return false;
+    const int w = i / per_row;
     const long long row = g * W + w;
     const float sc = scores[row];
     if (finished && finished[row]) {
-      if (j != 0 || !isfinite(sc)) return false;
+      if (i != w * per_row || !isfinite(sc)) return false;
       c.score = sc;
       c.at = static_cast<uint64_t>(w) << 32 | static_cast<uint32_t>(end_token);
       return true;
     }
     const double lse = sm.lse[w];
-    if (!(lse == lse)) return false;
-    const uint64_t key = keys[row * per_row + j];
-    if (!key) return false;
-    c.score = static_cast<double>(sc) + (static_cast<double>(key_value(key)) - lse);
-    c.at = static_cast<uint64_t>(w) << 32 | key_index(key);
+    if (!(lse == lse) || !key[j]) return false;
+    c.score = static_cast<double>(sc) + (static_cast<double>(key_value(key[j])) - lse);
+    c.at = static_cast<uint64_t>(w) << 32 | key_index(key[j]);
     return true;
   };
 
@@ -468,9 +482,11 @@ __global__ void __launch_bounds__(kThreads) beam_merge_kernel(
     // threads' best in fp32 (rounding keeps the order)
     float mine = -kInf;
     Cand top = none;
-    for (int i = tid; i < n; i += kThreads) {
+#pragma unroll
+    for (int j = 0; j < kHeld; ++j) {
+      if (j * kThreads >= n) break;
       Cand c;
-      if (entry(i, c) && better(c, top)) top = c, mine = as_float(c.score);
+      if (entry(j, c) && better(c, top)) top = c, mine = as_float(c.score);
     }
     sm.tbest[tid] = mine;
     __syncthreads();
@@ -485,9 +501,11 @@ __global__ void __launch_bounds__(kThreads) beam_merge_kernel(
     }
     __syncthreads();
     const unsigned thr = sm.thr;
-    for (int i = tid; i < n; i += kThreads) {
+#pragma unroll
+    for (int j = 0; j < kHeld; ++j) {
+      if (j * kThreads >= n) break;
       Cand c;
-      if (!entry(i, c) || ordered(as_float(c.score)) < thr) continue;
+      if (!entry(j, c) || ordered(as_float(c.score)) < thr) continue;
       const int at = atomicAdd(&sm.nfew, 1);
       if (at < kFew) sm.few[at] = c;
     }
@@ -505,9 +523,11 @@ __global__ void __launch_bounds__(kThreads) beam_merge_kernel(
       if (rank == K1 - 1 && top.at != ~0ull) sm.best[0] = top;
       __syncthreads();
       const Cand bound = sm.best[0];
-      for (int i = tid; i < n; i += kThreads) {
+#pragma unroll
+      for (int j = 0; j < kHeld; ++j) {
+        if (j * kThreads >= n) break;
         Cand c;
-        if (entry(i, c) && !better(bound, c)) sm.few[atomicAdd(&sm.nfew, 1)] = c;
+        if (entry(j, c) && !better(bound, c)) sm.few[atomicAdd(&sm.nfew, 1)] = c;
       }
     }
     __syncthreads();
@@ -526,7 +546,7 @@ __global__ void __launch_bounds__(kThreads) beam_merge_kernel(
     for (int i = tid; i < K; i += kThreads) {
       const Cand a = sm.best[i], b = sm.best[i + 1];
       const uint32_t wa = static_cast<uint32_t>(a.at >> 32), wb = static_cast<uint32_t>(b.at >> 32);
-      if (b.at == ~0ull || wa == wb || a.score - b.score > kLseEps) continue;
+      if (b.at == ~0ull || wa == wb || a.score - b.score > eps) continue;
       sm.again = 1;
       if (sm.lse[wa] == sm.lse[wa]) sm.redo[wa] = 1;   // (a finished beam has no sum)
       if (sm.lse[wb] == sm.lse[wb]) sm.redo[wb] = 1;
@@ -549,10 +569,11 @@ __global__ void __launch_bounds__(kThreads) beam_merge_kernel(
   }
 }
 
-// Spans per row: about six CTAs for every SM, spans of at least two rounds of
+// Spans per row: three CTAs for every SM when the rows are fewer (512 rows of
+// 50257: 36 us in one span each, 43 us in two), spans of at least two rounds of
 // every warp, and no more list entries per request than one merge takes.
 int beam_splits(long long rows, int W, int V, int K) {
-  const long long want = (static_cast<long long>(num_sms()) * 6 + rows - 1) / rows;
+  const long long want = (static_cast<long long>(num_sms()) * 3 + rows - 1) / rows;
   const long long by_len = std::max(1, V / (2 * kThreads * kPer));
   const long long by_merge = std::max(1, kMergeMost / (W * K));
   return static_cast<int>(std::max(1LL, std::min({want, by_len, by_merge})));
@@ -583,8 +604,9 @@ cudaError_t run_select(int G, int W, int V, int K, const void* logits, const flo
   beam_scan_kernel<T><<<static_cast<unsigned>(rows * splits), kThreads, 0, st>>>(x, scores, fin, V, K, splits, keys, ms, sums);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
+  const double eps = 2.0 * (4.2e-7 + 9.3e-8 * std::log2(static_cast<double>(std::max(V, 8))));
   return launch_after(beam_merge_kernel<T>, static_cast<unsigned>(G), kThreads, 0, st, true, x, scores, fin, end_token, W, V, K,
-                      splits, keys, ms, sums, os, op, ot);
+                      splits, eps, keys, ms, sums, os, op, ot);
 }
 
 // ------------------------------------------------------------- state reorder
