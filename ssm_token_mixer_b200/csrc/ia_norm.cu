@@ -6,14 +6,26 @@
 //   dw = sum_rows dy xhat,  db = sum_rows dy
 //
 // Both directions touch every value once (2 and 3 row-sized streams), so HBM
-// bounds them.  A row is held in registers by a group of threads (a warp up to
-// 512 columns, else up to 512 threads), which makes the variance a second pass
-// over registers instead of a difference of large sums.  The backward pass
-// keeps a group's columns fixed while it walks rows, so dw and db accumulate
-// in registers in fp32; the groups of a block add theirs in shared memory, the
-// block writes one partial row, and a second kernel adds the blocks' rows in a
-// fixed order: no atomics, equal bits from equal calls.  Rows wider than the
-// registers hold (12288 columns) are read again from L2 instead.
+// bounds them.  A row is held in registers by a group of threads (a warp where
+// its registers suffice), which makes the variance a second pass over
+// registers instead of a difference of large sums.  The rows to come are on
+// their way meanwhile: every thread copies its own vectors of the next rows
+// into its own slots of shared memory (cp.async), two or three rows ahead, which
+// takes neither registers nor barriers.  One row ahead in registers kept 32 KB
+// per SM in flight, half of what HBM's latency asks for.
+//
+// Loads and stores are 16 bytes wide whatever the row length: a group takes
+// every TG-th row with TG a multiple of the values per vector, so all its rows
+// start at the same offset from a 16-byte boundary, and its vectors are laid
+// from that boundary; a copy stops at the row's end, and the vectors across a
+// row's ends are stored value by value.
+//
+// The backward pass keeps a thread's columns fixed while its group walks rows,
+// so dw and db accumulate in registers in fp32; the groups of a block add
+// theirs in shared memory, the block writes one partial row, and a second
+// kernel adds the blocks' rows in a fixed order: no atomics, equal bits from
+// equal calls.  Rows wider than the registers hold (12280 columns) are read
+// again from L2 instead.
 #include <algorithm>
 #include <cmath>
 #include <cstdint>
@@ -26,72 +38,124 @@
 namespace ia {
 namespace {
 
-constexpr int kMaxHeld = 12288;   // widest row held in registers
+constexpr int kMaxHeld = 12280;   // widest row held in registers (512 threads, 24 values, less what an offset takes)
 
-// V consecutive values as fp32.  V = 4 (or 1 for rows that do not start on a
-// 4-value boundary).
-template <typename T, int V>
-__device__ __forceinline__ void load_v(const T* p, float* f) {
-  if constexpr (V == 1) {
-    if constexpr (sizeof(T) == 2) f[0] = __bfloat162float(p[0]);
-    else f[0] = p[0];
-  } else if constexpr (sizeof(T) == 2) {
-    static_assert(V == 4 || V == 8, "");
-    uint32_t w[V / 2];
+__device__ __forceinline__ uint64_t f2_add(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t f2_twice(float x) { return f2_pack(x, x); }
+__device__ __forceinline__ float f2_sum(uint64_t v) {
+  float lo, hi;
+  f2_unpack(v, lo, hi);
+  return lo + hi;
+}
+
+// One value as fp32, and back.
+template <typename T>
+__device__ __forceinline__ float ld1(const T* p, long long i) {
+  if constexpr (sizeof(T) == 2) return __bfloat162float(p[i]);
+  else return p[i];
+}
+template <typename T>
+__device__ __forceinline__ void st1(T* p, long long i, float f) {
+  if constexpr (sizeof(T) == 2) p[i] = __float2bfloat16(f);
+  else p[i] = f;
+}
+
+// 16 bytes: V values of a row from column c on.
+template <typename T>
+struct Vec {
+  static constexpr int V = 16 / sizeof(T);
+  uint4 u;
+  // In flight to `slot` (own to the thread) until the copies' group is awaited.
+  // Values at and past D become zero; those before the row (c < 0) are the
+  // previous row's and are cleared by get().
+  static __device__ __forceinline__ void fetch(uint4* slot, const T* row, int c, int D) {
+    const int left = (D - c) * static_cast<int>(sizeof(T));
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(slot)), "l"(left > 0 ? row + c : row - c % V),
+                 "r"(left >= 16 ? 16 : left > 0 ? left : 0)
+                 : "memory");
+  }
+  template <bool ALIGNED>
+  __device__ __forceinline__ void store(T* row, int c, int D) const {
+    if (c >= 0 && c + V <= D) {
+      *reinterpret_cast<uint4*>(row + c) = u;
+    } else if (!ALIGNED) {
+      float f[V];
+      get(f);
+#pragma unroll
+      for (int e = 0; e < V; ++e)
+        if (c + e >= 0 && c + e < D) st1(row, c + e, f[e]);
+    }
+  }
+  __device__ __forceinline__ void get(float* f) const {
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
     if constexpr (V == 8) {
-      const uint4 u = *reinterpret_cast<const uint4*>(p);
-      w[0] = u.x, w[1] = u.y, w[2] = u.z, w[3] = u.w;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {   // a bf16 is the high half of an fp32
+        f[2 * i] = __uint_as_float(w[i] << 16);
+        f[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+      }
     } else {
-      const uint2 u = *reinterpret_cast<const uint2*>(p);
-      w[0] = u.x, w[1] = u.y;
-    }
 #pragma unroll
-    for (int i = 0; i < V / 2; ++i) {   // a bf16 is the high half of an fp32
-      f[2 * i] = __uint_as_float(w[i] << 16);
-      f[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-    }
-  } else {
-#pragma unroll
-    for (int i = 0; i < V; i += 4) {
-      const float4 u = *reinterpret_cast<const float4*>(p + i);
-      f[i] = u.x, f[i + 1] = u.y, f[i + 2] = u.z, f[i + 3] = u.w;
+      for (int i = 0; i < 4; ++i) f[i] = __uint_as_float(w[i]);
     }
   }
-}
-template <typename T, int V>
-__device__ __forceinline__ void store_v(T* p, const float* f) {
-  if constexpr (V == 1) {
-    if constexpr (sizeof(T) == 2) p[0] = __float2bfloat16(f[0]);
-    else p[0] = f[0];
-  } else if constexpr (sizeof(T) == 2) {
-    uint32_t w[V / 2];
+  // The row's values in pairs (the arithmetic is packed: with single
+  // instructions the backward pass of bf16 rows was bound by issue slots).
+  template <bool ALIGNED>
+  __device__ __forceinline__ void get_row(uint64_t* p, int c) const {
+    float f[V];
+    get(f);
+    if (!ALIGNED && c < 0)
 #pragma unroll
-    for (int i = 0; i < V / 2; ++i) {
-      const __nv_bfloat162 h = __floats2bfloat162_rn(f[2 * i], f[2 * i + 1]);
-      w[i] = *reinterpret_cast<const uint32_t*>(&h);
-    }
-    if constexpr (V == 8) *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
-    else *reinterpret_cast<uint2*>(p) = make_uint2(w[0], w[1]);
-  } else {
+      for (int e = 0; e < V; ++e)
+        if (c + e < 0) f[e] = 0.f;
 #pragma unroll
-    for (int i = 0; i < V; i += 4) *reinterpret_cast<float4*>(p + i) = make_float4(f[i], f[i + 1], f[i + 2], f[i + 3]);
+    for (int i = 0; i < V / 2; ++i) p[i] = f2_pack(f[2 * i], f[2 * i + 1]);
   }
-}
-
-__device__ __forceinline__ float warp_sum(float x) {
+  __device__ __forceinline__ void put_pairs(const uint64_t* p) {
+    float f[V];
 #pragma unroll
-  for (int o = 16; o; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
-  return x;
-}
+    for (int i = 0; i < V / 2; ++i) f2_unpack(p[i], f[2 * i], f[2 * i + 1]);
+    put(f);
+  }
+  __device__ __forceinline__ void put(const float* f) {
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if constexpr (V == 8) {
+        const __nv_bfloat162 h = __floats2bfloat162_rn(f[2 * i], f[2 * i + 1]);
+        w[i] = *reinterpret_cast<const uint32_t*>(&h);
+      } else {
+        w[i] = __float_as_uint(f[i]);
+      }
+    }
+    u = make_uint4(w[0], w[1], w[2], w[3]);
+  }
+};
 
-// Sums NV values over a group of tpr threads (a multiple of 32): shuffles, then
-// one word per warp in shared memory.  `slot` alternates between two buffers so
-// that one barrier per call is enough.
+// Rows of a thread in shared memory (the current one among them), by its
+// vectors per row: 64 to 130 KB per SM in flight.
+constexpr int fwd_depth(int nv) { return nv == 1 ? 4 : 3; }
+constexpr int bwd_depth(int nv2) { return nv2 <= 2 ? 6 : nv2 <= 4 ? 4 : nv2 <= 8 ? 3 : 2; }
+__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+// All but the newest N groups of the thread's copies have landed.
+template <int N>
+__device__ __forceinline__ void copies_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+
+// Sums NV values over a group of tpr threads (a power of two up to 32, or a
+// multiple of 32): shuffles, then one word per warp in shared memory.  `slot`
+// alternates between two buffers so that one barrier per call is enough.  All
+// lanes of a warp call it together.
 template <int NV>
 __device__ __forceinline__ void group_sum(float (&x)[NV], int tpr, int group, int gt, float* buf, int slot) {
+  for (int o = min(tpr, 32) >> 1; o; o >>= 1)
 #pragma unroll
-  for (int i = 0; i < NV; ++i) x[i] = warp_sum(x[i]);
-  if (tpr == 32) return;
+    for (int i = 0; i < NV; ++i) x[i] += __shfl_xor_sync(0xffffffffu, x[i], o);
+  if (tpr <= 32) return;
   float* b = buf + (group * 2 + slot) * 32 * NV;
   const int w = gt >> 5, nw = tpr >> 5;
   if ((gt & 31) == 0)
@@ -106,173 +170,256 @@ __device__ __forceinline__ void group_sum(float (&x)[NV], int tpr, int group, in
   }
 }
 
-// E values per thread in E / V vectors: vector j of thread t covers columns
-// (j * tpr + t) * V ...
-template <typename T, int E, int V>
-__global__ void __launch_bounds__(512) ln_fwd_kernel(long long rows, int D, int tpr, const T* x,
+// V parameters in pairs from column c on (`none` outside the row, and without a pointer).
+template <int V, bool ALIGNED>
+__device__ __forceinline__ void load_params(const float* __restrict__ p, int c, int D, float none, uint64_t* q) {
+  if (p && (ALIGNED ? c < D : (c % 4 == 0 && c >= 0 && c + V <= D))) {
+#pragma unroll
+    for (int e = 0; e < V; e += 4) {
+      const float4 u = __ldg(reinterpret_cast<const float4*>(p + c + e));
+      q[e / 2] = f2_pack(u.x, u.y), q[e / 2 + 1] = f2_pack(u.z, u.w);
+    }
+  } else if (ALIGNED || !p) {
+#pragma unroll
+    for (int i = 0; i < V / 2; ++i) q[i] = f2_twice(none);
+  } else {
+    float f[V];
+#pragma unroll
+    for (int e = 0; e < V; ++e) f[e] = c + e >= 0 && c + e < D ? __ldg(p + c + e) : none;
+#pragma unroll
+    for (int i = 0; i < V / 2; ++i) q[i] = f2_pack(f[2 * i], f[2 * i + 1]);
+  }
+}
+
+// Forward: most threads per block and blocks of 256 per SM, by values per
+// thread.  (Backward: one block of up to 512 threads per SM.)
+constexpr int fwd_threads(int E) { return E == 32 ? 384 : 256; }
+constexpr int fwd_ctas(int E) { return E == 8 ? 5 : E == 16 ? 3 : 2; }
+
+// NV vectors per thread: vector j of thread t covers the columns from
+// (j tpr + t) V - mis on, mis the group's offset from a 16-byte boundary.
+template <typename T, int NV, bool ALIGNED>
+__global__ void __launch_bounds__(fwd_threads(NV * Vec<T>::V), NV * Vec<T>::V == 32 ? 1 : fwd_ctas(NV * Vec<T>::V)) ln_fwd_kernel(long long rows, int D, int tpr, const T* x,
                                                      const float* __restrict__ w, const float* __restrict__ b, float eps,
                                                      T* y, float* __restrict__ mean_out, float* __restrict__ rstd_out) {
+  constexpr int V = Vec<T>::V, E = NV * V, kAhead = fwd_depth(NV);
   __shared__ float buf[16 * 2 * 32];
   const int group = threadIdx.x / tpr, gt = threadIdx.x - group * tpr, groups = blockDim.x / tpr;
   const float inv = 1.f / static_cast<float>(D);
-  int slot = 0;
-  for (long long row = static_cast<long long>(blockIdx.x) * groups + group; row < rows;
-       row += static_cast<long long>(gridDim.x) * groups) {
-    const T* xr = x + row * D;
-    float v[E];
-    float s[1] = {0.f};
+  const long long step = static_cast<long long>(gridDim.x) * groups;
+  long long row = static_cast<long long>(blockIdx.x) * groups + group;
+  const int mis = static_cast<int>(row * D % V);
+  int slot = 0, at = 0;
+  extern __shared__ uint4 ring[];   // [kAhead][NV][threads]
+  auto fetch = [&](long long r, int k) {
+    if (r < rows)
 #pragma unroll
-    for (int j = 0; j < E / V; ++j) {
-      const int c = (j * tpr + gt) * V;
-      if (c < D) load_v<T, V>(xr + c, v + j * V);
-      else
+      for (int j = 0; j < NV; ++j)
+        Vec<T>::fetch(ring + (k * NV + j) * blockDim.x + threadIdx.x, x + r * D, (j * tpr + gt) * V - mis, D);
+    copies_commit();
+  };
 #pragma unroll
-        for (int e = 0; e < V; ++e) v[j * V + e] = 0.f;
+  for (int k = 0; k < kAhead - 1; ++k) fetch(row + k * step, k);
+  const int sub = tpr < 32 ? group % (32 / tpr) : 0;   // rows of a warp's groups follow one another
+  for (; row - sub < rows; row += step) {
+    const bool in = row < rows;
+    fetch(row + (kAhead - 1) * step, at == 0 ? kAhead - 1 : at - 1);
+    copies_wait<kAhead - 1>();
+    uint64_t v[E / 2];
+    float s[1];
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      Vec<T> q;
+      q.u = ring[(at * NV + j) * blockDim.x + threadIdx.x];
+      q.template get_row<ALIGNED>(v + j * V / 2, (j * tpr + gt) * V - mis);
     }
+    at = at + 1 == kAhead ? 0 : at + 1;
+    uint64_t t = 0ull;
 #pragma unroll
-    for (int e = 0; e < E; ++e) s[0] += v[e];
+    for (int i = 0; i < E / 2; ++i) t = f2_add(t, v[i]);
+    s[0] = f2_sum(t);
     group_sum<1>(s, tpr, group, gt, buf, slot);
     slot ^= 1;
     const float mean = s[0] * inv;
-    s[0] = 0.f;
+    const uint64_t minus = f2_twice(-mean);
+    t = 0ull;
 #pragma unroll
-    for (int j = 0; j < E / V; ++j)
-      if ((j * tpr + gt) * V < D)
+    for (int j = 0; j < NV; ++j) {
+      const int c = (j * tpr + gt) * V - mis;
 #pragma unroll
-        for (int e = 0; e < V; ++e) {
-          const float d = v[j * V + e] - mean;
-          s[0] = fmaf(d, d, s[0]);
+      for (int i = 0; i < V / 2; ++i) v[j * V / 2 + i] = f2_add(v[j * V / 2 + i], minus);
+      if (!ALIGNED && (c < 0 || c + V > D)) {   // centred values outside the row do not count
+#pragma unroll
+        for (int i = 0; i < V / 2; ++i) {
+          float lo, hi;
+          f2_unpack(v[j * V / 2 + i], lo, hi);
+          const int k = c + 2 * i;
+          v[j * V / 2 + i] = f2_pack(k >= 0 && k < D ? lo : 0.f, k + 1 >= 0 && k + 1 < D ? hi : 0.f);
         }
+      }
+      if (c < D)
+#pragma unroll
+        for (int i = 0; i < V / 2; ++i) t = f2_fma(v[j * V / 2 + i], v[j * V / 2 + i], t);
+    }
+    s[0] = f2_sum(t);
     group_sum<1>(s, tpr, group, gt, buf, slot);
     slot ^= 1;
     const float rstd = 1.f / sqrtf(s[0] * inv + eps);
-    T* yr = y + row * D;
+    const uint64_t r2 = f2_twice(rstd);
 #pragma unroll
-    for (int j = 0; j < E / V; ++j) {
-      const int c = (j * tpr + gt) * V;
-      if (c < D) {
-        float wv[V], bv[V], r[V];
+    for (int j = 0; j < NV; ++j) {
+      const int c = (j * tpr + gt) * V - mis;
+      if (c >= D || !in) continue;
+      uint64_t wv[V / 2], bv[V / 2], r[V / 2];
+      load_params<V, ALIGNED>(w, c, D, 1.f, wv);
+      load_params<V, ALIGNED>(b, c, D, 0.f, bv);
 #pragma unroll
-        for (int e = 0; e < V; ++e) wv[e] = 1.f, bv[e] = 0.f;
-        if (w) load_v<float, V>(w + c, wv);
-        if (b) load_v<float, V>(b + c, bv);
-#pragma unroll
-        for (int e = 0; e < V; ++e) r[e] = fmaf((v[j * V + e] - mean) * rstd, wv[e], bv[e]);
-        store_v<T, V>(yr + c, r);
-      }
+      for (int i = 0; i < V / 2; ++i) r[i] = f2_fma(f2_mul(v[j * V / 2 + i], r2), wv[i], bv[i]);
+      Vec<T> out;
+      out.put_pairs(r);
+      out.template store<ALIGNED>(y + row * D, c, D);
     }
-    if (gt == 0) {
+    if (gt == 0 && in) {
       if (mean_out) mean_out[row] = mean;
       if (rstd_out) rstd_out[row] = rstd;
     }
   }
 }
 
-// part: [gridDim.x][2][D] partial sums of dw and db (null: neither is wanted)
-template <typename T, int E, int V>
-__global__ void __launch_bounds__(512) ln_bwd_kernel(long long rows, int D, int tpr, const T* dy, const T* x,
+// part: [gridDim.x][2][D] partial sums of dw and db (null: neither is wanted).
+// HOLD: the weights stay in registers too.
+template <typename T, int NV, bool HOLD, bool ALIGNED>
+__global__ void __launch_bounds__(512, 1) ln_bwd_kernel(long long rows, int D, int tpr, const T* dy, const T* x,
                                                      const float* __restrict__ w, const float* __restrict__ mean_in,
                                                      const float* __restrict__ rstd_in, T* dx, float* __restrict__ part) {
+  constexpr int V = Vec<T>::V, E = NV * V, kAhead = bwd_depth(2 * NV);
   __shared__ float buf[16 * 2 * 32 * 2];
-  extern __shared__ float acc_sm[];   // [2][D] when the block has several groups
   const int group = threadIdx.x / tpr, gt = threadIdx.x - group * tpr, groups = blockDim.x / tpr;
   const float inv = 1.f / static_cast<float>(D);
   griddep_launch_dependents();
-  float aw[E], ab[E];
+  const long long step = static_cast<long long>(gridDim.x) * groups;
+  long long row = static_cast<long long>(blockIdx.x) * groups + group;
+  const int mis = static_cast<int>(row * D % V);
+  uint64_t aw[E / 2], ab[E / 2], held[HOLD ? E / 2 : 1];
 #pragma unroll
-  for (int e = 0; e < E; ++e) aw[e] = ab[e] = 0.f;
-  int slot = 0;
-  for (long long row = static_cast<long long>(blockIdx.x) * groups + group; row < rows;
-       row += static_cast<long long>(gridDim.x) * groups) {
-    const T *xr = x + row * D, *dr = dy + row * D;
-    float hat[E], g[E];
+  for (int i = 0; i < E / 2; ++i) aw[i] = ab[i] = 0ull;
+  if (HOLD)
 #pragma unroll
-    for (int j = 0; j < E / V; ++j) {
-      const int c = (j * tpr + gt) * V;
-      if (c < D) {
-        load_v<T, V>(xr + c, hat + j * V);
-        load_v<T, V>(dr + c, g + j * V);
+    for (int j = 0; j < NV; ++j) load_params<V, ALIGNED>(w, (j * tpr + gt) * V - mis, D, 1.f, held + j * V / 2);
+  int slot = 0, at = 0;
+  extern __shared__ uint4 ring[];   // [kAhead][2 NV][threads]; at the end the groups' sums, [groups][2][D]
+  auto fetch = [&](long long r, int k) {
+    if (r < rows)
+#pragma unroll
+      for (int j = 0; j < NV; ++j) {
+        const int c = (j * tpr + gt) * V - mis;
+        uint4* q = ring + (k * 2 * NV + j) * blockDim.x + threadIdx.x;
+        Vec<T>::fetch(q, x + r * D, c, D);
+        Vec<T>::fetch(q + NV * blockDim.x, dy + r * D, c, D);
+      }
+    copies_commit();
+  };
+  float next_mean, next_rstd;   // a row ahead: their latency is an iteration's
+  auto statistics = [&](long long r) {
+    next_mean = r < rows ? mean_in[r] : 0.f;
+    next_rstd = r < rows ? rstd_in[r] : 0.f;
+  };
+  statistics(row);
+#pragma unroll
+  for (int k = 0; k < kAhead - 1; ++k) fetch(row + k * step, k);
+  const int sub = tpr < 32 ? group % (32 / tpr) : 0;   // rows of a warp's groups follow one another
+  for (; row - sub < rows; row += step) {
+    const bool in = row < rows;
+    const float mean = next_mean, rstd = next_rstd;
+    statistics(row + step);
+    fetch(row + (kAhead - 1) * step, at == 0 ? kAhead - 1 : at - 1);
+    copies_wait<kAhead - 1>();
+    uint64_t hat[E / 2], g[E / 2];
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      const int c = (j * tpr + gt) * V - mis;
+      const uint4* q = ring + (at * 2 * NV + j) * blockDim.x + threadIdx.x;
+      Vec<T> r;
+      r.u = in ? q[0] : make_uint4(0u, 0u, 0u, 0u);   // (a warp's last rows: this group has none, and adds nothing)
+      r.template get_row<ALIGNED>(hat + j * V / 2, c);
+      r.u = in ? q[NV * blockDim.x] : make_uint4(0u, 0u, 0u, 0u);
+      r.template get_row<ALIGNED>(g + j * V / 2, c);
+    }
+    at = at + 1 == kAhead ? 0 : at + 1;
+    const uint64_t minus = f2_twice(-mean), r2 = f2_twice(rstd);
+    uint64_t t0 = 0ull, t1 = 0ull;
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      uint64_t wv[V / 2];
+      if (!HOLD) load_params<V, ALIGNED>(w, (j * tpr + gt) * V - mis, D, 1.f, wv);
+#pragma unroll
+      for (int k = 0; k < V / 2; ++k) {   // outside the row g is 0 and adds nothing
+        const int i = j * V / 2 + k;
+        hat[i] = f2_mul(f2_add(hat[i], minus), r2);
+        aw[i] = f2_fma(g[i], hat[i], aw[i]);
+        ab[i] = f2_add(ab[i], g[i]);
+        g[i] = f2_mul(g[i], HOLD ? held[i] : wv[k]);
+        t0 = f2_add(t0, g[i]);
+        t1 = f2_fma(g[i], hat[i], t1);
       }
     }
-    const float mean = mean_in[row], rstd = rstd_in[row];
-    float s[2] = {0.f, 0.f};
-#pragma unroll
-    for (int j = 0; j < E / V; ++j) {
-      const int c = (j * tpr + gt) * V;
-      if (c < D) {
-        float wv[V];
-#pragma unroll
-        for (int e = 0; e < V; ++e) wv[e] = 1.f;
-        if (w) load_v<float, V>(w + c, wv);
-#pragma unroll
-        for (int e = 0; e < V; ++e) {
-          const int i = j * V + e;
-          hat[i] = (hat[i] - mean) * rstd;
-          aw[i] = fmaf(g[i], hat[i], aw[i]);
-          ab[i] += g[i];
-          g[i] *= wv[e];
-          s[0] += g[i];
-          s[1] = fmaf(g[i], hat[i], s[1]);
-        }
-      }
-    }
+    float s[2] = {f2_sum(t0), f2_sum(t1)};
     group_sum<2>(s, tpr, group, gt, buf, slot);
     slot ^= 1;
-    const float c1 = s[0] * inv, c2 = s[1] * inv;
-    T* xo = dx + row * D;
+    const uint64_t c1 = f2_twice(-s[0] * inv), c2 = f2_twice(-s[1] * inv);
 #pragma unroll
-    for (int j = 0; j < E / V; ++j) {
-      const int c = (j * tpr + gt) * V;
-      if (c < D) {
-        float r[V];
+    for (int j = 0; j < NV; ++j) {
+      const int c = (j * tpr + gt) * V - mis;
+      if (c >= D || !in) continue;
+      uint64_t r[V / 2];
 #pragma unroll
-        for (int e = 0; e < V; ++e) {
-          const int i = j * V + e;
-          r[e] = rstd * (g[i] - c1 - hat[i] * c2);
-        }
-        store_v<T, V>(xo + c, r);
+      for (int k = 0; k < V / 2; ++k) {
+        const int i = j * V / 2 + k;
+        r[k] = f2_mul(r2, f2_fma(hat[i], c2, f2_add(g[i], c1)));
       }
+      Vec<T> out;
+      out.put_pairs(r);
+      out.template store<ALIGNED>(dx + row * D, c, D);
     }
   }
   if (!part) return;
   float* out = part + static_cast<long long>(blockIdx.x) * 2 * D;
-  if (groups == 1) {
+  asm volatile("cp.async.wait_all;" ::: "memory");
+  if (groups > 1) __syncthreads();   // every thread is done with its slots
+  float* own = groups == 1 ? out : reinterpret_cast<float*>(ring) + group * 2 * D;   // this group's sums
 #pragma unroll
-    for (int j = 0; j < E / V; ++j) {
-      const int c = (j * tpr + gt) * V;
-      if (c < D) {
-        store_v<float, V>(out + c, aw + j * V);
-        store_v<float, V>(out + D + c, ab + j * V);
-      }
-    }
-    return;
-  }
-  for (int gr = 0; gr < groups; ++gr) {   // one group after the other: a fixed order
-    if (gr == group) {
+  for (int j = 0; j < NV; ++j) {
+    const int c = (j * tpr + gt) * V - mis;
 #pragma unroll
-      for (int j = 0; j < E / V; ++j) {
-        const int c = (j * tpr + gt) * V;
+    for (int k = 0; k < 2; ++k) {
+      const uint64_t* p = (k ? ab : aw) + j * V / 2;
+      float* q = own + k * D;
+      if (ALIGNED) {
         if (c < D)
 #pragma unroll
-          for (int e = 0; e < V; ++e) {
-            acc_sm[c + e] = (gr ? acc_sm[c + e] : 0.f) + aw[j * V + e];
-            acc_sm[D + c + e] = (gr ? acc_sm[D + c + e] : 0.f) + ab[j * V + e];
-          }
+          for (int i = 0; i < V / 2; i += 2) *reinterpret_cast<ulonglong2*>(q + c + 2 * i) = make_ulonglong2(p[i], p[i + 1]);
+      } else {
+#pragma unroll
+        for (int i = 0; i < V / 2; ++i) {
+          float lo, hi;
+          f2_unpack(p[i], lo, hi);
+          const int at2 = c + 2 * i;
+          if (at2 >= 0 && at2 < D) q[at2] = lo;
+          if (at2 + 1 >= 0 && at2 + 1 < D) q[at2 + 1] = hi;
+        }
       }
     }
-    __syncthreads();
   }
-  for (int c = threadIdx.x; c < 2 * D; c += blockDim.x) out[c] = acc_sm[c];
+  if (groups == 1) return;
+  __syncthreads();
+  for (int c = threadIdx.x; c < 2 * D; c += blockDim.x) {   // the groups in order
+    float t = 0.f;
+    for (int gr = 0; gr < groups; ++gr) t += reinterpret_cast<const float*>(ring)[gr * 2 * D + c];
+    out[c] = t;
+  }
 }
 
 // ---- rows too wide for registers: one block per row, values read again
-template <typename T>
-__device__ __forceinline__ float ld1(const T* p, long long i) {
-  float f;
-  load_v<T, 1>(p + i, &f);
-  return f;
-}
-
 template <typename T>
 __global__ void __launch_bounds__(512) ln_fwd_wide_kernel(long long rows, int D, const T* x, const float* w,
                                                           const float* b, float eps, T* y, float* mean_out,
@@ -296,7 +443,7 @@ __global__ void __launch_bounds__(512) ln_fwd_wide_kernel(long long rows, int D,
     const float rstd = 1.f / sqrtf(s[0] / D + eps);
     for (int c = threadIdx.x; c < D; c += 512) {
       const float r = fmaf((ld1(xr, c) - mean) * rstd, w ? w[c] : 1.f, b ? b[c] : 0.f);
-      store_v<T, 1>(y + row * D + c, &r);
+      st1(y, row * D + c, r);
     }
     if (threadIdx.x == 0) {
       if (mean_out) mean_out[row] = mean;
@@ -341,26 +488,33 @@ __global__ void __launch_bounds__(512) ln_bwd_wide_kernel(long long rows, int D,
     for (int c = threadIdx.x; c < D; c += 512) {
       const float g = ld1(dr, c) * (w ? w[c] : 1.f);
       const float r = rstd * (g - c1 - (ld1(xr, c) - mean) * rstd * c2);
-      store_v<T, 1>(dx + row * D + c, &r);
+      st1(dx, row * D + c, r);
     }
   }
 }
 
-// dw[c], db[c] = sums of the partial rows: 32 columns x 8 row lanes per block,
-// the lanes' sums added in order.
-__global__ void __launch_bounds__(256) ln_reduce_kernel(int D, int nparts, const float* __restrict__ part,
-                                                        float* __restrict__ dw, float* __restrict__ db) {
-  __shared__ float sm[8][33];
+// dw[c], db[c] = sums of the partial rows: 32 columns x 32 row lanes per block,
+// a lane's loads in flight together, the lanes' sums added in order.
+__global__ void __launch_bounds__(1024) ln_reduce_kernel(int D, int nparts, const float* __restrict__ part,
+                                                         float* __restrict__ dw, float* __restrict__ db) {
+  __shared__ float sm[32][33];
   griddep_wait();
   const int c = blockIdx.x * 32 + (threadIdx.x & 31), r = threadIdx.x >> 5;   // columns of [2 D]
   float t = 0.f;
   if (c < 2 * D)
-    for (int i = r; i < nparts; i += 8) t += part[static_cast<long long>(i) * 2 * D + c];
+#pragma unroll 1
+    for (int i = r; i < nparts; i += 256) {
+      float v[8];
+#pragma unroll
+      for (int k = 0; k < 8; ++k) v[k] = i + 32 * k < nparts ? part[static_cast<long long>(i + 32 * k) * 2 * D + c] : 0.f;
+#pragma unroll
+      for (int k = 0; k < 8; ++k) t += v[k];
+    }
   sm[r][threadIdx.x & 31] = t;
   __syncthreads();
   if (r == 0 && c < 2 * D) {
 #pragma unroll
-    for (int i = 1; i < 8; ++i) t += sm[i][threadIdx.x & 31];
+    for (int i = 1; i < 32; ++i) t += sm[i][threadIdx.x & 31];
     if (c < D) {
       if (dw) dw[c] = t;
     } else if (db) {
@@ -370,40 +524,50 @@ __global__ void __launch_bounds__(256) ln_reduce_kernel(int D, int nparts, const
 }
 
 struct LnPlan {
-  int E, V, tpr, groups;
+  int nv, tpr, groups;
+  long long blocks;
 };
 
-// Vectors of 4 (8 for bf16) values where the row length keeps every row on a
-// 16-byte boundary, else single values; a warp per row up to 512 columns, then
-// as many threads as 8, 16 or 24 values each need.
-LnPlan ln_plan(int D, bool bf16) {
+int slots(int D, int V) { return D % V ? D + V - 1 : D; }   // values from the first vector's start to the row's end, at most
+
+// Threads per row for E values each: a multiple of 32, or a part of a warp;
+// blocks of up to `most` threads, as many as are resident; TG, the number of
+// groups, a multiple of the values per vector.
+LnPlan plan_rows(long long rows, int D, int V, int E, int most, long long most_blocks) {
   LnPlan p;
-  const int wide = bf16 ? 8 : 4;
-  p.V = D % wide == 0 ? wide : 1;
-  p.E = D <= 4096 ? 8 : D <= 8192 ? 16 : 24;
-  if (D <= 512) {
-    p.tpr = 32;
-    p.E = D <= 256 ? 8 : 16;
-  } else {
-    p.tpr = ((D + p.E - 1) / p.E + 31) / 32 * 32;
-  }
-  p.groups = p.tpr == 32 ? 8 : std::max(1, 512 / p.tpr);
+  p.nv = E / V;
+  const int need = (slots(D, V) + E - 1) / E;
+  p.tpr = 8;
+  while (p.tpr < 32 && p.tpr < need) p.tpr *= 2;
+  if (need > 32) p.tpr = (need + 31) / 32 * 32;
+  p.groups = std::max(1, std::min(most, 16 * 32) / p.tpr);
+  int unit = V;   // blocks that make groups * blocks a multiple of V
+  for (int g = p.groups; unit > 1 && g % 2 == 0; g /= 2) unit /= 2;
+  p.blocks = std::min((rows + p.groups - 1) / p.groups, most_blocks);
+  p.blocks = (p.blocks + unit - 1) / unit * unit;
   return p;
 }
 
-template <typename T, int V, typename F>
-cudaError_t by_e(int E, F f) {
-  switch (E) {
-    case 8: return f(std::integral_constant<int, 8>(), std::integral_constant<int, V>());
-    case 16: return f(std::integral_constant<int, 16>(), std::integral_constant<int, V>());
-    default: return f(std::integral_constant<int, 24>(), std::integral_constant<int, V>());
-  }
+// Values per thread.  Forward: 8 to 32, part of a warp per row up to 128
+// columns and one warp up to 1024.  Backward (four accumulators and copies per
+// value): 8 or 16, 24 for the rows that 512 threads do not hold with 16.
+LnPlan fwd_plan(long long rows, int D, int V) {
+  const int n = slots(D, V), E = n <= 256 ? 8 : n <= 4096 ? 16 : 32;
+  const int most = n <= 8192 ? 256 : 384;
+  return plan_rows(rows, D, V, E, most, (most == 384 ? 1LL : fwd_ctas(E)) * num_sms());
 }
+LnPlan bwd_plan(long long rows, int D, int V) {
+  const int n = slots(D, V), E = n <= 256 ? 8 : n <= 8192 ? 16 : 24;
+  return plan_rows(rows, D, V, E, 512, num_sms());
+}
+
 template <typename T, typename F>
-cudaError_t by_plan(const LnPlan& p, F f) {
-  if (p.V == 1) return by_e<T, 1>(p.E, f);
-  if constexpr (sizeof(T) == 2) return by_e<T, 8>(p.E, f);
-  else return by_e<T, 4>(p.E, f);
+cudaError_t by_values(int nv, F f) {
+  constexpr int k = 8 / Vec<T>::V;   // vectors of 8 values
+  if (nv == k) return f(std::integral_constant<int, k>());
+  if (nv == 2 * k) return f(std::integral_constant<int, 2 * k>());
+  if (nv == 3 * k) return f(std::integral_constant<int, 3 * k>());
+  return f(std::integral_constant<int, 4 * k>());
 }
 
 template <typename T>
@@ -411,26 +575,26 @@ cudaError_t ln_fwd(long long rows, int D, const void* x, const float* w, const f
                    float* rstd, cudaStream_t st) {
   const T* xt = static_cast<const T*>(x);
   T* yt = static_cast<T*>(y);
-  const long long sms = num_sms();
   if (D > kMaxHeld) {
-    ln_fwd_wide_kernel<T><<<static_cast<unsigned>(std::min(rows, 4 * sms)), 512, 0, st>>>(rows, D, xt, w, b, eps, yt, mean, rstd);
+    const long long blocks = std::min<long long>(rows, 4LL * num_sms());
+    ln_fwd_wide_kernel<T><<<static_cast<unsigned>(blocks), 512, 0, st>>>(rows, D, xt, w, b, eps, yt, mean, rstd);
     return cudaGetLastError();
   }
-  const LnPlan p = ln_plan(D, sizeof(T) == 2);
-  const int threads = p.tpr * p.groups;
-  const long long blocks = std::min((rows + p.groups - 1) / p.groups, sms * (2048 / threads));
-  return by_plan<T>(p, [&](auto e, auto v) {
-    ln_fwd_kernel<T, e(), v()><<<static_cast<unsigned>(blocks), threads, 0, st>>>(rows, D, p.tpr, xt, w, b, eps, yt, mean, rstd);
+  const LnPlan p = fwd_plan(rows, D, Vec<T>::V);
+  return by_values<T>(p.nv, [&](auto nv) {
+    constexpr int n = nv() * Vec<T>::V == 24 ? 1 : nv();   // (24 values are not used here)
+    auto kern = D % Vec<T>::V == 0 ? ln_fwd_kernel<T, n, true> : ln_fwd_kernel<T, n, false>;
+    const int threads = p.tpr * p.groups, sm = fwd_depth(n) * n * threads * 16;
+    if (cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, sm); e != cudaSuccess) return e;
+    kern<<<static_cast<unsigned>(p.blocks), threads, sm, st>>>(rows, D, p.tpr, xt, w, b, eps, yt, mean, rstd);
     return cudaGetLastError();
   });
 }
 
-// Blocks of the backward pass, and so partial rows of dw and db: two per SM.
+// Blocks of the backward pass, and so partial rows of dw and db.
 long long bwd_blocks(long long rows, int D, bool bf16) {
-  const long long most = 2LL * num_sms();
-  if (D > kMaxHeld) return std::min(rows, most);
-  const LnPlan p = ln_plan(D, bf16);
-  return std::min((rows + p.groups - 1) / p.groups, most);
+  if (D > kMaxHeld) return std::min<long long>(rows, 2LL * num_sms());
+  return bwd_plan(rows, D, bf16 ? 8 : 4).blocks;
 }
 
 template <typename T>
@@ -450,18 +614,22 @@ cudaError_t ln_bwd(long long rows, int D, const void* dy, const void* x, const f
         rows, D, dt, xt, w, mean, rstd, ot);
     e = cudaGetLastError();
   } else {
-    const LnPlan p = ln_plan(D, sizeof(T) == 2);
+    const LnPlan p = bwd_plan(rows, D, Vec<T>::V);
     const int threads = p.tpr * p.groups;
-    const size_t sm = part && p.groups > 1 ? 2 * sizeof(float) * D : 0;
-    e = by_plan<T>(p, [&](auto ee, auto v) {
-      ln_bwd_kernel<T, ee(), v()><<<static_cast<unsigned>(blocks), threads, sm, st>>>(rows, D, p.tpr, dt, xt, w, mean,
-                                                                                      rstd, ot, part);
+    e = by_values<T>(p.nv, [&](auto nv) {
+      constexpr bool hold = nv() * Vec<T>::V <= 16;
+      constexpr int n = nv() * Vec<T>::V <= 24 ? nv() : 1;   // (32 values are not used here)
+      auto kern = D % Vec<T>::V == 0 ? ln_bwd_kernel<T, n, hold, true> : ln_bwd_kernel<T, n, hold, false>;
+      // (the groups' sums fit in the ring: 8 D bytes a group, D <= nv V tpr, against 32 nv bytes a thread and row of it)
+      const int sm = bwd_depth(2 * n) * 2 * n * threads * 16;
+      if (cudaError_t e2 = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, sm); e2 != cudaSuccess) return e2;
+      kern<<<static_cast<unsigned>(blocks), threads, sm, st>>>(rows, D, p.tpr, dt, xt, w, mean, rstd, ot, part);
       return cudaGetLastError();
     });
   }
   if (e != cudaSuccess || !part) return e;
   // (the wide form's last kernel does not write the partial rows: no overlap there)
-  return launch_after(ln_reduce_kernel, (2 * D + 31) / 32, 256, 0, st, D <= kMaxHeld, D, static_cast<int>(blocks), part, dw, db);
+  return launch_after(ln_reduce_kernel, (2 * D + 31) / 32, 1024, 0, st, D <= kMaxHeld, D, static_cast<int>(blocks), part, dw, db);
 }
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
