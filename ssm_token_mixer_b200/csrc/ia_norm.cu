@@ -193,13 +193,13 @@ __device__ __forceinline__ void load_params(const float* __restrict__ p, int c, 
 
 // Forward: most threads per block and blocks of 256 per SM, by values per
 // thread.  (Backward: one block of up to 512 threads per SM.)
-constexpr int fwd_threads(int E) { return E == 32 ? 384 : 256; }
-constexpr int fwd_ctas(int E) { return E == 8 ? 5 : E == 16 ? 3 : 2; }
+constexpr int fwd_ctas(int E) { return E == 8 ? 4 : E == 16 ? 3 : 1; }
 
 // NV vectors per thread: vector j of thread t covers the columns from
 // (j tpr + t) V - mis on, mis the group's offset from a 16-byte boundary.
-template <typename T, int NV, bool ALIGNED>
-__global__ void __launch_bounds__(fwd_threads(NV * Vec<T>::V), NV * Vec<T>::V == 32 ? 1 : fwd_ctas(NV * Vec<T>::V)) ln_fwd_kernel(long long rows, int D, int tpr, const T* x,
+// HOLD: weights and biases stay in registers.
+template <typename T, int NV, bool HOLD, bool ALIGNED>
+__global__ void __launch_bounds__(HOLD ? 256 : 512, HOLD ? fwd_ctas(NV * Vec<T>::V) : 1) ln_fwd_kernel(long long rows, int D, int tpr, const T* x,
                                                      const float* __restrict__ w, const float* __restrict__ b, float eps,
                                                      T* y, float* __restrict__ mean_out, float* __restrict__ rstd_out) {
   constexpr int V = Vec<T>::V, E = NV * V, kAhead = fwd_depth(NV);
@@ -220,6 +220,13 @@ __global__ void __launch_bounds__(fwd_threads(NV * Vec<T>::V), NV * Vec<T>::V ==
   };
 #pragma unroll
   for (int k = 0; k < kAhead - 1; ++k) fetch(row + k * step, k);
+  uint64_t held_w[HOLD ? E / 2 : 1], held_b[HOLD ? E / 2 : 1];
+  if (HOLD)
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      load_params<V, ALIGNED>(w, (j * tpr + gt) * V - mis, D, 1.f, held_w + j * V / 2);
+      load_params<V, ALIGNED>(b, (j * tpr + gt) * V - mis, D, 0.f, held_b + j * V / 2);
+    }
   const int sub = tpr < 32 ? group % (32 / tpr) : 0;   // rows of a warp's groups follow one another
   for (; row - sub < rows; row += step) {
     const bool in = row < rows;
@@ -271,10 +278,15 @@ __global__ void __launch_bounds__(fwd_threads(NV * Vec<T>::V), NV * Vec<T>::V ==
       const int c = (j * tpr + gt) * V - mis;
       if (c >= D || !in) continue;
       uint64_t wv[V / 2], bv[V / 2], r[V / 2];
-      load_params<V, ALIGNED>(w, c, D, 1.f, wv);
-      load_params<V, ALIGNED>(b, c, D, 0.f, bv);
+      if (!HOLD) {
+        load_params<V, ALIGNED>(w, c, D, 1.f, wv);
+        load_params<V, ALIGNED>(b, c, D, 0.f, bv);
+      }
 #pragma unroll
-      for (int i = 0; i < V / 2; ++i) r[i] = f2_fma(f2_mul(v[j * V / 2 + i], r2), wv[i], bv[i]);
+      for (int i = 0; i < V / 2; ++i) {
+        const int k = j * V / 2 + i;
+        r[i] = f2_fma(f2_mul(v[k], r2), HOLD ? held_w[k] : wv[i], HOLD ? held_b[k] : bv[i]);
+      }
       Vec<T> out;
       out.put_pairs(r);
       out.template store<ALIGNED>(y + row * D, c, D);
@@ -541,20 +553,18 @@ LnPlan plan_rows(long long rows, int D, int V, int E, int most, long long most_b
   while (p.tpr < 32 && p.tpr < need) p.tpr *= 2;
   if (need > 32) p.tpr = (need + 31) / 32 * 32;
   p.groups = std::max(1, std::min(most, 16 * 32) / p.tpr);
-  int unit = V;   // blocks that make groups * blocks a multiple of V
+  int unit = D % V ? V : 1;   // blocks that make groups * blocks a multiple of V (for rows that need it)
   for (int g = p.groups; unit > 1 && g % 2 == 0; g /= 2) unit /= 2;
   p.blocks = std::min((rows + p.groups - 1) / p.groups, most_blocks);
-  p.blocks = (p.blocks + unit - 1) / unit * unit;
+  p.blocks = std::max(1LL, p.blocks / unit) * unit;   // down, to stay resident together
   return p;
 }
 
-// Values per thread.  Forward: 8 to 32, part of a warp per row up to 128
-// columns and one warp up to 1024.  Backward (four accumulators and copies per
-// value): 8 or 16, 24 for the rows that 512 threads do not hold with 16.
+// Values per thread: 8 or 16, part of a warp per row up to 128 columns and one
+// warp up to 512; 24 for the rows that 512 threads do not hold with 16.
 LnPlan fwd_plan(long long rows, int D, int V) {
-  const int n = slots(D, V), E = n <= 256 ? 8 : n <= 4096 ? 16 : 32;
-  const int most = n <= 8192 ? 256 : 384;
-  return plan_rows(rows, D, V, E, most, (most == 384 ? 1LL : fwd_ctas(E)) * num_sms());
+  const int n = slots(D, V), E = n <= 256 ? 8 : n <= 4096 ? 16 : 24;
+  return plan_rows(rows, D, V, E, E == 24 ? 512 : 256, static_cast<long long>(fwd_ctas(E)) * num_sms());
 }
 LnPlan bwd_plan(long long rows, int D, int V) {
   const int n = slots(D, V), E = n <= 256 ? 8 : n <= 8192 ? 16 : 24;
@@ -566,8 +576,7 @@ cudaError_t by_values(int nv, F f) {
   constexpr int k = 8 / Vec<T>::V;   // vectors of 8 values
   if (nv == k) return f(std::integral_constant<int, k>());
   if (nv == 2 * k) return f(std::integral_constant<int, 2 * k>());
-  if (nv == 3 * k) return f(std::integral_constant<int, 3 * k>());
-  return f(std::integral_constant<int, 4 * k>());
+  return f(std::integral_constant<int, 3 * k>());
 }
 
 template <typename T>
@@ -582,8 +591,9 @@ cudaError_t ln_fwd(long long rows, int D, const void* x, const float* w, const f
   }
   const LnPlan p = fwd_plan(rows, D, Vec<T>::V);
   return by_values<T>(p.nv, [&](auto nv) {
-    constexpr int n = nv() * Vec<T>::V == 24 ? 1 : nv();   // (24 values are not used here)
-    auto kern = D % Vec<T>::V == 0 ? ln_fwd_kernel<T, n, true> : ln_fwd_kernel<T, n, false>;
+    constexpr bool hold = nv() * Vec<T>::V <= 16;
+    constexpr int n = nv();
+    auto kern = D % Vec<T>::V == 0 ? ln_fwd_kernel<T, n, hold, true> : ln_fwd_kernel<T, n, hold, false>;
     const int threads = p.tpr * p.groups, sm = fwd_depth(n) * n * threads * 16;
     if (cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, sm); e != cudaSuccess) return e;
     kern<<<static_cast<unsigned>(p.blocks), threads, sm, st>>>(rows, D, p.tpr, xt, w, b, eps, yt, mean, rstd);
@@ -618,7 +628,7 @@ cudaError_t ln_bwd(long long rows, int D, const void* dy, const void* x, const f
     const int threads = p.tpr * p.groups;
     e = by_values<T>(p.nv, [&](auto nv) {
       constexpr bool hold = nv() * Vec<T>::V <= 16;
-      constexpr int n = nv() * Vec<T>::V <= 24 ? nv() : 1;   // (32 values are not used here)
+      constexpr int n = nv();
       auto kern = D % Vec<T>::V == 0 ? ln_bwd_kernel<T, n, hold, true> : ln_bwd_kernel<T, n, hold, false>;
       // (the groups' sums fit in the ring: 8 D bytes a group, D <= nv V tpr, against 32 nv bytes a thread and row of it)
       const int sm = bwd_depth(2 * n) * 2 * n * threads * 16;
