@@ -18,6 +18,7 @@ Entry points (same names as the C-ABI):
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 
@@ -591,33 +592,19 @@ def _place(*named):
     return idx if idx >= 0 else _cuda_device(named).index
 
 
-class _On:
-    """Makes a call's device and stream current while outputs and scratch are
-    allocated and the kernels are launched, so that a tensor of another device
-    than the current one works and memory allocated for another stream belongs
-    to that stream's pool.  Gives the stream's handle."""
+_CURRENT = contextlib.nullcontext()
 
-    def __init__(self, idx, stream):
-        self.ctx = None
-        if stream is not None:
-            if stream.device_index != idx:
-                raise ValueError(f"stream is on cuda:{stream.device_index}, the tensors on cuda:{idx}")
-            self.ctx = torch.cuda.stream(stream)   # makes its device current too
-            self.raw = stream.cuda_stream
-        else:
-            if idx != torch.cuda.current_device():
-                self.ctx = torch.cuda.device(idx)
-            self.raw = torch.cuda.current_stream(idx).cuda_stream
 
-    def __enter__(self):
-        if self.ctx is not None:
-            self.ctx.__enter__()
-        return self.raw
-
-    def __exit__(self, *exc):
-        if self.ctx is not None:
-            self.ctx.__exit__(*exc)
-        return False
+def _on(idx, stream):
+    """(context, stream handle) of a call on device idx: inside the context the call's device and stream are current
+    while outputs and scratch are allocated and the kernels are launched, so that tensors of another device than the
+    current one work and memory allocated for another stream belongs to that stream's pool."""
+    if stream is not None:
+        if stream.device_index != idx:
+            raise ValueError(f"stream is on cuda:{stream.device_index}, the tensors on cuda:{idx}")
+        return torch.cuda.stream(stream), stream.cuda_stream   # makes its device current too
+    raw = torch._C._cuda_getCurrentRawStream(idx)
+    return (_CURRENT if idx == torch.cuda.current_device() else torch.cuda.device(idx)), raw
 
 
 def _linear_shape(B, H, N, d_k, d_v, dtype) -> IALinearShape:
@@ -705,10 +692,11 @@ def linear_prefill_fwd(q, k, v, log_decay, scale=None, state_in=None, want_state
     dev = _place(("q", q), ("k", k), ("v", v), ("log_decay", log_decay), ("state_in", state_in), ("o", o),
                         ("workspace", workspace))
     ref = ctypes.byref(shp)
-    with _On(dev, stream) as raw:
+    ctx, raw = _on(dev, stream)
+    with ctx:
         if o is None:
-            o = torch.empty(v.shape, dtype=q.dtype, device=dev)
-        st = torch.empty(n_state, dtype=torch.float32, device=dev) if want_state else None
+            o = torch.empty_like(v)
+        st = log_decay.new_empty(n_state) if want_state else None
         ws, wp, wb = _scratch(lib.ia_linear_prefill_workspace_bytes(ref), dev, workspace)
         rc = lib.ia_linear_prefill_fwd(ref, _ad(q), _ad(k), _ad(v), _ad(log_decay),
                                        shp.d_k ** -0.5 if scale is None else scale, _ad(state_in), _ad(o),
@@ -727,9 +715,9 @@ def linear_fwd_bwd(q, k, v, log_decay, dO, scale=None, workspace=None, stream=No
         _need("workspace", workspace)
     dev = _place(("q", q), ("k", k), ("v", v), ("log_decay", log_decay), ("dO", dO), ("workspace", workspace))
     ref = ctypes.byref(shp)
-    with _On(dev, stream) as raw:
-        o, dv = (torch.empty(v.shape, dtype=q.dtype, device=dev) for _ in range(2))
-        dq, dk = (torch.empty(q.shape, dtype=q.dtype, device=dev) for _ in range(2))
+    ctx, raw = _on(dev, stream)
+    with ctx:
+        o, dv, dq, dk = torch.empty_like(v), torch.empty_like(v), torch.empty_like(q), torch.empty_like(q)
         ws, wp, wb = _scratch(lib.ia_linear_fwd_bwd_workspace_bytes(ref), dev, workspace)
         rc = lib.ia_linear_fwd_bwd(ref, _ad(q), _ad(k), _ad(v), _ad(log_decay),
                                    shp.d_k ** -0.5 if scale is None else scale, _ad(dO), _ad(o), _ad(dq),
@@ -763,9 +751,10 @@ def linear_decode_step(q, k, v, log_decay, state, scale=None, state_out=None, pa
     dev = _place(("q", q), ("k", k), ("v", v), ("log_decay", log_decay), ("state", state),
                         ("state_out", state_out), ("parents", parents), ("o", o))
     out = state if state_out is None else state_out
-    with _On(dev, stream) as raw:
+    ctx, raw = _on(dev, stream)
+    with ctx:
         if o is None:
-            o = torch.empty(v.shape, dtype=q.dtype, device=dev)
+            o = torch.empty_like(v)
         rc = lib.ia_linear_decode_step(ctypes.byref(shp), _ad(q), _ad(k), _ad(v), _ad(log_decay),
                                        shp.d_k ** -0.5 if scale is None else scale, _ad(state), _ad(parents),
                                        beams, _ad(out), _ad(o), raw)
@@ -777,11 +766,13 @@ def _check_rows(x, weight, bias=None):
     _need("x", x)
     if x.dim() < 1 or x.numel() == 0:
         raise ValueError(f"x must be [..., D] and not empty, got shape {tuple(x.shape)}")
-    D = x.shape[-1]
+    size = x.shape[-1:]
+    D = size[0]
     _small("x", D)
-    for name, t in (("weight", weight), ("bias", bias)):
-        if t is not None:
-            _need(name, t, (D,), torch.float32)
+    if weight is not None and not _ok(weight, size, torch.float32):
+        _need("weight", weight, (D,), torch.float32)
+    if bias is not None and not _ok(bias, size, torch.float32):
+        _need("bias", bias, (D,), torch.float32)
     return x.numel() // D, D, _dtype_code(x)
 
 
@@ -793,11 +784,12 @@ def layer_norm_fwd(x, weight=None, bias=None, eps=1e-5, y=None, stream=None):
     if y is not None:
         _need("y", y, x.shape, x.dtype)
     dev = _place(("x", x), ("weight", weight), ("bias", bias), ("y", y))
-    with _On(dev, stream) as raw:
+    ctx, raw = _on(dev, stream)
+    with ctx:
         if y is None:
-            y = torch.empty(x.shape, dtype=x.dtype, device=dev)
-        mean = torch.empty(x.shape[:-1], dtype=torch.float32, device=dev)
-        rstd = torch.empty(x.shape[:-1], dtype=torch.float32, device=dev)
+            y = torch.empty_like(x)
+        mean = x.new_empty(x.shape[:-1], dtype=torch.float32)
+        rstd = torch.empty_like(mean)
         rc = lib.ia_layer_norm_fwd(rows, D, code, _ad(x), _ad(weight), _ad(bias), eps, _ad(y), _ad(mean),
                                    _ad(rstd), raw)
     _check(rc, "ia_layer_norm_fwd")
@@ -823,14 +815,15 @@ def layer_norm_bwd(dy, x, mean, rstd, weight=None, want_params=True, dx=None, wo
         _need("workspace", workspace)
     dev = _place(("x", x), ("dy", dy), ("mean", mean), ("rstd", rstd), ("weight", weight), ("dx", dx),
                         ("workspace", workspace))
-    with _On(dev, stream) as raw:
+    ctx, raw = _on(dev, stream)
+    with ctx:
         if dx is None:
-            dx = torch.empty(x.shape, dtype=x.dtype, device=dev)
+            dx = torch.empty_like(x)
         dw = db = ws = wp = None
         wb = 0
         if want_params:
-            dw = torch.empty(D, dtype=torch.float32, device=dev)
-            db = torch.empty(D, dtype=torch.float32, device=dev)
+            dw = x.new_empty(D, dtype=torch.float32)
+            db = torch.empty_like(dw)
             ws, wp, wb = _scratch(lib.ia_layer_norm_bwd_workspace_bytes(rows, D, code), dev, workspace)
         rc = lib.ia_layer_norm_bwd(rows, D, code, _ad(dy), _ad(x), _ad(weight), _ad(mean), _ad(rstd), _ad(dx),
                                    _ad(dw), _ad(db), wp, wb, raw)
@@ -863,10 +856,11 @@ def beam_select(logits, scores, K, finished=None, end_token=0, workspace=None, s
     if workspace is not None:
         _need("workspace", workspace)
     dev = _place(("logits", logits), ("scores", scores), ("finished", finished), ("workspace", workspace))
-    with _On(dev, stream) as raw:
-        out = torch.empty(G, K, dtype=torch.float32, device=dev)
-        parents = torch.empty(G, K, dtype=torch.int32, device=dev)
-        tokens = torch.empty(G, K, dtype=torch.int32, device=dev)
+    ctx, raw = _on(dev, stream)
+    with ctx:
+        out = scores.new_empty((G, K))
+        parents = scores.new_empty((G, K), dtype=torch.int32)
+        tokens = torch.empty_like(parents)
         ws, wp, wb = _scratch(lib.ia_beam_select_workspace_bytes(G, W, V, K, code), dev, workspace)
         rc = lib.ia_beam_select(G, W, V, K, code, _ad(logits), _ad(scores), _ad(finished), int(end_token), _ad(out),
                                 _ad(parents), _ad(tokens), wp, wb, raw)
@@ -883,9 +877,10 @@ def _reorder(call, where, shp, per, B, state, parents, out, stream):
     if out is not None:
         _need("out", out, dtype=torch.float32, numel=per * G * wout)
     dev = _place(("state", state), ("parents", parents), ("out", out))
-    with _On(dev, stream) as raw:
+    ctx, raw = _on(dev, stream)
+    with ctx:
         if out is None:
-            out = torch.empty(per * G * wout, dtype=torch.float32, device=dev)
+            out = state.new_empty(per * G * wout)
         rc = call(ctypes.byref(shp), B // G, wout, _ad(parents), _ad(state), _ad(out), raw)
     _check(rc, where)
     return out

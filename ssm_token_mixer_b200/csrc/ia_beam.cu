@@ -705,8 +705,7 @@ cudaError_t run_reorder(const Parts& p, long long groups, int win, int wout, con
   if (p.in[0] == p.out[0]) {
     const size_t bytes = sizeof(float) * 128 * width * win;
     auto kern = vec ? reorder_in_place_kernel<4> : reorder_in_place_kernel<1>;
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(bytes));
-    if (e != cudaSuccess) return e;
+    if (cudaError_t e = allow_smem(kern, bytes); e != cudaSuccess) return e;
     const long long bx = std::max(1LL, std::min((longest + 128 * width - 1) / (128 * width), (16LL * num_sms() + groups - 1) / groups));
     kern<<<dim3(static_cast<unsigned>(groups), static_cast<unsigned>(bx)), 128, bytes, st>>>(p, win, parents);
   } else {

@@ -8,6 +8,14 @@
 
 namespace ia {
 
+// Leave for `bytes` of dynamic shared memory.  Every kernel may use 48 KB, the
+// static part (16 KB at most here) included.
+template <typename K>
+cudaError_t allow_smem(K kern, size_t bytes) {
+  if (bytes <= 32 * 1024) return cudaSuccess;
+  return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(bytes));
+}
+
 template <typename... P, typename... A>
 cudaError_t launch_after(void (*kern)(P...), dim3 grid, dim3 block, size_t smem, cudaStream_t st, bool overlap, A... args) {
   cudaLaunchConfig_t cfg = {};

@@ -313,8 +313,7 @@ cudaError_t simt_launch(const LinArgs& a, int max_dx, bool state_only, cudaStrea
   const long long grid = static_cast<long long>(a.BH) * a.first[a.nprob] * (state_only ? a.nseg - 1 : a.nseg);
   if (grid > (1LL << 31) - 1) return cudaErrorInvalidConfiguration;
   auto kern = state_only ? lin_simt_kernel<BF16, true> : lin_simt_kernel<BF16, false>;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(bytes));
-  if (e != cudaSuccess) return e;
+  if (cudaError_t e = allow_smem(kern, bytes); e != cudaSuccess) return e;
   return launch_after(kern, static_cast<unsigned>(grid), kThreads, bytes, st, a.nseg > 1 && !state_only, a);
 }
 

@@ -595,7 +595,7 @@ cudaError_t ln_fwd(long long rows, int D, const void* x, const float* w, const f
     constexpr int n = nv();
     auto kern = D % Vec<T>::V == 0 ? ln_fwd_kernel<T, n, hold, true> : ln_fwd_kernel<T, n, hold, false>;
     const int threads = p.tpr * p.groups, sm = fwd_depth(n) * n * threads * 16;
-    if (cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, sm); e != cudaSuccess) return e;
+    if (cudaError_t e = allow_smem(kern, sm); e != cudaSuccess) return e;
     kern<<<static_cast<unsigned>(p.blocks), threads, sm, st>>>(rows, D, p.tpr, xt, w, b, eps, yt, mean, rstd);
     return cudaGetLastError();
   });
@@ -632,7 +632,7 @@ cudaError_t ln_bwd(long long rows, int D, const void* dy, const void* x, const f
       auto kern = D % Vec<T>::V == 0 ? ln_bwd_kernel<T, n, hold, true> : ln_bwd_kernel<T, n, hold, false>;
       // (the groups' sums fit in the ring: 8 D bytes a group, D <= nv V tpr, against 32 nv bytes a thread and row of it)
       const int sm = bwd_depth(2 * n) * 2 * n * threads * 16;
-      if (cudaError_t e2 = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, sm); e2 != cudaSuccess) return e2;
+      if (cudaError_t e2 = allow_smem(kern, sm); e2 != cudaSuccess) return e2;
       kern<<<static_cast<unsigned>(blocks), threads, sm, st>>>(rows, D, p.tpr, dt, xt, w, mean, rstd, ot, part);
       return cudaGetLastError();
     });
