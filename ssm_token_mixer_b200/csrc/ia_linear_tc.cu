@@ -71,6 +71,9 @@ struct Cfg {
   // d = 64: 126 us without, 118 us with); with one buffer it would hold up the
   // state instead (d = 128: 140 us without, 150 us with).
   static constexpr bool kSplit = NZ == 2;
+  // Every problem has dx = 64, and K 64 rows: a third less of shared memory is
+  // read for G4 than with 128 rows of which half mean nothing.
+  static constexpr bool kHalf = MAXDX == 64;
   static constexpr int TX = MAXDX / 64 * kBox;
   static constexpr int S_Z = NS * 2 * TX;
   static constexpr int S_ZW = S_Z + NT * kBox;          // each: hi, lo
@@ -134,6 +137,7 @@ __global__ void __launch_bounds__(512, 1) lin_tc_kernel(const __grid_constant__ 
                                                         const __grid_constant__ Maps maps) {
   using K = Cfg<MAXDX>;
   constexpr int NS = K::NS, NT = K::NT;
+  constexpr bool kZFreeUsed = K::NZ == 1 || STATE_ONLY;
   extern __shared__ uint8_t raw[];
   uint8_t* smem = raw + ((1024u - (smem_u32(raw) & 1023u)) & 1023u);
   const LinArgs& a = prm.a;
@@ -202,7 +206,9 @@ __global__ void __launch_bounds__(512, 1) lin_tc_kernel(const __grid_constant__ 
     const int L = min(C, a.N - chunk_at(c) * C);
     uint8_t* zw = smem + K::S_ZW + (c % K::NZ) * 2 * kBox;
     const uint8_t* zs = smem + sZ(c);
-    if (c >= K::NZ && !warp_wait(kZFree + c % K::NZ, c / K::NZ - 1)) return false;   // G4 has read the buffer
+    // G4 has read the buffer (with two of them and outputs to write, the role
+    // has already waited for a product issued after the G4 two chunks back)
+    if (kZFreeUsed && c >= K::NZ && !warp_wait(kZFree + c % K::NZ, c / K::NZ - 1)) return false;
     if (!warp_wait(kFullZ + c % NT, c / NT)) return false;
     const __nv_bfloat162 zero = __float2bfloat162_rn(0.f);
     __nv_bfloat162 probe = zero;   // 0 * z: NaN if any z is not finite
@@ -361,26 +367,31 @@ __global__ void __launch_bounds__(512, 1) lin_tc_kernel(const __grid_constant__ 
     if (u == 0) bulk_wait_all();
   } else if (warp < 12) {
     // ------------------------------------------------------------------- S
+    // The accumulator K of dx = 64 has M = 64 rows, in lanes 0-15 of each warp's
+    // quadrant: a lane takes half a row.  Else thread u takes row u.
+    constexpr int kCols = K::kHalf ? 32 : 64;
     const int u = tid - 2 * kRoleThreads;
-    const bool holds = u < dx;   // thread u carries row u of S
+    const int row = K::kHalf ? 16 * (warp - 8) + (lane & 15) : u, col = K::kHalf ? 32 * (lane >> 4) : 0;
+    const bool holds = row < dx;
     const long long per_state = static_cast<long long>(dx) * dz;
-    uint64_t S[32];              // its 64 columns in pairs
+    const long long at_state = static_cast<long long>(row) * dz + z0 + col;
+    uint64_t S[kCols / 2];       // its columns in pairs
     const float dec_full = expm1f(g * C);
     {
       const float* s0 = seg == 0 ? (pr.state_in ? pr.state_in + bh * per_state : nullptr)
                                  : STATE_ONLY ? nullptr : pr.seg + (static_cast<long long>(bh) * (a.nseg - 1) + seg - 1) * per_state;
 #pragma unroll
-      for (int i = 0; i < 16; ++i) {
+      for (int i = 0; i < kCols / 4; ++i) {
         float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (s0 && holds) v = *reinterpret_cast<const float4*>(s0 + static_cast<long long>(u) * dz + z0 + 4 * i);
+        if (s0 && holds) v = *reinterpret_cast<const float4*>(s0 + at_state + 4 * i);
         S[2 * i] = f2_pack(v.x, v.y), S[2 * i + 1] = f2_pack(v.z, v.w);
       }
     }
     auto write_operand = [&]() {   // and K has been read: the next G4 may overwrite it
       if (!STATE_ONLY && holds)
 #pragma unroll
-        for (int j = 0; j < 8; ++j)
-          *reinterpret_cast<uint4*>(smem + K::S_SB + u * 128 + ((j ^ (u & 7)) << 4)) =
+        for (int j = 0; j < kCols / 8; ++j)
+          *reinterpret_cast<uint4*>(smem + K::S_SB + row * 128 + (((col / 8 + j) ^ (row & 7)) << 4)) =
               make_uint4(pack2(S[4 * j]), pack2(S[4 * j + 1]), pack2(S[4 * j + 2]), pack2(S[4 * j + 3]));
       fence_async_smem();
       __syncwarp();
@@ -397,22 +408,35 @@ __global__ void __launch_bounds__(512, 1) lin_tc_kernel(const __grid_constant__ 
       const uint64_t dec2 = f2_pack(dec, dec);
       if (!warp_wait(kKFull, c)) break;
       tc_fence_after();
-      if (32 * (warp - 8) < dx) {
-        const uint32_t tk = tmem + (static_cast<uint32_t>(warp - 8) << 21) + kTK;
+      const uint32_t tk = tmem + (static_cast<uint32_t>(warp - 8) << 21) + kTK;
+      auto add = [&](int i, const uint32_t (&v)[16], const uint32_t (&w)[16]) {   // columns 16 i ..: both parts of w z
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
+        for (int k = 0; k < 8; ++k) {
+          const uint64_t hi = f2_pack(__uint_as_float(v[2 * k]), __uint_as_float(v[2 * k + 1]));
+          const uint64_t lo = f2_pack(__uint_as_float(w[2 * k]), __uint_as_float(w[2 * k + 1]));
+          uint64_t& S2 = S[8 * i + k];
+          S2 = f2_add(f2_fma(dec2, S2, S2), f2_add(hi, lo));
+        }
+      };
+      if (K::kHalf) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
           uint32_t v[16], w[16];
-          tmem_ld16(tk + 16 * q, v);
-          tmem_ld16(tk + 64 + 16 * q, w);
+          tmem_ld16_halves<32>(tk + 16 * i, v);
+          tmem_ld16_halves<32>(tk + 64 + 16 * i, w);
           tmem_ld_wait16(v);
           tmem_ld_wait16(w);
+          add(i, v, w);
+        }
+      } else if (32 * (warp - 8) < dx) {
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const uint64_t hi = f2_pack(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1]));
-            const uint64_t lo = f2_pack(__uint_as_float(w[2 * i]), __uint_as_float(w[2 * i + 1]));
-            uint64_t& S2 = S[8 * q + i];
-            S2 = f2_add(f2_fma(dec2, S2, S2), f2_add(hi, lo));
-          }
+        for (int i = 0; i < kCols / 16; ++i) {
+          uint32_t v[16], w[16];
+          tmem_ld16(tk + 16 * i, v);
+          tmem_ld16(tk + 64 + 16 * i, w);
+          tmem_ld_wait16(v);
+          tmem_ld_wait16(w);
+          add(i, v, w);
         }
       }
       tc_fence_before();
@@ -425,11 +449,11 @@ __global__ void __launch_bounds__(512, 1) lin_tc_kernel(const __grid_constant__ 
                             : (pr.state_out && seg == a.nseg - 1) ? pr.state_out + bh * per_state : nullptr;
     if (dst && holds)
 #pragma unroll
-      for (int i = 0; i < 16; ++i) {
+      for (int i = 0; i < kCols / 4; ++i) {
         float4 v;
         f2_unpack(S[2 * i], v.x, v.y);
         f2_unpack(S[2 * i + 1], v.z, v.w);
-        *reinterpret_cast<float4*>(dst + static_cast<long long>(u) * dz + z0 + 4 * i) = v;
+        *reinterpret_cast<float4*>(dst + at_state + 4 * i) = v;
       }
   } else if (warp == 12) {
     // ---------------------------------------------------------------- loads
@@ -495,15 +519,15 @@ __global__ void __launch_bounds__(512, 1) lin_tc_kernel(const __grid_constant__ 
         mma_commit(bars + kFreeX + c % NS);
       };
       auto g4 = [&](int c) {
-        // rows of K past dx (a second 64-row block when dx = 64) are taken from
-        // the next tile of the stage and never read
+        // (beside wider problems, the rows of K past dx = 64 are taken from the
+        // next tile in shared memory and never read)
         const int zb = c % K::NZ;
         const uint64_t y = mnmajor(sY(c)), zw = mnmajor(K::S_ZW + zb * 2 * kBox);
 #pragma unroll 4
         for (int kk = 0; kk < 8; ++kk)
-          mma_f16(tmem + kTK, y + kk * kTok, zw + kk * kTok, idesc_bf16(128, 128, 1, 1), kk > 0);
+          mma_f16(tmem + kTK, y + kk * kTok, zw + kk * kTok, idesc_bf16(K::kHalf ? 64 : 128, 128, 1, 1), kk > 0);
         mma_commit(bars + kKFull);
-        mma_commit(bars + kZFree + zb);
+        if (kZFreeUsed) mma_commit(bars + kZFree + zb);
         mma_commit(bars + kFreeY + c % NS);   // G1 of this chunk came before
         if (STATE_ONLY) mma_commit(bars + kFreeZ + c % NT);
       };
