@@ -57,13 +57,15 @@ constexpr int kBox = C * 128;           // 64 bf16 columns x 128 tokens, 128-byt
 constexpr int kRoleThreads = 128;
 constexpr int kThreads = 3 * kRoleThreads + 64;
 constexpr uint32_t kAtom = 1024;        // 8 rows of 128 bytes
+constexpr int kTries = 1 << 18;         // of a bounded wait
 
 // TMEM columns
 constexpr uint32_t kTA = 0, kTO1 = 256, kTO2 = 320, kTK = 384;
 
 template <int MAXDX>
 struct Cfg {
-  static constexpr int NS = 2;                          // stages of X and Y
+  static constexpr int NX = MAXDX == 64 ? 3 : 2;        // stages of X, released late (by G3)
+  static constexpr int NY = 2;                          // and of Y, released by G4
   static constexpr int NT = MAXDX == 64 ? 3 : 2;        // stages of Z, needed first and released last
   static constexpr int NZ = MAXDX == 64 ? 2 : 1;        // buffers of w z
   // Who weighs z.  With two buffers the state's warps take half of it off the
@@ -75,18 +77,19 @@ struct Cfg {
   // read for G4 than with 128 rows of which half mean nothing.
   static constexpr bool kHalf = MAXDX == 64;
   static constexpr int TX = MAXDX / 64 * kBox;
-  static constexpr int S_Z = NS * 2 * TX;
+  static constexpr int S_Y = NX * TX;
+  static constexpr int S_Z = S_Y + NY * TX;
   static constexpr int S_ZW = S_Z + NT * kBox;          // each: hi, lo
   static constexpr int S_SB = S_ZW + NZ * 2 * kBox;     // [dx][64] bf16, 128-byte swizzled
   static constexpr int S_OUT = S_SB + MAXDX * 128;
   static constexpr int S_BAR = S_OUT + kBox;
-  static constexpr int S_POW = S_BAR + 256;             // lambda^n, n = 0 .. C - 1
+  static constexpr int S_POW = S_BAR + 272;             // lambda^n, n = 0 .. C - 1
   static constexpr int SMEM = S_POW + C * 4 + 1024;     // + alignment of the base
 };
 
 enum Bar {
-  kFullXY = 0, kFullZ = 2, kFreeX = 5, kFreeY = 7, kFreeZ = 9, kAFull = 12, kPReady = 14, kZReady = 16, kZFree = 18,
-  kSReady = 20, kSFree, kKFull, kOFull, kOFree, kDrain, kBars
+  kFullX = 0, kFullY = 3, kFullZ = 5, kFreeX = 8, kFreeY = 11, kFreeZ = 13, kAFull = 16, kPReady = 18, kZReady = 20,
+  kZFree = 22, kSReady = 24, kSFree, kKFull, kOFull, kOFree, kDrain, kBars
 };
 
 struct Maps {
@@ -127,6 +130,36 @@ __device__ __forceinline__ bool elect_one() {
   return p != 0;
 }
 
+// The products and commits of the MMA warp: its lanes run the same code, so that
+// descriptors and addresses stay in uniform registers, and `lead` lets one
+// lane issue.
+__device__ __forceinline__ void mma_ss(bool lead, uint32_t d, uint64_t adesc, uint64_t bdesc, uint32_t idesc, uint32_t acc) {
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "setp.ne.b32 q, %5, 0;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(acc), "r"(static_cast<uint32_t>(lead))
+      : "memory");
+}
+__device__ __forceinline__ void mma_ts(bool lead, uint32_t d, uint32_t a, uint64_t bdesc, uint32_t idesc, uint32_t acc) {
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "setp.ne.b32 q, %5, 0;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+      "r"(a), "l"(bdesc), "r"(idesc), "r"(acc), "r"(static_cast<uint32_t>(lead))
+      : "memory");
+}
+__device__ __forceinline__ void commit_to(bool lead, uint64_t* bar) {
+  asm volatile(
+      "{\n\t.reg .pred q;\n\t"
+      "setp.ne.b32 q, %1, 0;\n\t"
+      "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(smem_u32(bar)),
+      "r"(static_cast<uint32_t>(lead))
+      : "memory");
+}
+
 // kind::f16 instruction descriptor with bf16 A and B, fp32 D.
 __host__ __device__ constexpr uint32_t idesc_bf16(int M, int N, int a_mn, int b_mn) {
   return idesc_f16(M, N, a_mn, b_mn) | (1u << 7) | (1u << 10);
@@ -136,7 +169,7 @@ template <int MAXDX, bool STATE_ONLY>
 __global__ void __launch_bounds__(512, 1) lin_tc_kernel(const __grid_constant__ TcParams prm,
                                                         const __grid_constant__ Maps maps) {
   using K = Cfg<MAXDX>;
-  constexpr int NS = K::NS, NT = K::NT;
+  constexpr int NX = K::NX, NY = K::NY, NT = K::NT;
   constexpr bool kZFreeUsed = K::NZ == 1 || STATE_ONLY;
   extern __shared__ uint8_t raw[];
   uint8_t* smem = raw + ((1024u - (smem_u32(raw) & 1023u)) & 1023u);
@@ -164,10 +197,10 @@ __global__ void __launch_bounds__(512, 1) lin_tc_kernel(const __grid_constant__ 
   uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(smem + K::S_BAR + 8 * kBars);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + K::S_BAR + 8 * kBars + 4);
   int* bad = reinterpret_cast<int*>(smem + K::S_BAR + 8 * kBars + 8);   // [4]
-  static_assert(8 * kBars + 24 <= 256, "barriers and flags fit their slot");
+  static_assert(8 * kBars + 24 <= 272, "barriers and flags fit their slot");
   const uint32_t sbase = smem_u32(smem);
-  auto sX = [&](int c) { return (c % NS) * 2 * K::TX; };
-  auto sY = [&](int c) { return (c % NS) * 2 * K::TX + K::TX; };
+  auto sX = [&](int c) { return (c % NX) * K::TX; };
+  auto sY = [&](int c) { return K::S_Y + (c % NY) * K::TX; };
   auto sZ = [&](int c) { return K::S_Z + (c % NT) * kBox; };
 
   if (warp == 0) {
@@ -195,7 +228,20 @@ __global__ void __launch_bounds__(512, 1) lin_tc_kernel(const __grid_constant__ 
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_holder;
-  auto wait = [&](int bar, uint32_t parity) { return mbar_wait_or_abort(bars + bar, parity & 1u, a.err, abort_flag); };
+  // Each try sleeps in hardware until the phase completes or some microseconds
+  // have passed; kTries of them are a second or so.  (The library's wait reads
+  // the clock instead; its code, inlined at 25 places, was a third of this
+  // kernel's 44 KB, which the instruction caches do not hold.)
+  auto wait = [&](int bar, uint32_t parity) {
+#pragma unroll 1
+    for (int i = 0; i < kTries; ++i) {
+      if (mbar_test(bars + bar, parity & 1u)) return true;
+      if (*abort_flag) return false;
+    }
+    atomicOr(a.err, kErrTimeout);
+    *abort_flag = 1;
+    return false;
+  };
   // one outcome for a warp: what follows is warp-wide
   auto warp_wait = [&](int bar, uint32_t parity) { return __all_sync(0xffffffffu, wait(bar, parity)) != 0; };
 
@@ -397,12 +443,10 @@ __global__ void __launch_bounds__(512, 1) lin_tc_kernel(const __grid_constant__ 
       __syncwarp();
       if (lane == 0) mbar_arrive(bars + kSReady);
     };
-    write_operand();
-
+    int weighed = 0;
 #pragma unroll 1
     for (int c = -1; c < n; ++c) {
-      if (K::kSplit && c + 1 < n && !weigh(c + 1, 1, u)) break;
-      if (c < 0) continue;
+      if (c >= 0) {
       const int L = min(C, a.N - chunk_at(c) * C);
       const float dec = L == C || rev ? dec_full : expm1f(g * L);
       const uint64_t dec2 = f2_pack(dec, dec);
@@ -440,9 +484,16 @@ __global__ void __launch_bounds__(512, 1) lin_tc_kernel(const __grid_constant__ 
         }
       }
       tc_fence_before();
+      }
       if (c + 1 < n) {
-        if (!STATE_ONLY && !warp_wait(kSFree, c)) break;   // G3 has read the old operand
+        if (!STATE_ONLY && c >= 0 && !warp_wait(kSFree, c)) break;   // G3 has read the old operand
         write_operand();
+      }
+      if (K::kSplit) {   // two chunks ahead of the state
+        bool ok = true;
+#pragma unroll 1
+        for (; ok && weighed < min(n, c + 3); ++weighed) ok = weigh(weighed, 1, u);
+        if (!ok) break;
       }
     }
     float* dst = STATE_ONLY ? pr.seg + (static_cast<long long>(bh) * (a.nseg - 1) + seg) * per_state
@@ -460,37 +511,38 @@ __global__ void __launch_bounds__(512, 1) lin_tc_kernel(const __grid_constant__ 
     if (elect_one()) {
       const CUtensorMap *mx = &maps.m[prm.mi[pi].x], *my = &maps.m[prm.mi[pi].y], *mz = &maps.m[prm.mi[pi].z];
       int issued_z = 0, issued_y = 0, issued_x = 0;
+      auto fetch = [&](int bar, int dst, const CUtensorMap* m, int boxes, int col, int t0) {
+        mbar_arrive_expect_tx(bars + bar, boxes * kBox);
+#pragma unroll 1
+        for (int x = 0; x < boxes; ++x) tma_load_3d(sbase + dst + x * kBox, m, col + 64 * x, t0, bh, bars + bar);
+      };
 #pragma unroll 1
       for (int c = 0; c < n; ++c) {
         const int t0 = chunk_at(c) * C;
         if (c >= NT && !wait(kFreeZ + c % NT, c / NT - 1)) break;
-        mbar_arrive_expect_tx(bars + kFullZ + c % NT, kBox);
-        tma_load_3d(sbase + sZ(c), mz, z0, t0, bh, bars + kFullZ + c % NT);
+        fetch(kFullZ + c % NT, sZ(c), mz, 1, z0, t0);
         issued_z = c + 1;
-        uint64_t* full = bars + kFullXY + c % NS;
-        if (c >= NS && !wait(kFreeY + c % NS, c / NS - 1)) break;
-        mbar_arrive_expect_tx(full, (STATE_ONLY ? 1 : 2) * nbx * kBox);
-        for (int x = 0; x < nbx; ++x) tma_load_3d(sbase + sY(c) + x * kBox, my, 64 * x, t0, bh, full);
+        if (c >= NY && !wait(kFreeY + c % NY, c / NY - 1)) break;
+        fetch(kFullY + c % NY, sY(c), my, nbx, 0, t0);
         issued_y = c + 1;
-        if (!STATE_ONLY) {
-          if (c >= NS && !wait(kFreeX + c % NS, c / NS - 1)) break;
-          for (int x = 0; x < nbx; ++x) tma_load_3d(sbase + sX(c) + x * kBox, mx, 64 * x, t0, bh, full);
-        }
+        if (STATE_ONLY) continue;
+        if (c >= NX && !wait(kFreeX + c % NX, c / NX - 1)) break;
+        fetch(kFullX + c % NX, sX(c), mx, nbx, 0, t0);
         issued_x = c + 1;
       }
       // no copy lands after the block exits
+#pragma unroll 1
       for (int c = max(0, issued_z - NT); c < issued_z; ++c) mbar_wait(bars + kFullZ + c % NT, (c / NT) & 1, a.err);
-      for (int c = max(0, issued_y - NS); c < issued_x; ++c) mbar_wait(bars + kFullXY + c % NS, (c / NS) & 1, a.err);
-      if (issued_x < issued_y) {
-        // aborted between Y and X of a chunk: its barrier cannot complete; its Y gets a millisecond to land
-        const unsigned long long t = global_ns();
-        while (global_ns() - t < 1000000ull) __nanosleep(1000);
-      }
+#pragma unroll 1
+      for (int c = max(0, issued_y - NY); c < issued_y; ++c) mbar_wait(bars + kFullY + c % NY, (c / NY) & 1, a.err);
+#pragma unroll 1
+      for (int c = max(0, issued_x - NX); c < issued_x; ++c) mbar_wait(bars + kFullX + c % NX, (c / NX) & 1, a.err);
     }
     __syncwarp();
   } else {
     // ------------------------------------------------------------------ MMA
-    if (elect_one()) {
+    {
+      const bool lead = elect_one();
       bool issued = false;
       // descriptors of a stage's tiles: K-major for G1 and G3's X, MN-major
       // (the token index contracted) for G2 and G4
@@ -504,9 +556,9 @@ __global__ void __launch_bounds__(512, 1) lin_tc_kernel(const __grid_constant__ 
 #pragma unroll
           for (int kk = 0; kk < 4; ++kk) {
             const uint64_t step = (b * kBox + kk * 32) >> 4;
-            mma_f16(tmem + kTA + 128 * (c & 1), x + step, y + step, idesc_bf16(128, 128, 0, 0), b + kk > 0);
+            mma_ss(lead, tmem + kTA + 128 * (c & 1), x + step, y + step, idesc_bf16(128, 128, 0, 0), b + kk > 0);
           }
-        mma_commit(bars + kAFull + (c & 1));
+        commit_to(lead, bars + kAFull + (c & 1));
       };
       auto g3 = [&](int c) {
         const uint64_t x = kmajor(sX(c)), sb = mnmajor(K::S_SB);
@@ -514,9 +566,9 @@ __global__ void __launch_bounds__(512, 1) lin_tc_kernel(const __grid_constant__ 
         for (int b = 0; b < nbx; ++b)
 #pragma unroll
           for (int kk = 0; kk < 4; ++kk)
-            mma_f16(tmem + kTO1, x + ((b * kBox + kk * 32) >> 4), sb + (4 * b + kk) * kTok, idesc_bf16(128, 64, 0, 1), b + kk > 0);
-        mma_commit(bars + kSFree);
-        mma_commit(bars + kFreeX + c % NS);
+            mma_ss(lead, tmem + kTO1, x + ((b * kBox + kk * 32) >> 4), sb + (4 * b + kk) * kTok, idesc_bf16(128, 64, 0, 1), b + kk > 0);
+        commit_to(lead, bars + kSFree);
+        commit_to(lead, bars + kFreeX + c % NX);
       };
       auto g4 = [&](int c) {
         // (beside wider problems, the rows of K past dx = 64 are taken from the
@@ -525,23 +577,23 @@ __global__ void __launch_bounds__(512, 1) lin_tc_kernel(const __grid_constant__ 
         const uint64_t y = mnmajor(sY(c)), zw = mnmajor(K::S_ZW + zb * 2 * kBox);
 #pragma unroll 4
         for (int kk = 0; kk < 8; ++kk)
-          mma_f16(tmem + kTK, y + kk * kTok, zw + kk * kTok, idesc_bf16(K::kHalf ? 64 : 128, 128, 1, 1), kk > 0);
-        mma_commit(bars + kKFull);
-        if (kZFreeUsed) mma_commit(bars + kZFree + zb);
-        mma_commit(bars + kFreeY + c % NS);   // G1 of this chunk came before
-        if (STATE_ONLY) mma_commit(bars + kFreeZ + c % NT);
+          mma_ss(lead, tmem + kTK, y + kk * kTok, zw + kk * kTok, idesc_bf16(K::kHalf ? 64 : 128, 128, 1, 1), kk > 0);
+        commit_to(lead, bars + kKFull);
+        if (kZFreeUsed) commit_to(lead, bars + kZFree + zb);
+        commit_to(lead, bars + kFreeY + c % NY);   // G1 of this chunk came before
+        if (STATE_ONLY) commit_to(lead, bars + kFreeZ + c % NT);
       };
       auto g2 = [&](int c) {
         const uint64_t z = mnmajor(sZ(c));
 #pragma unroll 4
         for (int kk = 0; kk < 8; ++kk)
-          mma_f16_ts(tmem + kTO2, tmem + kTA + 128 * (c & 1) + 8 * kk, z + kk * kTok, idesc_bf16(128, 64, 0, 1), kk > 0);
-        mma_commit(bars + kOFull);
-        mma_commit(bars + kFreeZ + c % NT);
+          mma_ts(lead, tmem + kTO2, tmem + kTA + 128 * (c & 1) + 8 * kk, z + kk * kTok, idesc_bf16(128, 64, 0, 1), kk > 0);
+        commit_to(lead, bars + kOFull);
+        commit_to(lead, bars + kFreeZ + c % NT);
       };
       bool ok = true;
       if (!STATE_ONLY) {
-        ok = wait(kFullXY, 0);
+        ok = warp_wait(kFullX, 0) && warp_wait(kFullY, 0);
         if (ok) {
           tc_fence_after();
           g1(0);
@@ -551,26 +603,27 @@ __global__ void __launch_bounds__(512, 1) lin_tc_kernel(const __grid_constant__ 
 #pragma unroll 1
       for (int c = 0; ok && c < n; ++c) {
         // K is free once the state has taken it (which also made S's operand)
-        if (!wait(kSReady, c) || !wait(kFullXY + c % NS, c / NS) || !wait(kZReady + c % K::NZ, c / K::NZ)) break;
+        if (!warp_wait(kSReady, c) || !warp_wait(kZReady + c % K::NZ, c / K::NZ)) break;
+        if (STATE_ONLY && !warp_wait(kFullY + c % NY, c / NY)) break;   // (else G1 has waited for Y)
         tc_fence_after();
         g4(c);
         issued = true;
         if (!STATE_ONLY) {
           if (c + 1 < n) {
-            if (!wait(kFullXY + (c + 1) % NS, (c + 1) / NS)) break;
+            if (!warp_wait(kFullX + (c + 1) % NX, (c + 1) / NX) || !warp_wait(kFullY + (c + 1) % NY, (c + 1) / NY)) break;
             tc_fence_after();
             g1(c + 1);
           }
-          if (c > 0 && !wait(kOFree, c - 1)) break;
+          if (c > 0 && !warp_wait(kOFree, c - 1)) break;
           tc_fence_after();
           g3(c);
-          if (!wait(kPReady + (c & 1), c >> 1)) break;
+          if (!warp_wait(kPReady + (c & 1), c >> 1)) break;
           tc_fence_after();
           g2(c);
         }
       }
       if (issued) {   // every product is done before TMEM and shared memory go
-        mma_commit(bars + kDrain);
+        commit_to(lead, bars + kDrain);
         mbar_wait(bars + kDrain, 0, a.err);
       }
     }
