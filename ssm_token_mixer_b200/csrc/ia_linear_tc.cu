@@ -18,17 +18,18 @@
 // carried and returned keeps fp32-like accuracy.  P and the S operand are
 // rounded to bf16 once, like the output.
 //
-// Roles (448 threads, four warps at most per register file: 128 registers):
+// Roles (448 threads, four warps at most per register file: 128 registers; or
+// 576, five warps: 96):
 //   warps 0-3   P: A from TMEM, decayed, back to TMEM as the A operand of G2.
 //               lambda^(t-s) = lambda^(t - e) lambda^(e - s) over groups of 32
 //               columns that end at e <= t: both factors <= 1 and constant per
 //               thread.  Groups on the other side of the diagonal are zero and
 //               not read.
-//   warps 4-7   O: w z of the next chunk for G4; then O1, O2 from TMEM, out
-//               through shared memory and a TMA store
+//   warps 4-7   O: O1, O2 from TMEM, out through shared memory and a TMA store
 //   warps 8-11  S: K from TMEM, S in registers, S in bf16 to shared memory for
-//               the next chunk's G3; half of w z when there are two buffers
-//   warp 12     TMA loads        warp 13   issues G1-G4
+//               the next chunk's G3
+//   warps 12-15 W: w z for G4 (where there are none, O does it)
+//   then a warp for the TMA loads and one that issues G1-G4
 // Per chunk G4, G1 of the next chunk, G3 and G2 are issued in this order, so
 // that P and the state work while the products of the other roles run.  The
 // loops of the roles are kept short on purpose: with everything unrolled the
@@ -55,7 +56,10 @@ namespace {
 constexpr int C = kLinTcChunk;
 constexpr int kBox = C * 128;           // 64 bf16 columns x 128 tokens, 128-byte swizzled: 16 KB
 constexpr int kRoleThreads = 128;
-constexpr int kThreads = 3 * kRoleThreads + 64;
+// With d = 64 and outputs to write, z is weighed by warps of its own (at 96
+// registers a thread), else by the output warps.
+constexpr bool has_w(int maxdx, bool state_only) { return maxdx == 64 && !state_only; }
+constexpr int threads(int maxdx, bool state_only) { return (has_w(maxdx, state_only) ? 4 : 3) * kRoleThreads + 64; }
 constexpr uint32_t kAtom = 1024;        // 8 rows of 128 bytes
 constexpr int kTries = 1 << 18;         // of a bounded wait
 
@@ -68,11 +72,6 @@ struct Cfg {
   static constexpr int NY = 2;                          // and of Y, released by G4
   static constexpr int NT = MAXDX == 64 ? 3 : 2;        // stages of Z, needed first and released last
   static constexpr int NZ = MAXDX == 64 ? 2 : 1;        // buffers of w z
-  // Who weighs z.  With two buffers the state's warps take half of it off the
-  // output warps, which carry the longest chain (training step of B8 H16 N2048,
-  // d = 64: 126 us without, 118 us with); with one buffer it would hold up the
-  // state instead (d = 128: 140 us without, 150 us with).
-  static constexpr bool kSplit = NZ == 2;
   // Every problem has dx = 64, and K 64 rows: a third less of shared memory is
   // read for G4 than with 128 rows of which half mean nothing.
   static constexpr bool kHalf = MAXDX == 64;
@@ -166,11 +165,11 @@ __host__ __device__ constexpr uint32_t idesc_bf16(int M, int N, int a_mn, int b_
 }
 
 template <int MAXDX, bool STATE_ONLY>
-__global__ void __launch_bounds__(512, 1) lin_tc_kernel(const __grid_constant__ TcParams prm,
+__global__ void __launch_bounds__(has_w(MAXDX, STATE_ONLY) ? 640 : 512, 1) lin_tc_kernel(const __grid_constant__ TcParams prm,
                                                         const __grid_constant__ Maps maps) {
   using K = Cfg<MAXDX>;
   constexpr int NX = K::NX, NY = K::NY, NT = K::NT;
-  constexpr bool kZFreeUsed = K::NZ == 1 || STATE_ONLY;
+  constexpr bool kW = has_w(MAXDX, STATE_ONLY);
   extern __shared__ uint8_t raw[];
   uint8_t* smem = raw + ((1024u - (smem_u32(raw) & 1023u)) & 1023u);
   const LinArgs& a = prm.a;
@@ -211,7 +210,7 @@ __global__ void __launch_bounds__(512, 1) lin_tc_kernel(const __grid_constant__ 
     for (int i = 0; i < kBars; ++i) {   // arrivals: one, or one per warp of the roles that fill the buffer
       const bool warps4 = i == kPReady || i == kPReady + 1 || i == kSReady || i == kOFree ||
                           i == kZReady || i == kZReady + 1;
-      mbar_init(bars + i, K::kSplit && (i == kZReady || i == kZReady + 1) ? 8 : warps4 ? 4 : 1);
+      mbar_init(bars + i, warps4 ? 4 : 1);
     }
     for (int i = 0; i < 4; ++i) bad[i] = C;
     *abort_flag = 0;
@@ -245,26 +244,23 @@ __global__ void __launch_bounds__(512, 1) lin_tc_kernel(const __grid_constant__ 
   // one outcome for a warp: what follows is warp-wide
   auto warp_wait = [&](int bar, uint32_t parity) { return __all_sync(0xffffffffu, wait(bar, parity)) != 0; };
 
-  // w z of chunk c (of half of it if split) in two bf16 parts, at z's own
-  // offsets (row = token); u: the thread among its role's 128
-  auto weigh = [&](int c, int half, int u) -> bool {
-    constexpr int kIter = K::kSplit ? 4 : 8;
+  // w z of chunk c in two bf16 parts, at z's own offsets (row = token); u: the
+  // thread among its role's 128
+  auto weigh = [&](int c, int u) -> bool {
     const int L = min(C, a.N - chunk_at(c) * C);
     uint8_t* zw = smem + K::S_ZW + (c % K::NZ) * 2 * kBox;
     const uint8_t* zs = smem + sZ(c);
-    // G4 has read the buffer (with two of them and outputs to write, the role
-    // has already waited for a product issued after the G4 two chunks back)
-    if (kZFreeUsed && c >= K::NZ && !warp_wait(kZFree + c % K::NZ, c / K::NZ - 1)) return false;
+    if (c >= K::NZ && !warp_wait(kZFree + c % K::NZ, c / K::NZ - 1)) return false;   // G4 has read the buffer
     if (!warp_wait(kFullZ + c % NT, c / NT)) return false;
     const __nv_bfloat162 zero = __float2bfloat162_rn(0.f);
     __nv_bfloat162 probe = zero;   // 0 * z: NaN if any z is not finite
-    uint32_t off = (4 * half * kRoleThreads + u) * 16;
-    int t = 64 * half + (u >> 3);
+    uint32_t off = u * 16;
+    int t = u >> 3;
     uint4 zn = *reinterpret_cast<const uint4*>(zs + off);
 #pragma unroll 1
-    for (int i = 0; i < kIter; ++i) {
+    for (int i = 0; i < 8; ++i) {
       const uint32_t zz[4] = {zn.x, zn.y, zn.z, zn.w};
-      if (i + 1 < kIter) zn = *reinterpret_cast<const uint4*>(zs + off + 16 * kRoleThreads);
+      if (i < 7) zn = *reinterpret_cast<const uint4*>(zs + off + 16 * kRoleThreads);
       const float wt = t < L ? pw[rev ? t : L - 1 - t] : 0.f;
       const uint64_t w2 = f2_pack(wt, wt), minus = f2_pack(-1.f, -1.f);
       uint32_t hi[4], lo[4];
@@ -285,7 +281,7 @@ __global__ void __launch_bounds__(512, 1) lin_tc_kernel(const __grid_constant__ 
       // tokens before it.  G2 reads a zero instead and the output warps write
       // NaN from its token on.
 #pragma unroll 1
-      for (int i = 16 * half; i < 16 * half + 4 * kIter; ++i) {
+      for (int i = 0; i < 32; ++i) {
         const int it = i >> 2, tt = 16 * it + (u >> 3);
         uint32_t* z = reinterpret_cast<uint32_t*>(smem + sZ(c) + (it * kRoleThreads + u) * 16) + (i & 3);
         uint32_t x = *z;
@@ -319,37 +315,34 @@ __global__ void __launch_bounds__(512, 1) lin_tc_kernel(const __grid_constant__ 
 #pragma unroll 1
         for (int gr = 0; gr < 4; ++gr) {
           const int side = rev ? gr - warp : warp - gr;   // > 0: whole group, 0: the diagonal one, < 0: nothing
-          uint32_t w[16];
-          if (side < 0) {
+          const float f = pw[side > 0 ? (rev ? 32 * gr - t : t - 32 * gr - 31) : 0];
+          const uint64_t ff = f2_pack(f, f);
 #pragma unroll
-            for (int i = 0; i < 16; ++i) w[i] = 0u;
-          } else {
-            uint32_t v[2][16];
-            tmem_ld16(ta + 32 * gr, v[0]);
-            tmem_ld16(ta + 32 * gr + 16, v[1]);
-            const float f = pw[side > 0 ? (rev ? 32 * gr - t : t - 32 * gr - 31) : 0];
-            tmem_ld_wait16(v[0]);
-            tmem_ld_wait16(v[1]);
-            if (side > 0) {
-              const uint64_t ff = f2_pack(f, f);
+          for (int hf = 0; hf < 2; ++hf) {   // 16 columns at a time
+            uint32_t w[8];
+            if (side < 0) {
 #pragma unroll
-              for (int i = 0; i < 16; ++i) {
-                const uint32_t* x = &v[i >> 3][2 * (i & 7)];
-                float lo, hi;
-                f2_unpack(f2_mul(f2_mul(f2_pack(__uint_as_float(x[0]), __uint_as_float(x[1])), e[i]), ff), lo, hi);
-                w[i] = pack_bf16(lo, hi);
-              }
+              for (int i = 0; i < 8; ++i) w[i] = 0u;
             } else {
-              // select, not multiply: a masked score may be infinite or NaN
-              auto val = [&](int j) {
-                const int d = rev ? j - lane : lane - j;
-                return d >= 0 ? __uint_as_float(v[j >> 4][j & 15]) * pw[max(d, 0)] : 0.f;
-              };
+              uint32_t v[16];
+              tmem_ld16(ta + 32 * gr + 16 * hf, v);
+              tmem_ld_wait16(v);
+              if (side > 0) {
 #pragma unroll
-              for (int i = 0; i < 16; ++i) w[i] = pack_bf16(val(2 * i), val(2 * i + 1));
+                for (int i = 0; i < 8; ++i)
+                  w[i] = pack2(f2_mul(f2_mul(f2_pack(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1])), e[8 * hf + i]), ff));
+              } else {
+                // select, not multiply: a masked score may be infinite or NaN
+                auto val = [&](int j) {
+                  const int d = rev ? 16 * hf + j - lane : lane - 16 * hf - j;
+                  return d >= 0 ? __uint_as_float(v[j]) * pw[max(d, 0)] : 0.f;
+                };
+#pragma unroll
+                for (int i = 0; i < 8; ++i) w[i] = pack_bf16(val(2 * i), val(2 * i + 1));
+              }
             }
+            tmem_st8(ta + 16 * gr + 8 * hf, w);   // columns of A that this lane has read already
           }
-          tmem_st16(ta + 16 * gr, w);   // columns of A that this lane has read already
         }
         tmem_st_wait();
         tc_fence_before();
@@ -368,7 +361,7 @@ __global__ void __launch_bounds__(512, 1) lin_tc_kernel(const __grid_constant__ 
     uint8_t* row = smem + K::S_OUT + u * 128;
 #pragma unroll 1
     for (int c = -1; c < n; ++c) {
-      if (c + 1 < n) alive = alive && weigh(c + 1, 0, u);
+      if (!kW && c + 1 < n) alive = alive && weigh(c + 1, u);
       if (c < 0) continue;           // the first chunk is weighed before the first output
       if (STATE_ONLY) {
         if (!alive) break;
@@ -443,7 +436,6 @@ __global__ void __launch_bounds__(512, 1) lin_tc_kernel(const __grid_constant__ 
       __syncwarp();
       if (lane == 0) mbar_arrive(bars + kSReady);
     };
-    int weighed = 0;
 #pragma unroll 1
     for (int c = -1; c < n; ++c) {
       if (c >= 0) {
@@ -489,12 +481,6 @@ __global__ void __launch_bounds__(512, 1) lin_tc_kernel(const __grid_constant__ 
         if (!STATE_ONLY && c >= 0 && !warp_wait(kSFree, c)) break;   // G3 has read the old operand
         write_operand();
       }
-      if (K::kSplit) {   // two chunks ahead of the state
-        bool ok = true;
-#pragma unroll 1
-        for (; ok && weighed < min(n, c + 3); ++weighed) ok = weigh(weighed, 1, u);
-        if (!ok) break;
-      }
     }
     float* dst = STATE_ONLY ? pr.seg + (static_cast<long long>(bh) * (a.nseg - 1) + seg) * per_state
                             : (pr.state_out && seg == a.nseg - 1) ? pr.state_out + bh * per_state : nullptr;
@@ -506,7 +492,13 @@ __global__ void __launch_bounds__(512, 1) lin_tc_kernel(const __grid_constant__ 
         f2_unpack(S[2 * i + 1], v.z, v.w);
         *reinterpret_cast<float4*>(dst + at_state + 4 * i) = v;
       }
-  } else if (warp == 12) {
+  } else if (kW && warp < 16) {
+    // ------------------------------------------------------------------- W
+    const int u = tid - 3 * kRoleThreads;
+#pragma unroll 1
+    for (int c = 0; c < n; ++c)
+      if (!weigh(c, u)) break;
+  } else if (warp == (kW ? 16 : 12)) {
     // ---------------------------------------------------------------- loads
     if (elect_one()) {
       const CUtensorMap *mx = &maps.m[prm.mi[pi].x], *my = &maps.m[prm.mi[pi].y], *mz = &maps.m[prm.mi[pi].z];
@@ -579,7 +571,7 @@ __global__ void __launch_bounds__(512, 1) lin_tc_kernel(const __grid_constant__ 
         for (int kk = 0; kk < 8; ++kk)
           mma_ss(lead, tmem + kTK, y + kk * kTok, zw + kk * kTok, idesc_bf16(K::kHalf ? 64 : 128, 128, 1, 1), kk > 0);
         commit_to(lead, bars + kKFull);
-        if (kZFreeUsed) commit_to(lead, bars + kZFree + zb);
+        commit_to(lead, bars + kZFree + zb);
         commit_to(lead, bars + kFreeY + c % NY);   // G1 of this chunk came before
         if (STATE_ONLY) commit_to(lead, bars + kFreeZ + c % NT);
       };
@@ -656,7 +648,7 @@ cudaError_t launch(const TcParams& prm, const Maps& maps, bool state_only, cudaS
   auto kern = state_only ? lin_tc_kernel<MAXDX, true> : lin_tc_kernel<MAXDX, false>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<MAXDX>::SMEM);
   if (e != cudaSuccess) return e;
-  return launch_after(kern, static_cast<unsigned>(grid), kThreads, Cfg<MAXDX>::SMEM, st, a.nseg > 1 && !state_only, prm, maps);
+  return launch_after(kern, static_cast<unsigned>(grid), threads(MAXDX, state_only), Cfg<MAXDX>::SMEM, st, a.nseg > 1 && !state_only, prm, maps);
 }
 
 }  // namespace
