@@ -8,7 +8,7 @@
 //   G1  A  = X Y^T            128 x 128 x dx   operands straight from TMA
 //   G2  O2 = P Z              128 x 64 x 128   P = decayed, masked A, from TMEM
 //   G3  O1 = X S              128 x 64 x dx    S = the entering state in bf16
-//   G4  K  = Y^T (w Z)        dx x 128 x 128   w z in two bf16 parts, side by side
+//   G4  K  = Y^T (w Z)        dx x 64 x 256    w z in two bf16 parts
 //   out = scale (O2 + lambda^(p+1) O1),  S <- lambda^L S + K in fp32 registers
 //
 // Rounding.  Decays multiply fp32 accumulators wherever they can: A before it
@@ -30,7 +30,7 @@
 //               the next chunk's G3
 //   warps 12-15 W: w z for G4 (where there are none, O does it)
 //   then a warp for the TMA loads and one that issues G1-G4
-// Per chunk G4, G1 of the next chunk, G3 and G2 are issued in this order, so
+// Per chunk G4, G1 of the next chunk, G3 (or G3 first) and G2 are issued, so
 // that P and the state work while the products of the other roles run.  The
 // loops of the roles are kept short on purpose: with everything unrolled the
 // warps spent six of seven issue slots waiting for instructions (three roles
@@ -63,8 +63,6 @@ constexpr int threads(int maxdx, bool state_only) { return (has_w(maxdx, state_o
 constexpr uint32_t kAtom = 1024;        // 8 rows of 128 bytes
 constexpr int kTries = 1 << 18;         // of a bounded wait
 
-// TMEM columns
-constexpr uint32_t kTA = 0, kTO1 = 256, kTO2 = 320, kTK = 384;
 
 template <int MAXDX>
 struct Cfg {
@@ -72,6 +70,14 @@ struct Cfg {
   static constexpr int NY = 2;                          // and of Y, released by G4
   static constexpr int NT = MAXDX == 64 ? 3 : 2;        // stages of Z, needed first and released last
   static constexpr int NZ = MAXDX == 64 ? 2 : 1;        // buffers of w z
+  // TMEM columns (A twice, with P in its place).  With wide X a second O1 lets
+  // G3 go first, so that X's stage is loaded again early: its two stages hide
+  // the load no longer (forward of B4 H16 N2048 d128 44.6 us without, 41.5
+  // with).  That leaves 64 columns for K, whose two parts are then contracted
+  // one after the other (16 products instead of 8 twice as wide); with d = 64
+  // and three stages this costs more than it gives (27.1 us, and 27.8).
+  static constexpr bool kO1Twice = MAXDX == 128;
+  static constexpr uint32_t kTA = 0, kTO1 = 256, kTO2 = kO1Twice ? 384 : 320, kTK = kO1Twice ? 448 : 384;
   // Every problem has dx = 64, and K 64 rows: a third less of shared memory is
   // read for G4 than with 128 rows of which half mean nothing.
   static constexpr bool kHalf = MAXDX == 64;
@@ -311,7 +317,7 @@ __global__ void __launch_bounds__(has_w(MAXDX, STATE_ONLY) ? 640 : 512, 1) lin_t
         const int b = c & 1;
         if (!warp_wait(kAFull + b, c >> 1)) break;
         tc_fence_after();
-        const uint32_t ta = tmem + (static_cast<uint32_t>(warp) << 21) + kTA + 128 * b;
+        const uint32_t ta = tmem + (static_cast<uint32_t>(warp) << 21) + K::kTA + 128 * b;
 #pragma unroll 1
         for (int gr = 0; gr < 4; ++gr) {
           const int side = rev ? gr - warp : warp - gr;   // > 0: whole group, 0: the diagonal one, < 0: nothing
@@ -377,8 +383,8 @@ __global__ void __launch_bounds__(has_w(MAXDX, STATE_ONLY) ? 640 : 512, 1) lin_t
 #pragma unroll 1
       for (int q = 0; q < 4; ++q) {
         uint32_t v1[16], v2[16], w[8];
-        tmem_ld16(to + kTO1 + 16 * q, v1);
-        tmem_ld16(to + kTO2 + 16 * q, v2);
+        tmem_ld16(to + K::kTO1 + (K::kO1Twice ? 64 * (c & 1) : 0) + 16 * q, v1);
+        tmem_ld16(to + K::kTO2 + 16 * q, v2);
         tmem_ld_wait16(v1);
         tmem_ld_wait16(v2);
 #pragma unroll
@@ -444,35 +450,26 @@ __global__ void __launch_bounds__(has_w(MAXDX, STATE_ONLY) ? 640 : 512, 1) lin_t
       const uint64_t dec2 = f2_pack(dec, dec);
       if (!warp_wait(kKFull, c)) break;
       tc_fence_after();
-      const uint32_t tk = tmem + (static_cast<uint32_t>(warp - 8) << 21) + kTK;
-      auto add = [&](int i, const uint32_t (&v)[16], const uint32_t (&w)[16]) {   // columns 16 i ..: both parts of w z
-#pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          const uint64_t hi = f2_pack(__uint_as_float(v[2 * k]), __uint_as_float(v[2 * k + 1]));
-          const uint64_t lo = f2_pack(__uint_as_float(w[2 * k]), __uint_as_float(w[2 * k + 1]));
-          uint64_t& S2 = S[8 * i + k];
-          S2 = f2_add(f2_fma(dec2, S2, S2), f2_add(hi, lo));
-        }
-      };
-      if (K::kHalf) {
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          uint32_t v[16], w[16];
-          tmem_ld16_halves<32>(tk + 16 * i, v);
-          tmem_ld16_halves<32>(tk + 64 + 16 * i, w);
-          tmem_ld_wait16(v);
-          tmem_ld_wait16(w);
-          add(i, v, w);
-        }
-      } else if (32 * (warp - 8) < dx) {
+      const uint32_t tk = tmem + (static_cast<uint32_t>(warp - 8) << 21) + K::kTK;
+      if (K::kHalf || 32 * (warp - 8) < dx) {
 #pragma unroll
         for (int i = 0; i < kCols / 16; ++i) {
           uint32_t v[16], w[16];
-          tmem_ld16(tk + 16 * i, v);
-          tmem_ld16(tk + 64 + 16 * i, w);
+          auto load = [&](uint32_t from, uint32_t (&r)[16]) {
+            if (K::kHalf) tmem_ld16_halves<32>(from, r);
+            else tmem_ld16(from, r);
+          };
+          load(tk + 16 * i, v);
+          if (!K::kO1Twice) load(tk + 64 + 16 * i, w);
           tmem_ld_wait16(v);
-          tmem_ld_wait16(w);
-          add(i, v, w);
+          if (!K::kO1Twice) tmem_ld_wait16(w);
+#pragma unroll
+          for (int k = 0; k < 8; ++k) {
+            uint64_t add = f2_pack(__uint_as_float(v[2 * k]), __uint_as_float(v[2 * k + 1]));
+            if (!K::kO1Twice) add = f2_add(add, f2_pack(__uint_as_float(w[2 * k]), __uint_as_float(w[2 * k + 1])));
+            uint64_t& S2 = S[8 * i + k];
+            S2 = f2_add(f2_fma(dec2, S2, S2), add);
+          }
         }
       }
       tc_fence_before();
@@ -548,7 +545,7 @@ __global__ void __launch_bounds__(has_w(MAXDX, STATE_ONLY) ? 640 : 512, 1) lin_t
 #pragma unroll
           for (int kk = 0; kk < 4; ++kk) {
             const uint64_t step = (b * kBox + kk * 32) >> 4;
-            mma_ss(lead, tmem + kTA + 128 * (c & 1), x + step, y + step, idesc_bf16(128, 128, 0, 0), b + kk > 0);
+            mma_ss(lead, tmem + K::kTA + 128 * (c & 1), x + step, y + step, idesc_bf16(128, 128, 0, 0), b + kk > 0);
           }
         commit_to(lead, bars + kAFull + (c & 1));
       };
@@ -558,7 +555,7 @@ __global__ void __launch_bounds__(has_w(MAXDX, STATE_ONLY) ? 640 : 512, 1) lin_t
         for (int b = 0; b < nbx; ++b)
 #pragma unroll
           for (int kk = 0; kk < 4; ++kk)
-            mma_ss(lead, tmem + kTO1, x + ((b * kBox + kk * 32) >> 4), sb + (4 * b + kk) * kTok, idesc_bf16(128, 64, 0, 1), b + kk > 0);
+            mma_ss(lead, tmem + K::kTO1 + (K::kO1Twice ? 64 * (c & 1) : 0), x + ((b * kBox + kk * 32) >> 4), sb + (4 * b + kk) * kTok, idesc_bf16(128, 64, 0, 1), b + kk > 0);
         commit_to(lead, bars + kSFree);
         commit_to(lead, bars + kFreeX + c % NX);
       };
@@ -567,9 +564,11 @@ __global__ void __launch_bounds__(has_w(MAXDX, STATE_ONLY) ? 640 : 512, 1) lin_t
         // next tile in shared memory and never read)
         const int zb = c % K::NZ;
         const uint64_t y = mnmajor(sY(c)), zw = mnmajor(K::S_ZW + zb * 2 * kBox);
+        constexpr int kSteps = K::kO1Twice ? 16 : 8;   // hi then lo, or side by side
 #pragma unroll 4
-        for (int kk = 0; kk < 8; ++kk)
-          mma_ss(lead, tmem + kTK, y + kk * kTok, zw + kk * kTok, idesc_bf16(K::kHalf ? 64 : 128, 128, 1, 1), kk > 0);
+        for (int kk = 0; kk < kSteps; ++kk)
+          mma_ss(lead, tmem + K::kTK, y + (kk & 7) * kTok, zw + kk * kTok,
+                 idesc_bf16(K::kHalf ? 64 : 128, 128 * 8 / kSteps, 1, 1), kk > 0);
         commit_to(lead, bars + kKFull);
         commit_to(lead, bars + kZFree + zb);
         commit_to(lead, bars + kFreeY + c % NY);   // G1 of this chunk came before
@@ -579,7 +578,7 @@ __global__ void __launch_bounds__(has_w(MAXDX, STATE_ONLY) ? 640 : 512, 1) lin_t
         const uint64_t z = mnmajor(sZ(c));
 #pragma unroll 4
         for (int kk = 0; kk < 8; ++kk)
-          mma_ts(lead, tmem + kTO2, tmem + kTA + 128 * (c & 1) + 8 * kk, z + kk * kTok, idesc_bf16(128, 64, 0, 1), kk > 0);
+          mma_ts(lead, tmem + K::kTO2, tmem + K::kTA + 128 * (c & 1) + 8 * kk, z + kk * kTok, idesc_bf16(128, 64, 0, 1), kk > 0);
         commit_to(lead, bars + kOFull);
         commit_to(lead, bars + kFreeZ + c % NT);
       };
@@ -594,8 +593,13 @@ __global__ void __launch_bounds__(has_w(MAXDX, STATE_ONLY) ? 640 : 512, 1) lin_t
       }
 #pragma unroll 1
       for (int c = 0; ok && c < n; ++c) {
-        // K is free once the state has taken it (which also made S's operand)
-        if (!warp_wait(kSReady, c) || !warp_wait(kZReady + c % K::NZ, c / K::NZ)) break;
+        // S's operand is made, and K taken
+        if (!warp_wait(kSReady, c)) break;
+        if (!STATE_ONLY && K::kO1Twice) {
+          tc_fence_after();
+          g3(c);
+        }
+        if (!warp_wait(kZReady + c % K::NZ, c / K::NZ)) break;
         if (STATE_ONLY && !warp_wait(kFullY + c % NY, c / NY)) break;   // (else G1 has waited for Y)
         tc_fence_after();
         g4(c);
@@ -607,8 +611,10 @@ __global__ void __launch_bounds__(has_w(MAXDX, STATE_ONLY) ? 640 : 512, 1) lin_t
             g1(c + 1);
           }
           if (c > 0 && !warp_wait(kOFree, c - 1)) break;
-          tc_fence_after();
-          g3(c);
+          if (!K::kO1Twice) {
+            tc_fence_after();
+            g3(c);
+          }
           if (!warp_wait(kPReady + (c & 1), c >> 1)) break;
           tc_fence_after();
           g2(c);
