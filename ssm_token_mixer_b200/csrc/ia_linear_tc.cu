@@ -18,8 +18,8 @@
 // carried and returned keeps fp32-like accuracy.  P and the S operand are
 // rounded to bf16 once, like the output.
 //
-// Roles (448 threads, four warps at most per register file: 128 registers; or
-// 576, five warps: 96):
+// Roles (448 threads, four warps at most on a quarter of the registers: 128 a
+// thread; or 576, five warps: 96):
 //   warps 0-3   P: A from TMEM, decayed, back to TMEM as the A operand of G2.
 //               lambda^(t-s) = lambda^(t - e) lambda^(e - s) over groups of 32
 //               columns that end at e <= t: both factors <= 1 and constant per
@@ -28,7 +28,8 @@
 //   warps 4-7   O: O1, O2 from TMEM, out through shared memory and a TMA store
 //   warps 8-11  S: K from TMEM, S in registers, S in bf16 to shared memory for
 //               the next chunk's G3
-//   warps 12-15 W: w z for G4 (where there are none, O does it)
+//   warps 12-15 W: w z for G4 (where there are none, O does it; a pass for the
+//               states alone has nothing else for P and O to do)
 //   then a warp for the TMA loads and one that issues G1-G4
 // Per chunk G4, G1 of the next chunk, G3 (or G3 first) and G2 are issued, so
 // that P and the state work while the products of the other roles run.  The
@@ -61,22 +62,20 @@ constexpr int kRoleThreads = 128;
 constexpr bool has_w(int maxdx, bool state_only) { return maxdx == 64 && !state_only; }
 constexpr int threads(int maxdx, bool state_only) { return (has_w(maxdx, state_only) ? 4 : 3) * kRoleThreads + 64; }
 constexpr uint32_t kAtom = 1024;        // 8 rows of 128 bytes
-constexpr int kTries = 1 << 18;         // of a bounded wait
 
-
-template <int MAXDX>
+template <int MAXDX, bool STATE_ONLY>
 struct Cfg {
-  static constexpr int NX = MAXDX == 64 ? 3 : 2;        // stages of X, released late (by G3)
-  static constexpr int NY = 2;                          // and of Y, released by G4
-  static constexpr int NT = MAXDX == 64 ? 3 : 2;        // stages of Z, needed first and released last
-  static constexpr int NZ = MAXDX == 64 ? 2 : 1;        // buffers of w z
+  static constexpr int NX = STATE_ONLY ? 0 : MAXDX == 64 ? 3 : 2;   // stages of X, released late (by G3)
+  static constexpr int NY = STATE_ONLY ? 3 : 2;         // and of Y, released by G4
+  static constexpr int NT = STATE_ONLY || MAXDX == 64 ? 3 : 2;      // stages of Z, needed first and released last
+  static constexpr int NZ = STATE_ONLY || MAXDX == 64 ? 2 : 1;      // buffers of w z
   // TMEM columns (A twice, with P in its place).  With wide X a second O1 lets
   // G3 go first, so that X's stage is loaded again early: its two stages hide
   // the load no longer (forward of B4 H16 N2048 d128 44.6 us without, 41.5
   // with).  That leaves 64 columns for K, whose two parts are then contracted
   // one after the other (16 products instead of 8 twice as wide); with d = 64
   // and three stages this costs more than it gives (27.1 us, and 27.8).
-  static constexpr bool kO1Twice = MAXDX == 128;
+  static constexpr bool kO1Twice = MAXDX == 128 && !STATE_ONLY;
   static constexpr uint32_t kTA = 0, kTO1 = 256, kTO2 = kO1Twice ? 384 : 320, kTK = kO1Twice ? 448 : 384;
   // Every problem has dx = 64, and K 64 rows: a third less of shared memory is
   // read for G4 than with 128 rows of which half mean nothing.
@@ -86,15 +85,16 @@ struct Cfg {
   static constexpr int S_Z = S_Y + NY * TX;
   static constexpr int S_ZW = S_Z + NT * kBox;          // each: hi, lo
   static constexpr int S_SB = S_ZW + NZ * 2 * kBox;     // [dx][64] bf16, 128-byte swizzled
-  static constexpr int S_OUT = S_SB + MAXDX * 128;
-  static constexpr int S_BAR = S_OUT + kBox;
-  static constexpr int S_POW = S_BAR + 272;             // lambda^n, n = 0 .. C - 1
+  static constexpr int S_OUT = S_SB + (STATE_ONLY ? 0 : MAXDX * 128);
+  static constexpr int S_BAR = S_OUT + (STATE_ONLY ? 0 : kBox);
+  static constexpr int S_POW = S_BAR + 288;             // lambda^n, n = 0 .. C - 1
   static constexpr int SMEM = S_POW + C * 4 + 1024;     // + alignment of the base
+  static_assert(NX <= 3 && NY <= 3 && NT <= 3 && NZ <= 2, "their barriers");
 };
 
 enum Bar {
-  kFullX = 0, kFullY = 3, kFullZ = 5, kFreeX = 8, kFreeY = 11, kFreeZ = 13, kAFull = 16, kPReady = 18, kZReady = 20,
-  kZFree = 22, kSReady = 24, kSFree, kKFull, kOFull, kOFree, kDrain, kBars
+  kFullX = 0, kFullY = 3, kFullZ = 6, kFreeX = 9, kFreeY = 12, kFreeZ = 15, kAFull = 18, kPReady = 20, kZReady = 22,
+  kZFree = 24, kSReady = 26, kSFree, kKFull, kOFull, kOFree, kDrain, kBars
 };
 
 struct Maps {
@@ -173,9 +173,15 @@ __host__ __device__ constexpr uint32_t idesc_bf16(int M, int N, int a_mn, int b_
 template <int MAXDX, bool STATE_ONLY>
 __global__ void __launch_bounds__(has_w(MAXDX, STATE_ONLY) ? 640 : 512, 1) lin_tc_kernel(const __grid_constant__ TcParams prm,
                                                         const __grid_constant__ Maps maps) {
-  using K = Cfg<MAXDX>;
-  constexpr int NX = K::NX, NY = K::NY, NT = K::NT;
+  using K = Cfg<MAXDX, STATE_ONLY>;
+  constexpr int kNX = K::NX ? K::NX : 1, NY = K::NY, NT = K::NT;
   constexpr bool kW = has_w(MAXDX, STATE_ONLY);
+  // The state-only pass has room for two K, so that one is contracted while the
+  // state takes the other (its barriers: those of A and P, which it has no other
+  // use for), and its P and O warps weigh half of z each: a chunk of d = 128
+  // takes 0.8 us, and 1.4 with one K, weighed by four warps.
+  auto k_full = [](int c) { return STATE_ONLY ? kAFull + (c & 1) : static_cast<int>(kKFull); };
+  auto k_col = [](int c) { return K::kTK - (STATE_ONLY ? 128 * (c & 1) : 0); };
   extern __shared__ uint8_t raw[];
   uint8_t* smem = raw + ((1024u - (smem_u32(raw) & 1023u)) & 1023u);
   const LinArgs& a = prm.a;
@@ -202,9 +208,9 @@ __global__ void __launch_bounds__(has_w(MAXDX, STATE_ONLY) ? 640 : 512, 1) lin_t
   uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(smem + K::S_BAR + 8 * kBars);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + K::S_BAR + 8 * kBars + 4);
   int* bad = reinterpret_cast<int*>(smem + K::S_BAR + 8 * kBars + 8);   // [4]
-  static_assert(8 * kBars + 24 <= 272, "barriers and flags fit their slot");
+  static_assert(8 * kBars + 24 <= 288, "barriers and flags fit their slot");
   const uint32_t sbase = smem_u32(smem);
-  auto sX = [&](int c) { return (c % NX) * K::TX; };
+  auto sX = [&](int c) { return (c % kNX) * K::TX; };
   auto sY = [&](int c) { return K::S_Y + (c % NY) * K::TX; };
   auto sZ = [&](int c) { return K::S_Z + (c % NT) * kBox; };
 
@@ -216,7 +222,8 @@ __global__ void __launch_bounds__(has_w(MAXDX, STATE_ONLY) ? 640 : 512, 1) lin_t
     for (int i = 0; i < kBars; ++i) {   // arrivals: one, or one per warp of the roles that fill the buffer
       const bool warps4 = i == kPReady || i == kPReady + 1 || i == kSReady || i == kOFree ||
                           i == kZReady || i == kZReady + 1;
-      mbar_init(bars + i, warps4 ? 4 : 1);
+      const bool warps8 = STATE_ONLY && (i == kZReady || i == kZReady + 1);
+      mbar_init(bars + i, warps8 ? 8 : warps4 ? 4 : 1);
     }
     for (int i = 0; i < 4; ++i) bad[i] = C;
     *abort_flag = 0;
@@ -233,26 +240,16 @@ __global__ void __launch_bounds__(has_w(MAXDX, STATE_ONLY) ? 640 : 512, 1) lin_t
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_holder;
-  // Each try sleeps in hardware until the phase completes or some microseconds
-  // have passed; kTries of them are a second or so.  (The library's wait reads
-  // the clock instead; its code, inlined at 25 places, was a third of this
-  // kernel's 44 KB, which the instruction caches do not hold.)
   auto wait = [&](int bar, uint32_t parity) {
-#pragma unroll 1
-    for (int i = 0; i < kTries; ++i) {
-      if (mbar_test(bars + bar, parity & 1u)) return true;
-      if (*abort_flag) return false;
-    }
-    atomicOr(a.err, kErrTimeout);
-    *abort_flag = 1;
-    return false;
+    return mbar_wait_or_abort(bars + bar, parity & 1u, a.err, abort_flag);
   };
   // one outcome for a warp: what follows is warp-wide
   auto warp_wait = [&](int bar, uint32_t parity) { return __all_sync(0xffffffffu, wait(bar, parity)) != 0; };
 
-  // w z of chunk c in two bf16 parts, at z's own offsets (row = token); u: the
-  // thread among its role's 128
-  auto weigh = [&](int c, int u) -> bool {
+  // w z of chunk c (of a half in the state-only pass) in two bf16 parts, at z's
+  // own offsets (row = token); u: the thread among its role's 128
+  auto weigh = [&](int c, int u, int half) -> bool {
+    constexpr int kIter = STATE_ONLY ? 4 : 8;
     const int L = min(C, a.N - chunk_at(c) * C);
     uint8_t* zw = smem + K::S_ZW + (c % K::NZ) * 2 * kBox;
     const uint8_t* zs = smem + sZ(c);
@@ -260,13 +257,13 @@ __global__ void __launch_bounds__(has_w(MAXDX, STATE_ONLY) ? 640 : 512, 1) lin_t
     if (!warp_wait(kFullZ + c % NT, c / NT)) return false;
     const __nv_bfloat162 zero = __float2bfloat162_rn(0.f);
     __nv_bfloat162 probe = zero;   // 0 * z: NaN if any z is not finite
-    uint32_t off = u * 16;
-    int t = u >> 3;
+    uint32_t off = (4 * half * kRoleThreads + u) * 16;
+    int t = 64 * half + (u >> 3);
     uint4 zn = *reinterpret_cast<const uint4*>(zs + off);
 #pragma unroll 1
-    for (int i = 0; i < 8; ++i) {
+    for (int i = 0; i < kIter; ++i) {
       const uint32_t zz[4] = {zn.x, zn.y, zn.z, zn.w};
-      if (i < 7) zn = *reinterpret_cast<const uint4*>(zs + off + 16 * kRoleThreads);
+      if (i + 1 < kIter) zn = *reinterpret_cast<const uint4*>(zs + off + 16 * kRoleThreads);
       const float wt = t < L ? pw[rev ? t : L - 1 - t] : 0.f;
       const uint64_t w2 = f2_pack(wt, wt), minus = f2_pack(-1.f, -1.f);
       uint32_t hi[4], lo[4];
@@ -307,7 +304,11 @@ __global__ void __launch_bounds__(has_w(MAXDX, STATE_ONLY) ? 640 : 512, 1) lin_t
 
   if (warp < 4) {
     // ------------------------------------------------------------------- P
-    if (!STATE_ONLY) {
+    if (STATE_ONLY) {
+#pragma unroll 1
+      for (int c = 0; c < n; ++c)
+        if (!weigh(c, tid, 0)) break;
+    } else {
       const int t = tid;   // row of the chunk
       uint64_t e[16];      // lambda^(distance of column 32 gr + j from its group's near end), pairs
 #pragma unroll
@@ -367,7 +368,7 @@ __global__ void __launch_bounds__(has_w(MAXDX, STATE_ONLY) ? 640 : 512, 1) lin_t
     uint8_t* row = smem + K::S_OUT + u * 128;
 #pragma unroll 1
     for (int c = -1; c < n; ++c) {
-      if (!kW && c + 1 < n) alive = alive && weigh(c + 1, u);
+      if (!kW && c + 1 < n) alive = alive && weigh(c + 1, u, STATE_ONLY);
       if (c < 0) continue;           // the first chunk is weighed before the first output
       if (STATE_ONLY) {
         if (!alive) break;
@@ -433,7 +434,7 @@ __global__ void __launch_bounds__(has_w(MAXDX, STATE_ONLY) ? 640 : 512, 1) lin_t
       }
     }
     auto write_operand = [&]() {   // and K has been read: the next G4 may overwrite it
-      if (!STATE_ONLY && holds)
+      if (holds)
 #pragma unroll
         for (int j = 0; j < kCols / 8; ++j)
           *reinterpret_cast<uint4*>(smem + K::S_SB + row * 128 + (((col / 8 + j) ^ (row & 7)) << 4)) =
@@ -448,9 +449,9 @@ __global__ void __launch_bounds__(has_w(MAXDX, STATE_ONLY) ? 640 : 512, 1) lin_t
       const int L = min(C, a.N - chunk_at(c) * C);
       const float dec = L == C || rev ? dec_full : expm1f(g * L);
       const uint64_t dec2 = f2_pack(dec, dec);
-      if (!warp_wait(kKFull, c)) break;
+      if (STATE_ONLY ? !warp_wait(k_full(c), c >> 1) : !warp_wait(kKFull, c)) break;
       tc_fence_after();
-      const uint32_t tk = tmem + (static_cast<uint32_t>(warp - 8) << 21) + K::kTK;
+      const uint32_t tk = tmem + (static_cast<uint32_t>(warp - 8) << 21) + k_col(c);
       if (K::kHalf || 32 * (warp - 8) < dx) {
 #pragma unroll
         for (int i = 0; i < kCols / 16; ++i) {
@@ -474,8 +475,11 @@ __global__ void __launch_bounds__(has_w(MAXDX, STATE_ONLY) ? 640 : 512, 1) lin_t
       }
       tc_fence_before();
       }
-      if (c + 1 < n) {
-        if (!STATE_ONLY && c >= 0 && !warp_wait(kSFree, c)) break;   // G3 has read the old operand
+      if (STATE_ONLY) {
+        __syncwarp();
+        if (c >= 0 && lane == 0) mbar_arrive(bars + kPReady + (c & 1));   // K's buffer is free
+      } else if (c + 1 < n) {
+        if (c >= 0 && !warp_wait(kSFree, c)) break;   // G3 has read the old operand
         write_operand();
       }
     }
@@ -494,7 +498,7 @@ __global__ void __launch_bounds__(has_w(MAXDX, STATE_ONLY) ? 640 : 512, 1) lin_t
     const int u = tid - 3 * kRoleThreads;
 #pragma unroll 1
     for (int c = 0; c < n; ++c)
-      if (!weigh(c, u)) break;
+      if (!weigh(c, u, 0)) break;
   } else if (warp == (kW ? 16 : 12)) {
     // ---------------------------------------------------------------- loads
     if (elect_one()) {
@@ -515,8 +519,8 @@ __global__ void __launch_bounds__(has_w(MAXDX, STATE_ONLY) ? 640 : 512, 1) lin_t
         fetch(kFullY + c % NY, sY(c), my, nbx, 0, t0);
         issued_y = c + 1;
         if (STATE_ONLY) continue;
-        if (c >= NX && !wait(kFreeX + c % NX, c / NX - 1)) break;
-        fetch(kFullX + c % NX, sX(c), mx, nbx, 0, t0);
+        if (c >= kNX && !wait(kFreeX + c % kNX, c / kNX - 1)) break;
+        fetch(kFullX + c % kNX, sX(c), mx, nbx, 0, t0);
         issued_x = c + 1;
       }
       // no copy lands after the block exits
@@ -525,7 +529,7 @@ __global__ void __launch_bounds__(has_w(MAXDX, STATE_ONLY) ? 640 : 512, 1) lin_t
 #pragma unroll 1
       for (int c = max(0, issued_y - NY); c < issued_y; ++c) mbar_wait(bars + kFullY + c % NY, (c / NY) & 1, a.err);
 #pragma unroll 1
-      for (int c = max(0, issued_x - NX); c < issued_x; ++c) mbar_wait(bars + kFullX + c % NX, (c / NX) & 1, a.err);
+      for (int c = max(0, issued_x - kNX); c < issued_x; ++c) mbar_wait(bars + kFullX + c % kNX, (c / kNX) & 1, a.err);
     }
     __syncwarp();
   } else {
@@ -557,7 +561,7 @@ __global__ void __launch_bounds__(has_w(MAXDX, STATE_ONLY) ? 640 : 512, 1) lin_t
           for (int kk = 0; kk < 4; ++kk)
             mma_ss(lead, tmem + K::kTO1 + (K::kO1Twice ? 64 * (c & 1) : 0), x + ((b * kBox + kk * 32) >> 4), sb + (4 * b + kk) * kTok, idesc_bf16(128, 64, 0, 1), b + kk > 0);
         commit_to(lead, bars + kSFree);
-        commit_to(lead, bars + kFreeX + c % NX);
+        commit_to(lead, bars + kFreeX + c % kNX);
       };
       auto g4 = [&](int c) {
         // (beside wider problems, the rows of K past dx = 64 are taken from the
@@ -567,9 +571,9 @@ __global__ void __launch_bounds__(has_w(MAXDX, STATE_ONLY) ? 640 : 512, 1) lin_t
         constexpr int kSteps = K::kO1Twice ? 16 : 8;   // hi then lo, or side by side
 #pragma unroll 4
         for (int kk = 0; kk < kSteps; ++kk)
-          mma_ss(lead, tmem + K::kTK, y + (kk & 7) * kTok, zw + kk * kTok,
+          mma_ss(lead, tmem + k_col(c), y + (kk & 7) * kTok, zw + kk * kTok,
                  idesc_bf16(K::kHalf ? 64 : 128, 128 * 8 / kSteps, 1, 1), kk > 0);
-        commit_to(lead, bars + kKFull);
+        commit_to(lead, bars + k_full(c));
         commit_to(lead, bars + kZFree + zb);
         commit_to(lead, bars + kFreeY + c % NY);   // G1 of this chunk came before
         if (STATE_ONLY) commit_to(lead, bars + kFreeZ + c % NT);
@@ -594,8 +598,8 @@ __global__ void __launch_bounds__(has_w(MAXDX, STATE_ONLY) ? 640 : 512, 1) lin_t
 #pragma unroll 1
       for (int c = 0; ok && c < n; ++c) {
         // S's operand is made, and K taken
-        if (!warp_wait(kSReady, c)) break;
-        if (!STATE_ONLY && K::kO1Twice) {
+        if (STATE_ONLY ? c >= 2 && !warp_wait(kPReady + (c & 1), (c >> 1) - 1) : !warp_wait(kSReady, c)) break;
+        if (K::kO1Twice) {
           tc_fence_after();
           g3(c);
         }
@@ -606,7 +610,7 @@ __global__ void __launch_bounds__(has_w(MAXDX, STATE_ONLY) ? 640 : 512, 1) lin_t
         issued = true;
         if (!STATE_ONLY) {
           if (c + 1 < n) {
-            if (!warp_wait(kFullX + (c + 1) % NX, (c + 1) / NX) || !warp_wait(kFullY + (c + 1) % NY, (c + 1) / NY)) break;
+            if (!warp_wait(kFullX + (c + 1) % kNX, (c + 1) / kNX) || !warp_wait(kFullY + (c + 1) % NY, (c + 1) / NY)) break;
             tc_fence_after();
             g1(c + 1);
           }
@@ -652,9 +656,9 @@ cudaError_t launch(const TcParams& prm, const Maps& maps, bool state_only, cudaS
   const long long grid = static_cast<long long>(a.BH) * a.first[a.nprob] * (state_only ? a.nseg - 1 : a.nseg);
   if (grid > (1LL << 31) - 1) return cudaErrorInvalidConfiguration;
   auto kern = state_only ? lin_tc_kernel<MAXDX, true> : lin_tc_kernel<MAXDX, false>;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<MAXDX>::SMEM);
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (state_only ? Cfg<MAXDX, true>::SMEM : Cfg<MAXDX, false>::SMEM));
   if (e != cudaSuccess) return e;
-  return launch_after(kern, static_cast<unsigned>(grid), threads(MAXDX, state_only), Cfg<MAXDX>::SMEM, st, a.nseg > 1 && !state_only, prm, maps);
+  return launch_after(kern, static_cast<unsigned>(grid), threads(MAXDX, state_only), (state_only ? Cfg<MAXDX, true>::SMEM : Cfg<MAXDX, false>::SMEM), st, a.nseg > 1 && !state_only, prm, maps);
 }
 
 }  // namespace
