@@ -374,13 +374,17 @@ LinPlan lin_plan(const ia_linear_shape_t& s, bool train) {
   const int width = std::max(s.d_k, s.d_v);
   const long long slots = static_cast<long long>(num_sms()) * (p.tc || width > 128 ? 1 : width > 64 ? 2 : 4);
   // In microseconds on a B200: a chunk of the full pass and of the state-only
-  // pass, what a wave of CTAs costs beside its chunks, and the launches of the
-  // state-only pass and of the carry.  (d = 64: a sequence of 56 chunks alone
-  // takes 88.6 us whole, 78.7 in 2 segments, 31.7 in 8; d = 128: 119, 101, 71.)
-  const bool wide = width > 64;
-  const double full = p.tc ? (wide ? 2.1 : 1.5) : (wide ? 40.0 : 20.0);
-  const double state = p.tc ? (wide ? 1.2 : 1.0) : 0.45 * full;
-  const double wave = 3.5, extra = 2.0, carry = 3.0;
+  // pass, what a wave of CTAs costs beside its chunks, the launch of the
+  // state-only pass, and the carry over n segments.  Measured: 56 chunks of
+  // d = 64 and 16 heads take 79.5 us whole, 65.6 in 2 segments, 40.0 in 4, 27.3
+  // in 8 (planned), 38.4 in 12; 55 of d = 128 take 110.7, 82.9, 53.9 in 4
+  // (planned), 69.9 in 5, 61.9 in 8; 8 chunks of d = 64 and one head 15.3 whole,
+  // 15.6, 12.6, 11.0 in 8 (planned); of 16 heads 15.5 whole (planned) and 16.4
+  // in 4.
+  const bool wide = (p.tc && !train ? s.d_k : width) > 64;   // the tensor-core pass: x and y alone
+  const double full = p.tc ? (wide ? 1.95 : 1.3) : (wide ? 40.0 : 20.0);
+  const double state = p.tc ? (wide ? 0.8 : 0.75) : 0.45 * full;
+  const double wave = 4.5, state_wave = 3.0, extra = 1.5, carry = 2.0, carry_each = 0.04;
   if (const char* env = std::getenv("IA_LINEAR_SEGMENTS")) {   // forced count (tuning and tests)
     const int want = std::atoi(env);
     if (want >= 1) {
@@ -399,8 +403,8 @@ LinPlan lin_plan(const ia_linear_shape_t& s, bool train) {
     if (nseg != n) continue;
     auto waves = [&](long long ctas) { return static_cast<double>((ctas + slots - 1) / slots); };
     double t = waves(streams * n) * (cps * full + wave);
-    if (n > 1) t += waves(streams * (n - 1)) * (cps * state + wave) + extra;
-    if (n > 2) t += carry;
+    if (n > 1) t += waves(streams * (n - 1)) * (cps * state + state_wave) + extra;
+    if (n > 2) t += carry + n * carry_each;
     if (n == 1 || t < best) {
       best = t;
       p.nseg = n;
