@@ -47,10 +47,12 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kMaxW = 64, kMaxK = 64;
-constexpr int kPer = 8;                       // values per lane and round
+constexpr int kVec = 32;                      // bytes per lane and round
+template <typename T>
+constexpr int kPer = kVec / static_cast<int>(sizeof(T));   // its values
 constexpr int kWarps = kThreads / 32;
 constexpr int kKeep = 128;                    // a warp's list is cut back to K when it is longer
-constexpr int kCap = kKeep + 32 * kPer;       // and grows by at most this much in a round
+constexpr int kCap = kKeep + 32;              // and grows by at most this much in a round
 constexpr int kSlots = kCap / 32;
 constexpr float kSlack = 2.f;
 constexpr int kMergeMost = 2048;              // entries one merge takes (or one per beam and place, if more)
@@ -143,12 +145,14 @@ __device__ __noinline__ int cut_back(uint64_t* buf, int n, int K, int lane) {
 }
 
 constexpr int kAll = kWarps * kMaxK;   // keys the CTA's merge takes
+static_assert(kWarps * kCap >= kMaxK * kPer<__nv_bfloat16>, "the best vectors' values fit the lists");
 struct ScanSmem {
-  uint64_t buf[kWarps][kCap];
+  uint64_t buf[kWarps][kCap];   // of vectors: (largest value, number)
   uint64_t all[kAll];
+  uint64_t top[kMaxK];      // the best vectors, sorted
   volatile float lead[kWarps];   // r-th largest of the lanes' largest values, per warp
   int count[kWarps];        // of the warps' lists
-  int total;
+  int total, found;
   float m[kWarps];
   double s[kWarps];
 };
@@ -159,22 +163,52 @@ __device__ __forceinline__ float to_f(T x) {
   else return x;
 }
 
-// kPer values from a 16-byte boundary.
+// A lane's values of one round, as loaded.
 template <typename T>
-__device__ __forceinline__ void load8(const T* p, float (&f)[kPer]) {
-  if constexpr (sizeof(T) == 2) {
-    const uint4 u = __ldcs(reinterpret_cast<const uint4*>(p));
-    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      f[2 * i] = __uint_as_float(w[i] << 16);
-      f[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-    }
-  } else {
-    const float4 a = __ldcs(reinterpret_cast<const float4*>(p)), b = __ldcs(reinterpret_cast<const float4*>(p) + 1);
-    f[0] = a.x, f[1] = a.y, f[2] = a.z, f[3] = a.w, f[4] = b.x, f[5] = b.y, f[6] = b.z, f[7] = b.w;
+struct Vec {
+  uint32_t w[8];
+  __device__ __forceinline__ void load(const T* p) {   // from a 32-byte boundary
+    asm volatile("ld.global.L1::no_allocate.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                 : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]), "=r"(w[4]), "=r"(w[5]), "=r"(w[6]), "=r"(w[7])
+                 : "l"(p));
   }
-}
+  __device__ __forceinline__ void load_part(const T* p, int n) {   // n < kPer values from anywhere
+    clear();
+#pragma unroll
+    for (int i = 0; i < kPer<T>; ++i)
+      if (i < n) {
+        if constexpr (sizeof(T) == 2) {
+          const uint32_t u = __bfloat16_as_ushort(p[i]);
+          w[i / 2] = i & 1 ? (w[i / 2] & 0xffffu) | u << 16 : (w[i / 2] & 0xffff0000u) | u;
+        } else {
+          w[i] = __float_as_uint(p[i]);
+        }
+      }
+  }
+  __device__ __forceinline__ void clear() {   // -inf
+#pragma unroll
+    for (int i = 0; i < 8; ++i) w[i] = sizeof(T) == 2 ? 0xff80ff80u : 0xff800000u;
+  }
+  __device__ __forceinline__ float max() const {   // of those that are numbers
+    if constexpr (sizeof(T) == 2) {
+      __nv_bfloat162 m[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        m[i] = __hmax2(reinterpret_cast<const __nv_bfloat162&>(w[2 * i]), reinterpret_cast<const __nv_bfloat162&>(w[2 * i + 1]));
+      m[0] = __hmax2(__hmax2(m[0], m[1]), __hmax2(m[2], m[3]));
+      return fmaxf(__low2float(m[0]), __high2float(m[0]));
+    } else {
+      float m = __uint_as_float(w[0]);
+#pragma unroll
+      for (int i = 1; i < 8; ++i) m = fmaxf(m, __uint_as_float(w[i]));
+      return m;
+    }
+  }
+  __device__ __forceinline__ uint64_t pair(int i) const {
+    if constexpr (sizeof(T) == 2) return f2_pack(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xffff0000u));
+    else return f2_pack(__uint_as_float(w[2 * i]), __uint_as_float(w[2 * i + 1]));
+  }
+};
 
 __device__ __forceinline__ bool live(float score, bool fin) { return !fin && isfinite(score); }
 
@@ -195,11 +229,13 @@ __global__ void __launch_bounds__(kThreads, 4) beam_scan_kernel(const T* __restr
   if (!live(scores[row], finished && finished[row])) return;   // the merge does not read this row's lists
 
   const T* x = logits + static_cast<long long>(row) * V;
-  // values before the first 16-byte boundary, then whole vectors of kPer, then the rest
-  const int head = min(V, static_cast<int>(((16 - (reinterpret_cast<uintptr_t>(x) & 15)) & 15) / sizeof(T)));
-  const int nvec = (V - head) / kPer;
+  // Vector 0 holds the values before the first 32-byte boundary, vectors 1 ..
+  // nvec kPer values each, and nvec + 1 the rest.
+  constexpr int P = kPer<T>;
+  const int head = min(V, static_cast<int>(((kVec - (reinterpret_cast<uintptr_t>(x) & (kVec - 1))) & (kVec - 1)) / sizeof(T)));
+  const int nvec = (V - head) / P;
   const int span = nvec / splits + 1;
-  const int v0 = min(nvec, split * span), v1 = min(nvec, v0 + span);
+  const int v0 = min(nvec, split * span), v1 = min(nvec, v0 + span);   // counted from vector 1
 
   uint64_t* buf = sm.buf[warp];
   const int r = (K + kWarps - 1) / kWarps;
@@ -216,10 +252,8 @@ __global__ void __launch_bounds__(kThreads, 4) beam_scan_kernel(const T* __restr
     }
     if (lane == 0) sm.lead[warp] = unordered(M);
   };
-  auto take = [&](const float (&f)[kPer], int idx, int round) {   // idx: index of f[0]; unused places hold -inf
-    float tm = f[0];
-#pragma unroll
-    for (int i = 1; i < kPer; ++i) tm = fmaxf(tm, f[i]);
+  auto take = [&](const Vec<T>& f, uint32_t id, int round) {
+    const float tm = f.max();
     if (__any_sync(full, tm > m + kSlack)) {
       float M = tm;
 #pragma unroll
@@ -229,15 +263,19 @@ __global__ void __launch_bounds__(kThreads, 4) beam_scan_kernel(const T* __restr
       minus_m = f2_pack(-m, -m);
     }
     // (nothing above -inf yet: every term is 0, or NaN)
-    uint64_t e2[kPer / 2];
+    uint64_t e2[P / 2];
 #pragma unroll
-    for (int i = 0; i < kPer / 2; ++i) {
+    for (int i = 0; i < P / 2; ++i) {
       float lo, hi;
-      f2_unpack(f2_mul(f2_add(f2_pack(f[2 * i], f[2 * i + 1]), minus_m), f2_pack(kLog2e, kLog2e)), lo, hi);
+      f2_unpack(f2_mul(f2_add(f.pair(i), minus_m), f2_pack(kLog2e, kLog2e)), lo, hi);
       e2[i] = f2_pack(ex2(lo), ex2(hi));
     }
+#pragma unroll
+    for (int o = P / 4; o; o >>= 1)
+#pragma unroll
+      for (int i = 0; i < o; ++i) e2[i] = f2_add(e2[i], e2[i + o]);
     float lo, hi;
-    f2_unpack(f2_add(f2_add(e2[0], e2[1]), f2_add(e2[2], e2[3])), lo, hi);
+    f2_unpack(e2[0], lo, hi);
     s += static_cast<double>(lo + hi);
     best = fmaxf(best, tm);
     if ((round & (round + 1)) == 0) {   // rounds 0, 1, 3, 7, ...
@@ -248,10 +286,7 @@ __global__ void __launch_bounds__(kThreads, 4) beam_scan_kernel(const T* __restr
       tv = fmaxf(tv, least);
     }
     if (__any_sync(full, tm >= tv && tm > -kInf)) {
-      if (tm >= tv)   // few lanes: each appends its own
-#pragma unroll
-        for (int i = 0; i < kPer; ++i)
-          if (f[i] >= tv && f[i] > -kInf) buf[atomicAdd(&sm.count[warp], 1)] = make_key(f[i], idx + i);
+      if (tm >= tv && tm > -kInf) buf[atomicAdd(&sm.count[warp], 1)] = make_key(tm, id);
       __syncwarp();
       const int count = sm.count[warp];
       if (count > kKeep) {
@@ -263,36 +298,31 @@ __global__ void __launch_bounds__(kThreads, 4) beam_scan_kernel(const T* __restr
     }
   };
 
-  float f[kPer], g[kPer];
-  auto load = [&](int vec, float (&d)[kPer]) {
-    if (vec < v1) load8(x + head + static_cast<long long>(vec) * kPer, d);
-    else
-#pragma unroll
-      for (int i = 0; i < kPer; ++i) d[i] = -kInf;
+  Vec<T> f, f1, f2;        // this round's values and, on their way, the next two rounds'
+  auto load = [&](int vec, Vec<T>& d) {
+    if (vec < v1) d.load(x + head + static_cast<long long>(vec) * P);
+    else d.clear();
   };
-  const int first = v0 + warp * 32;
-  load(first + lane, f);
-#pragma unroll
-  for (int i = 0; i < kPer; ++i) best = fmaxf(best, f[i]);
+  const int first = v0 + warp * 32 + lane;
+  load(first, f);
+  load(first + kThreads, f1);
   if (lane == 0) sm.count[warp] = 0;
+  best = fmaxf(best, f.max());
   announce();              // of the first round's values, so that few of them are listed
   __syncthreads();
   int round = 0;
 #pragma unroll 1
-  for (int vec = first; vec < v1; vec += kThreads, ++round) {
-    load(vec + kThreads + lane, g);   // the next round's values are on their way meanwhile
-    take(f, head + (vec + lane) * kPer, round);
-#pragma unroll
-    for (int i = 0; i < kPer; ++i) f[i] = g[i];
+  for (int vec = first; vec - lane < v1; vec += kThreads, ++round) {
+    load(vec + 2 * kThreads, f2);
+    take(f, vec + 1, round);
+    f = f1;
+    f1 = f2;
   }
-  if (warp == 0) {   // the ends: head values by the first span, tail values by the last (each fewer than one vector)
-    const int tail0 = head + nvec * kPer;
-    const int n_head = split == 0 ? head : 0, n_tail = split == splits - 1 ? V - tail0 : 0;
-    const int idx = lane < n_head ? lane : lane - n_head < n_tail ? tail0 + lane - n_head : -1;
-#pragma unroll
-    for (int i = 0; i < kPer; ++i) f[i] = -kInf;
-    if (idx >= 0) f[0] = to_f(x[idx]);
-    if (n_head + n_tail > 0) take(f, idx, round);
+  if (warp == 0) {   // the ends
+    const int tail = V - head - nvec * P;
+    const int n = lane == 0 && split == 0 ? head : lane == 1 && split == splits - 1 ? tail : 0;
+    f.load_part(lane == 0 ? x : x + V - tail, n);
+    if (__any_sync(full, n > 0)) take(f, lane == 0 ? 0 : nvec + 1, round);
   }
   // the CTA's list from what the warps' lists hold above the last threshold
   announce();
@@ -304,7 +334,7 @@ __global__ void __launch_bounds__(kThreads, 4) beam_scan_kernel(const T* __restr
     sm.m[warp] = m;
     sm.s[warp] = s;
   }
-  if (tid == 0) sm.total = 0;
+  if (tid == 0) sm.total = sm.found = 0;
   __syncthreads();
   float least = sm.lead[0];
 #pragma unroll
@@ -318,9 +348,32 @@ __global__ void __launch_bounds__(kThreads, 4) beam_scan_kernel(const T* __restr
     int rank = 0;
 #pragma unroll 4
     for (int j = 0; j < total; ++j) rank += sm.all[j] > key;
+    if (rank < K) sm.top[rank] = key;
+  }
+  __syncthreads();
+  // The K best values are among the K best vectors: whatever is left out has K
+  // vectors' maxima before it.
+  const int tops = min(total, K);
+  const float bound = tops == K ? key_value(sm.top[K - 1]) : -kInf;
+  uint64_t* found = sm.buf[0];
+  for (int i = tid; i < tops * P; i += kThreads) {
+    const uint32_t id = key_index(sm.top[i / P]), e = i % P;
+    const uint32_t idx = id == 0 ? e : head + (id - 1) * P + e;
+    if (idx < static_cast<uint32_t>(id == 0 ? head : V)) {
+      const float v = to_f(x[idx]);
+      if (v >= bound && v > -kInf) found[atomicAdd(&sm.found, 1)] = make_key(v, idx);
+    }
+  }
+  __syncthreads();
+  const int n = sm.found;
+  for (int i = tid; i < n; i += kThreads) {
+    const uint64_t key = found[i];
+    int rank = 0;
+#pragma unroll 4
+    for (int j = 0; j < n; ++j) rank += found[j] > key;
     if (rank < K) keys[at * K + rank] = key;
   }
-  for (int i = total + tid; i < K; i += kThreads) keys[at * K + i] = 0;
+  for (int i = n + tid; i < K; i += kThreads) keys[at * K + i] = 0;
 
   // maximum and sum of the CTA.  A NaN logit made its lane's sum NaN; +inf made inf - inf.
   if (warp == 0) {
@@ -572,9 +625,9 @@ __global__ void __launch_bounds__(kThreads) beam_merge_kernel(
 // Spans per row: three CTAs for every SM when the rows are fewer (512 rows of
 // 50257: 36 us in one span each, 43 us in two), spans of at least two rounds of
 // every warp, and no more list entries per request than one merge takes.
-int beam_splits(long long rows, int W, int V, int K) {
+int beam_splits(long long rows, int W, int V, int K, int per) {   // per: values of a vector
   const long long want = (static_cast<long long>(num_sms()) * 3 + rows - 1) / rows;
-  const long long by_len = std::max(1, V / (2 * kThreads * kPer));
+  const long long by_len = std::max(1, V / (2 * kThreads * per));
   const long long by_merge = std::max(1, kMergeMost / (W * K));
   return static_cast<int>(std::max(1LL, std::min({want, by_len, by_merge})));
 }
@@ -595,7 +648,7 @@ template <typename T>
 cudaError_t run_select(int G, int W, int V, int K, const void* logits, const float* scores, const unsigned char* fin,
                        int end_token, float* os, int* op, int* ot, char* ws, cudaStream_t st) {
   const long long rows = static_cast<long long>(G) * W;
-  const int splits = beam_splits(rows, W, V, K);
+  const int splits = beam_splits(rows, W, V, K, kPer<T>);
   const BeamWs o = beam_ws(rows, splits, K);
   auto* keys = reinterpret_cast<uint64_t*>(ws + o.keys);
   auto* ms = reinterpret_cast<float*>(ws + o.ms);
@@ -732,6 +785,7 @@ ia_status_t check_reorder(int B, int win, int wout, const int* parents, const vo
   return IA_OK;
 }
 
+int per_vector(ia_dtype_t dt) { return dt == IA_F32 ? kPer<float> : kPer<__nv_bfloat16>; }
 bool valid_beam(int G, int W, int V, int K, ia_dtype_t dt) {
   return G > 0 && W > 0 && W <= kMaxW && V > 0 && K > 0 && K <= kMaxK && (dt == IA_F32 || dt == IA_BF16);
 }
@@ -746,7 +800,7 @@ extern "C" {
 size_t ia_beam_select_workspace_bytes(int G, int W, int V, int K, ia_dtype_t dtype) {
   if (!valid_beam(G, W, V, K, dtype)) return 0;
   const long long rows = static_cast<long long>(G) * W;
-  return beam_ws(rows, beam_splits(rows, W, V, K), K).total;
+  return beam_ws(rows, beam_splits(rows, W, V, K, per_vector(dtype)), K).total;
 }
 
 ia_status_t ia_beam_select(int G, int W, int V, int K, ia_dtype_t dtype, const void* logits, const float* scores,
@@ -758,7 +812,7 @@ ia_status_t ia_beam_select(int G, int W, int V, int K, ia_dtype_t dtype, const v
   for (const void* p : ptrs)
     if (p && !aligned16(p)) return IA_ERR_INVALID_ARG;
   if (finished && (end_token < 0 || end_token >= V)) return IA_ERR_INVALID_ARG;
-  if (static_cast<long long>(G) * W * beam_splits(static_cast<long long>(G) * W, W, V, K) > (1LL << 31) - 1)
+  if (static_cast<long long>(G) * W * beam_splits(static_cast<long long>(G) * W, W, V, K, per_vector(dtype)) > (1LL << 31) - 1)
     return IA_ERR_UNSUPPORTED;   // one block per row and span
   if (!workspace || workspace_bytes < ia_beam_select_workspace_bytes(G, W, V, K, dtype)) return IA_ERR_WORKSPACE;
   if (inject_launch_failure()) return IA_ERR_CUDA;
