@@ -4,17 +4,28 @@
 // Selection.  Candidate (w, t) of a request scores
 //   scores[w] + x[w][t] - lse_w,   lse_w = log sum_t exp(x[w][t]).
 // Within a beam the order is that of x, so a beam's K best tokens need no
-// lse, and the scan kernel finds both in one pass over the logits (which HBM
-// bounds): a CTA takes a span of one row, its warps interleaved.  A warp
-// appends the values that reach a threshold to its list in shared memory,
-// without a barrier.  The threshold costs next to nothing: every
-// lane keeps the largest value it has seen, a warp takes the r-th largest of
-// its lanes' (of the first round before any is listed, then after 2, 4, 8, ... rounds) and the least of the eight warps'
-// is reached by at least 8 r >= K values of the span.  About 40 (1 + ln n)
-// values of n rounds reach it for K = 16.  A list that grows past 128 all the
-// same (ties, ascending rows) is cut back to its K best.  The merge kernel,
-// one CTA per request, adds the spans' sums and picks the K best of the rows'
-// lists.
+// lse, and the scan kernel finds both in one pass over the logits: a CTA takes
+// a span of one row, its warps interleaved, each lane a vector of 32 bytes a
+// round.  What is listed is the vector, by its largest value, as the K best
+// values lie in the K best vectors: a lane whose vector reaches a threshold
+// appends it to its warp's list in shared memory, without a barrier, and only
+// the last K are taken apart.  (With every value listed by itself a round ran
+// twice the instructions.)  The threshold: every lane keeps the largest value
+// it has seen, a warp takes the r-th largest of its lanes' (of the first round
+// before any is listed, then after 2, 4, 8, ... rounds), and the least of the
+// eight warps' is reached by at least 8 r >= K vectors of the span.  About
+// 40 (1 + ln n) vectors of n rounds reach it for K = 16.  A list that grows past
+// 128 all the same (ties, ascending rows) is cut back to its K best.  The merge
+// kernel, one CTA per request, adds the spans' sums and picks the K best of the
+// rows' lists.
+//
+// Bound.  Reading the logits once would take 7.9 us for 64 x 8 x 50257 in bf16 and
+// 15.7 in fp32; both kernels take 23.4 and 31.1 (34.4 and 31.1 with 16 bytes a
+// round and values listed).  Instructions bound the scan: unpacking, maximum,
+// exponential and sum of 16 values are some 110 of the 130 that a warp runs a
+// round; 512 rows on 592 places leave 3 or 4 CTAs on an SM, and beginning and
+// end of a row, which no other row's rounds cover, are 5 us of it.  The loads
+// are one round ahead; two ahead move more registers than they hide (24.5 us).
 //
 // Order keys.  (value, lower index first) is one 64-bit number: the fp32 value
 // mapped to an order-preserving integer above the complement of the index.
@@ -226,8 +237,8 @@ __global__ void __launch_bounds__(kThreads, 4) beam_scan_kernel(const T* __restr
   const unsigned at = blockIdx.x, row = at / static_cast<unsigned>(splits);
   const int split = static_cast<int>(at - row * splits);
   griddep_launch_dependents();
-  if (!live(scores[row], finished && finished[row])) return;   // the merge does not read this row's lists
-
+  const float score = scores[row];
+  const bool fin = finished && finished[row];
   const T* x = logits + static_cast<long long>(row) * V;
   // Vector 0 holds the values before the first 32-byte boundary, vectors 1 ..
   // nvec kPer values each, and nvec + 1 the rest.
@@ -236,6 +247,15 @@ __global__ void __launch_bounds__(kThreads, 4) beam_scan_kernel(const T* __restr
   const int nvec = (V - head) / P;
   const int span = nvec / splits + 1;
   const int v0 = min(nvec, split * span), v1 = min(nvec, v0 + span);   // counted from vector 1
+
+  Vec<T> f, f1;            // this round's values and, on their way, the next one's
+  auto load = [&](int vec, Vec<T>& d) {
+    if (vec < v1) d.load(x + head + static_cast<long long>(vec) * P);
+    else d.clear();
+  };
+  const int first = v0 + warp * 32 + lane;
+  load(first, f);
+  if (!live(score, fin)) return;   // the merge does not read this row's lists
 
   uint64_t* buf = sm.buf[warp];
   const int r = (K + kWarps - 1) / kWarps;
@@ -271,12 +291,11 @@ __global__ void __launch_bounds__(kThreads, 4) beam_scan_kernel(const T* __restr
       e2[i] = f2_pack(ex2(lo), ex2(hi));
     }
 #pragma unroll
-    for (int o = P / 4; o; o >>= 1)
-#pragma unroll
-      for (int i = 0; i < o; ++i) e2[i] = f2_add(e2[i], e2[i + o]);
-    float lo, hi;
-    f2_unpack(e2[0], lo, hi);
-    s += static_cast<double>(lo + hi);
+    for (int i = 0; i < P / 2; i += 4) {   // 8 terms at a time
+      float lo, hi;
+      f2_unpack(f2_add(f2_add(e2[i], e2[i + 1]), f2_add(e2[i + 2], e2[i + 3])), lo, hi);
+      s += static_cast<double>(lo + hi);
+    }
     best = fmaxf(best, tm);
     if ((round & (round + 1)) == 0) {   // rounds 0, 1, 3, 7, ...
       if (round > 0) announce();
@@ -298,14 +317,6 @@ __global__ void __launch_bounds__(kThreads, 4) beam_scan_kernel(const T* __restr
     }
   };
 
-  Vec<T> f, f1, f2;        // this round's values and, on their way, the next two rounds'
-  auto load = [&](int vec, Vec<T>& d) {
-    if (vec < v1) d.load(x + head + static_cast<long long>(vec) * P);
-    else d.clear();
-  };
-  const int first = v0 + warp * 32 + lane;
-  load(first, f);
-  load(first + kThreads, f1);
   if (lane == 0) sm.count[warp] = 0;
   best = fmaxf(best, f.max());
   announce();              // of the first round's values, so that few of them are listed
@@ -313,10 +324,9 @@ __global__ void __launch_bounds__(kThreads, 4) beam_scan_kernel(const T* __restr
   int round = 0;
 #pragma unroll 1
   for (int vec = first; vec - lane < v1; vec += kThreads, ++round) {
-    load(vec + 2 * kThreads, f2);
+    load(vec + kThreads, f1);
     take(f, vec + 1, round);
     f = f1;
-    f1 = f2;
   }
   if (warp == 0) {   // the ends
     const int tail = V - head - nvec * P;

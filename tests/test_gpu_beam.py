@@ -55,6 +55,19 @@ def test_ties_go_to_the_lowest_index(dt):
     assert check(z, torch.zeros(1, 1, device="cuda"), 4)["tokens"].tolist() == [[2, 0, 1, 3]]
 
 
+@pytest.mark.parametrize("dt", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("V", [1, 2, 7, 8, 9, 15, 16, 17, 31, 33, 47, 4111])
+def test_few_distinct_values(dt, V):
+    """Ties across the boundaries of the scan's vectors, whose rows begin at every alignment."""
+    device()
+    g = torch.Generator().manual_seed(V)
+    x = torch.randint(0, 3, (3, 7, V), generator=g).to(dt).cuda()
+    x[1, :, : V // 2] = -INF
+    x[2, 0] = -1.0
+    check(x, -torch.arange(21, dtype=torch.float32, device="cuda").view(3, 7) * 7, 64)
+    check(x, -torch.arange(21, dtype=torch.float32, device="cuda").view(3, 7) * 7, 5)
+
+
 def test_ordered_rows():
     """Ascending logits keep replacing the best so far; descending ones never do."""
     device()
