@@ -8,15 +8,17 @@
 //   G1  A  = X Y^T            128 x 128 x dx   operands straight from TMA
 //   G2  O2 = P Z              128 x 64 x 128   P = decayed, masked A, from TMEM
 //   G3  O1 = X S              128 x 64 x dx    S = the entering state in bf16
-//   G4  K  = Y^T (w Z)        dx x 64 x 256    w z in two bf16 parts
+//   G4  K  = Y^T (w Z)        dx x 64 x 256    w z in two bf16 parts, or three
 //   out = scale (O2 + lambda^(p+1) O1),  S <- lambda^L S + K in fp32 registers
 //
 // Rounding.  Decays multiply fp32 accumulators wherever they can: A before it
 // is rounded to P, O1 after the product, S in registers.  Only the weights
-// w = lambda^(L-1-p) of G4 sit on a contracted index; w z is split into hi +
-// lo bf16 parts (2^-16 of a value left over), so that the fp32 state that is
-// carried and returned keeps fp32-like accuracy.  P and the S operand are
-// rounded to bf16 once, like the output.
+// w = lambda^(L-1-p) of G4 sit on a contracted index, and w z is split into
+// bf16 parts.  Where the caller takes the final state in fp32 there are three
+// (2^-25 of a value left over): the state is off by 1.4e-7 (N = 2048, d = 64) to
+// 3.8e-7 (d = 128), less than token by token in fp32 (6e-7).  Where the state only
+// feeds outputs of 8 bits there are two (2^-17 left over, 2.5e-6).  P and the S
+// operand are rounded to bf16 once, like the output.
 //
 // Roles (448 threads, four warps at most on a quarter of the registers: 128 a
 // thread; or 576, five warps: 96):
@@ -25,7 +27,9 @@
 //               columns that end at e <= t: both factors <= 1 and constant per
 //               thread.  Groups on the other side of the diagonal are zero and
 //               not read.
-//   warps 4-7   O: O1, O2 from TMEM, out through shared memory and a TMA store
+//   warps 4-7   O: O1, O2 from TMEM, out through shared memory and TMA stores,
+//               each warp its 32 rows by itself (stores straight from the
+//               registers, 32 bytes a lane, were 5 % slower)
 //   warps 8-11  S: K from TMEM, S in registers, S in bf16 to shared memory for
 //               the next chunk's G3
 //   warps 12-15 W: w z for G4 (where there are none, O does it; a pass for the
@@ -61,20 +65,29 @@ constexpr int kRoleThreads = 128;
 // registers a thread), else by the output warps.
 constexpr bool has_w(int maxdx, bool state_only) { return maxdx == 64 && !state_only; }
 constexpr int threads(int maxdx, bool state_only) { return (has_w(maxdx, state_only) ? 4 : 3) * kRoleThreads + 64; }
+constexpr int kBad = 8;                 // chunks whose marks of NaN are kept apart
 constexpr uint32_t kAtom = 1024;        // 8 rows of 128 bytes
 
-template <int MAXDX, bool STATE_ONLY>
+template <int MAXDX, bool STATE_ONLY, int PARTS>
 struct Cfg {
-  static constexpr int NX = STATE_ONLY ? 0 : MAXDX == 64 ? 3 : 2;   // stages of X, released late (by G3)
-  static constexpr int NY = STATE_ONLY ? 3 : 2;         // and of Y, released by G4
-  static constexpr int NT = STATE_ONLY || MAXDX == 64 ? 3 : 2;      // stages of Z, needed first and released last
-  static constexpr int NZ = STATE_ONLY || MAXDX == 64 ? 2 : 1;      // buffers of w z
+  // Stages.  X is released late (by G3), Y by G4; Z is needed first and released
+  // last.  What the third part of w z takes comes from X and, at d = 64, from
+  // half of the output tile (prefill of B8 H16 N2048 d64: 29.5 us with two parts,
+  // 33.9 with three; with one buffer of w z and three stages of X 37.4, with two
+  // stages of Z and three of X 39.5.  B4 H16 d128: 40.2 and 42.9; with two stages of
+  // X and no output tile 46.7).
+  static constexpr bool kFull3 = PARTS == 3 && !STATE_ONLY;
+  static constexpr int NX = STATE_ONLY ? 0 : MAXDX == 64 ? (kFull3 ? 2 : 3) : kFull3 ? 1 : 2;
+  static constexpr int NY = STATE_ONLY && PARTS == 2 ? 3 : 2;
+  static constexpr int NT = MAXDX == 64 || STATE_ONLY || kFull3 ? 3 : 2;
+  static constexpr int NZ = MAXDX == 64 || STATE_ONLY ? 2 : 1;         // buffers of w z
+  static constexpr int kOutCols = kFull3 && MAXDX == 64 ? 32 : 64;     // columns staged for a store
   // TMEM columns (A twice, with P in its place).  With wide X a second O1 lets
-  // G3 go first, so that X's stage is loaded again early: its two stages hide
-  // the load no longer (forward of B4 H16 N2048 d128 44.6 us without, 41.5
-  // with).  That leaves 64 columns for K, whose two parts are then contracted
-  // one after the other (16 products instead of 8 twice as wide); with d = 64
-  // and three stages this costs more than it gives (27.1 us, and 27.8).
+  // G3 go first, so that X's stage is loaded again early: its stages alone do
+  // not hide the load (forward of B4 H16 N2048 d128 44.6 us without, 41.5 with).
+  // That leaves 64 columns for K, whose parts are then contracted one after the
+  // other (16 products instead of 8 twice as wide); with d = 64 and three stages
+  // this costs more than it gives (B8 H12 N2048: 27.1 us, and 27.8).
   static constexpr bool kO1Twice = MAXDX == 128 && !STATE_ONLY;
   static constexpr uint32_t kTA = 0, kTO1 = 256, kTO2 = kO1Twice ? 384 : 320, kTK = kO1Twice ? 448 : 384;
   // Every problem has dx = 64, and K 64 rows: a third less of shared memory is
@@ -83,13 +96,14 @@ struct Cfg {
   static constexpr int TX = MAXDX / 64 * kBox;
   static constexpr int S_Y = NX * TX;
   static constexpr int S_Z = S_Y + NY * TX;
-  static constexpr int S_ZW = S_Z + NT * kBox;          // each: hi, lo
-  static constexpr int S_SB = S_ZW + NZ * 2 * kBox;     // [dx][64] bf16, 128-byte swizzled
+  static constexpr int S_ZW = S_Z + NT * kBox;          // each: its parts
+  static constexpr int S_SB = S_ZW + NZ * PARTS * kBox; // [dx][64] bf16, 128-byte swizzled
   static constexpr int S_OUT = S_SB + (STATE_ONLY ? 0 : MAXDX * 128);
-  static constexpr int S_BAR = S_OUT + (STATE_ONLY ? 0 : kBox);
-  static constexpr int S_POW = S_BAR + 288;             // lambda^n, n = 0 .. C - 1
+  static constexpr int S_BAR = S_OUT + (STATE_ONLY ? 0 : C * 2 * kOutCols);
+  static constexpr int S_POW = S_BAR + 304;             // lambda^n, n = 0 .. C - 1
   static constexpr int SMEM = S_POW + C * 4 + 1024;     // + alignment of the base
   static_assert(NX <= 3 && NY <= 3 && NT <= 3 && NZ <= 2, "their barriers");
+  static_assert(SMEM <= 232448, "what a CTA may have");
 };
 
 enum Bar {
@@ -98,10 +112,11 @@ enum Bar {
 };
 
 struct Maps {
-  CUtensorMap m[8];    // q, k, v, dO and o, dq, dk, dv (a prefill: q, k, v and o at 4)
+  CUtensorMap in[4];    // q, k, v, dO
+  CUtensorMap out[4];   // by problem
 };
 struct MapIdx {
-  int x, y, z, out;
+  int x, y, z;
 };
 struct TcParams {
   LinArgs a;
@@ -170,10 +185,10 @@ __host__ __device__ constexpr uint32_t idesc_bf16(int M, int N, int a_mn, int b_
   return idesc_f16(M, N, a_mn, b_mn) | (1u << 7) | (1u << 10);
 }
 
-template <int MAXDX, bool STATE_ONLY>
+template <int MAXDX, bool STATE_ONLY, int PARTS>
 __global__ void __launch_bounds__(has_w(MAXDX, STATE_ONLY) ? 640 : 512, 1) lin_tc_kernel(const __grid_constant__ TcParams prm,
                                                         const __grid_constant__ Maps maps) {
-  using K = Cfg<MAXDX, STATE_ONLY>;
+  using K = Cfg<MAXDX, STATE_ONLY, PARTS>;
   constexpr int kNX = K::NX ? K::NX : 1, NY = K::NY, NT = K::NT;
   constexpr bool kW = has_w(MAXDX, STATE_ONLY);
   // The state-only pass has room for two K, so that one is contracted while the
@@ -207,8 +222,8 @@ __global__ void __launch_bounds__(has_w(MAXDX, STATE_ONLY) ? 640 : 512, 1) lin_t
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + K::S_BAR);
   uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(smem + K::S_BAR + 8 * kBars);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + K::S_BAR + 8 * kBars + 4);
-  int* bad = reinterpret_cast<int*>(smem + K::S_BAR + 8 * kBars + 8);   // [4]
-  static_assert(8 * kBars + 24 <= 288, "barriers and flags fit their slot");
+  int* bad = reinterpret_cast<int*>(smem + K::S_BAR + 8 * kBars + 8);   // [kBad]
+  static_assert(8 * kBars + 8 + 4 * kBad <= 304, "barriers and flags fit their slot");
   const uint32_t sbase = smem_u32(smem);
   auto sX = [&](int c) { return (c % kNX) * K::TX; };
   auto sY = [&](int c) { return K::S_Y + (c % NY) * K::TX; };
@@ -225,7 +240,7 @@ __global__ void __launch_bounds__(has_w(MAXDX, STATE_ONLY) ? 640 : 512, 1) lin_t
       const bool warps8 = STATE_ONLY && (i == kZReady || i == kZReady + 1);
       mbar_init(bars + i, warps8 ? 8 : warps4 ? 4 : 1);
     }
-    for (int i = 0; i < 4; ++i) bad[i] = C;
+    for (int i = 0; i < kBad; ++i) bad[i] = C;
     *abort_flag = 0;
     fence_barrier_init();
   }
@@ -246,12 +261,12 @@ __global__ void __launch_bounds__(has_w(MAXDX, STATE_ONLY) ? 640 : 512, 1) lin_t
   // one outcome for a warp: what follows is warp-wide
   auto warp_wait = [&](int bar, uint32_t parity) { return __all_sync(0xffffffffu, wait(bar, parity)) != 0; };
 
-  // w z of chunk c (of a half in the state-only pass) in two bf16 parts, at z's
-  // own offsets (row = token); u: the thread among its role's 128
+  // w z of chunk c (of a half in the state-only pass) in bf16 parts, at z's own
+  // offsets (row = token); u: the thread among its role's 128
   auto weigh = [&](int c, int u, int half) -> bool {
     constexpr int kIter = STATE_ONLY ? 4 : 8;
     const int L = min(C, a.N - chunk_at(c) * C);
-    uint8_t* zw = smem + K::S_ZW + (c % K::NZ) * 2 * kBox;
+    uint8_t* zw = smem + K::S_ZW + (c % K::NZ) * PARTS * kBox;
     const uint8_t* zs = smem + sZ(c);
     if (c >= K::NZ && !warp_wait(kZFree + c % K::NZ, c / K::NZ - 1)) return false;   // G4 has read the buffer
     if (!warp_wait(kFullZ + c % NT, c / NT)) return false;
@@ -266,16 +281,20 @@ __global__ void __launch_bounds__(has_w(MAXDX, STATE_ONLY) ? 640 : 512, 1) lin_t
       if (i + 1 < kIter) zn = *reinterpret_cast<const uint4*>(zs + off + 16 * kRoleThreads);
       const float wt = t < L ? pw[rev ? t : L - 1 - t] : 0.f;
       const uint64_t w2 = f2_pack(wt, wt), minus = f2_pack(-1.f, -1.f);
-      uint32_t hi[4], lo[4];
+      uint32_t part[PARTS][4];
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         probe = __hfma2(*reinterpret_cast<const __nv_bfloat162*>(&zz[e]), zero, probe);
-        const uint64_t v = f2_mul(f2_pack(bf_lo(zz[e]), bf_hi(zz[e])), w2);
-        hi[e] = pack2(v);
-        lo[e] = pack2(f2_fma(f2_pack(bf_lo(hi[e]), bf_hi(hi[e])), minus, v));
+        uint64_t v = f2_mul(f2_pack(bf_lo(zz[e]), bf_hi(zz[e])), w2);
+#pragma unroll
+        for (int k = 0; k < PARTS; ++k) {
+          part[k][e] = pack2(v);
+          if (k + 1 < PARTS) v = f2_fma(f2_pack(bf_lo(part[k][e]), bf_hi(part[k][e])), minus, v);   // exact
+        }
       }
-      *reinterpret_cast<uint4*>(zw + off) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-      *reinterpret_cast<uint4*>(zw + kBox + off) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+#pragma unroll
+      for (int k = 0; k < PARTS; ++k)
+        *reinterpret_cast<uint4*>(zw + k * kBox + off) = make_uint4(part[k][0], part[k][1], part[k][2], part[k][3]);
       off += 16 * kRoleThreads;
       t += 16;
     }
@@ -292,7 +311,7 @@ __global__ void __launch_bounds__(has_w(MAXDX, STATE_ONLY) ? 640 : 512, 1) lin_t
         if ((x & 0x7f800000u) == 0x7f800000u) x &= 0x0000ffffu;
         if (x != *z) {
           *z = x;
-          atomicMin(bad + (c & 3), rev ? C - 1 - tt : tt);
+          atomicMin(bad + c % kBad, rev ? C - 1 - tt : tt);
         }
       }
     }
@@ -364,8 +383,27 @@ __global__ void __launch_bounds__(has_w(MAXDX, STATE_ONLY) ? 640 : 512, 1) lin_t
     const int p = rev ? C - 1 - u : u;
     const float hd = a.scale * expf(g * (p + 1));
     const uint64_t scale2 = f2_pack(a.scale, a.scale), hd2 = f2_pack(hd, hd);
-    const CUtensorMap* mo = &maps.m[prm.mi[pi].out];
-    uint8_t* row = smem + K::S_OUT + u * 128;
+    const CUtensorMap* mo = &maps.out[pi];
+    constexpr int kRow = 2 * K::kOutCols;                  // bytes; a warp stages its 32 rows of them
+    uint8_t* stage = smem + K::S_OUT + u * kRow;
+    const int swz = K::kOutCols == 64 ? u & 7 : (u >> 1) & 3;
+    auto stage_free = [&]() {   // the warp's last store has left its rows
+      if (lane == 0) bulk_wait_read_0();
+      __syncwarp();
+    };
+    auto stage_out = [&](int col, int t0, bool last) {
+      fence_async_smem();
+      if (last) tc_fence_before();
+      __syncwarp();
+      if (lane == 0) {
+        if (last) mbar_arrive(bars + kOFree);
+        const int t = t0 + 32 * (warp - 4);
+        if (t < a.N) {
+          tma_store_3d(mo, sbase + K::S_OUT + (warp - 4) * 32 * kRow, col, t, bh);
+          bulk_commit();
+        }
+      }
+    };
 #pragma unroll 1
     for (int c = -1; c < n; ++c) {
       if (!kW && c + 1 < n) alive = alive && weigh(c + 1, u, STATE_ONLY);
@@ -374,15 +412,17 @@ __global__ void __launch_bounds__(has_w(MAXDX, STATE_ONLY) ? 640 : 512, 1) lin_t
         if (!alive) break;
         continue;
       }
-      const bool ok = alive && warp_wait(kOFull, c);
-      const int from = *reinterpret_cast<volatile int*>(bad + (c & 3));
-      if (u == 0) bulk_wait_read_0();                      // the last store has left the staging tile
-      if (named_sync_or(1, kRoleThreads, !ok)) break;      // one outcome for the role
+      if (!alive || !warp_wait(kOFull, c)) break;
       tc_fence_after();
-      if (u == 0 && from < C) bad[c & 3] = C;              // all have read it; its next use follows this chunk's kOFree
+      const int from = *reinterpret_cast<volatile int*>(bad + c % kBad);
+      if (u == 0) bad[(c + kBad - 1) % kBad] = C;   // the last chunk's: every warp has read it before this kOFull
       const uint32_t to = tmem + (static_cast<uint32_t>(warp - 4) << 21);
+      const int t0 = chunk_at(c) * C;
+      if (K::kOutCols == 64) stage_free();
 #pragma unroll 1
       for (int q = 0; q < 4; ++q) {
+        const int at = K::kOutCols == 64 ? q : q & 1;      // 32-byte piece of the staged row
+        if (K::kOutCols == 32 && at == 0) stage_free();
         uint32_t v1[16], v2[16], w[8];
         tmem_ld16(to + K::kTO1 + (K::kO1Twice ? 64 * (c & 1) : 0) + 16 * q, v1);
         tmem_ld16(to + K::kTO2 + 16 * q, v2);
@@ -398,19 +438,13 @@ __global__ void __launch_bounds__(has_w(MAXDX, STATE_ONLY) ? 640 : 512, 1) lin_t
         if (p >= from)
 #pragma unroll
           for (int i = 0; i < 8; ++i) w[i] = 0x7fc07fc0u;   // NaN
-        *reinterpret_cast<uint4*>(row + (((2 * q) ^ (u & 7)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
-        *reinterpret_cast<uint4*>(row + (((2 * q + 1) ^ (u & 7)) << 4)) = make_uint4(w[4], w[5], w[6], w[7]);
+        *reinterpret_cast<uint4*>(stage + (((2 * at) ^ swz) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
+        *reinterpret_cast<uint4*>(stage + (((2 * at + 1) ^ swz) << 4)) = make_uint4(w[4], w[5], w[6], w[7]);
+        if (K::kOutCols == 32 && q == 1) stage_out(z0, t0, false);
       }
-      tc_fence_before();
-      fence_async_smem();
-      named_sync(1, kRoleThreads);
-      if (u == 0) {
-        tma_store_3d(mo, sbase + K::S_OUT, z0, chunk_at(c) * C, bh);
-        bulk_commit();
-      }
-      if (lane == 0) mbar_arrive(bars + kOFree);
+      stage_out(K::kOutCols == 64 ? z0 : z0 + 32, t0, true);
     }
-    if (u == 0) bulk_wait_all();
+    if (lane == 0) bulk_wait_all();
   } else if (warp < 12) {
     // ------------------------------------------------------------------- S
     // The accumulator K of dx = 64 has M = 64 rows, in lanes 0-15 of each warp's
@@ -502,7 +536,7 @@ __global__ void __launch_bounds__(has_w(MAXDX, STATE_ONLY) ? 640 : 512, 1) lin_t
   } else if (warp == (kW ? 16 : 12)) {
     // ---------------------------------------------------------------- loads
     if (elect_one()) {
-      const CUtensorMap *mx = &maps.m[prm.mi[pi].x], *my = &maps.m[prm.mi[pi].y], *mz = &maps.m[prm.mi[pi].z];
+      const CUtensorMap *mx = &maps.in[prm.mi[pi].x], *my = &maps.in[prm.mi[pi].y], *mz = &maps.in[prm.mi[pi].z];
       int issued_z = 0, issued_y = 0, issued_x = 0;
       auto fetch = [&](int bar, int dst, const CUtensorMap* m, int boxes, int col, int t0) {
         mbar_arrive_expect_tx(bars + bar, boxes * kBox);
@@ -567,12 +601,21 @@ __global__ void __launch_bounds__(has_w(MAXDX, STATE_ONLY) ? 640 : 512, 1) lin_t
         // (beside wider problems, the rows of K past dx = 64 are taken from the
         // next tile in shared memory and never read)
         const int zb = c % K::NZ;
-        const uint64_t y = mnmajor(sY(c)), zw = mnmajor(K::S_ZW + zb * 2 * kBox);
-        constexpr int kSteps = K::kO1Twice ? 16 : 8;   // hi then lo, or side by side
+        const uint64_t y = mnmajor(sY(c)), zw = mnmajor(K::S_ZW + zb * PARTS * kBox);
+        if (K::kO1Twice) {   // the parts one after the other
 #pragma unroll 4
-        for (int kk = 0; kk < kSteps; ++kk)
-          mma_ss(lead, tmem + k_col(c), y + (kk & 7) * kTok, zw + kk * kTok,
-                 idesc_bf16(K::kHalf ? 64 : 128, 128 * 8 / kSteps, 1, 1), kk > 0);
+          for (int kk = 0; kk < 8 * PARTS; ++kk)
+            mma_ss(lead, tmem + k_col(c), y + (kk & 7) * kTok, zw + kk * kTok, idesc_bf16(128, 64, 1, 1), kk > 0);
+        } else {             // the first two side by side, the third into the second's columns
+#pragma unroll 4
+          for (int kk = 0; kk < 8; ++kk)
+            mma_ss(lead, tmem + k_col(c), y + kk * kTok, zw + kk * kTok, idesc_bf16(K::kHalf ? 64 : 128, 128, 1, 1), kk > 0);
+          if (PARTS == 3)
+#pragma unroll 4
+            for (int kk = 0; kk < 8; ++kk)
+              mma_ss(lead, tmem + k_col(c) + 64, y + kk * kTok, zw + ((2 * kBox) >> 4) + kk * kTok,
+                     idesc_bf16(K::kHalf ? 64 : 128, 64, 1, 1), 1);
+        }
         commit_to(lead, bars + k_full(c));
         commit_to(lead, bars + kZFree + zb);
         commit_to(lead, bars + kFreeY + c % NY);   // G1 of this chunk came before
@@ -636,29 +679,35 @@ __global__ void __launch_bounds__(has_w(MAXDX, STATE_ONLY) ? 640 : 512, 1) lin_t
   if (warp == 0) tmem_dealloc(tmem, 512);
 }
 
-// [BH][N][W] bf16 as boxes of 64 columns x 128 tokens of one (b,h), 128-byte
-// swizzled; tokens past N read as zero and are not written.
-bool encode_map(CUtensorMap* m, const void* x, int BH, int N, int W) {
+// [BH][N][W] bf16 as boxes of `cols` (64 or 32) columns x `rows` tokens of one
+// (b,h), swizzled over the box's row; tokens past N read as zero and are not
+// written.
+bool encode_map(CUtensorMap* m, const void* x, int BH, int N, int W, int rows, int cols) {
   const EncodeTiledFn enc = encode_tiled();
   if (!enc) return false;
   const cuuint64_t dims[3] = {static_cast<cuuint64_t>(W), static_cast<cuuint64_t>(N), static_cast<cuuint64_t>(BH)};
   const cuuint64_t strides[2] = {static_cast<cuuint64_t>(W) * 2, static_cast<cuuint64_t>(N) * W * 2};
-  const cuuint32_t box[3] = {64, C, 1};
+  const cuuint32_t box[3] = {static_cast<cuuint32_t>(cols), static_cast<cuuint32_t>(rows), 1};
   const cuuint32_t estr[3] = {1, 1, 1};
   return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(x), dims, strides, box, estr,
-             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
-             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+             CU_TENSOR_MAP_INTERLEAVE_NONE, cols == 64 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+             CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int MAXDX>
-cudaError_t launch(const TcParams& prm, const Maps& maps, bool state_only, cudaStream_t st) {
+template <int MAXDX, bool STATE_ONLY, int PARTS>
+cudaError_t launch(const TcParams& prm, const Maps& maps, cudaStream_t st) {
   const LinArgs& a = prm.a;
-  const long long grid = static_cast<long long>(a.BH) * a.first[a.nprob] * (state_only ? a.nseg - 1 : a.nseg);
+  const long long grid = static_cast<long long>(a.BH) * a.first[a.nprob] * (STATE_ONLY ? a.nseg - 1 : a.nseg);
   if (grid > (1LL << 31) - 1) return cudaErrorInvalidConfiguration;
-  auto kern = state_only ? lin_tc_kernel<MAXDX, true> : lin_tc_kernel<MAXDX, false>;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (state_only ? Cfg<MAXDX, true>::SMEM : Cfg<MAXDX, false>::SMEM));
-  if (e != cudaSuccess) return e;
-  return launch_after(kern, static_cast<unsigned>(grid), threads(MAXDX, state_only), (state_only ? Cfg<MAXDX, true>::SMEM : Cfg<MAXDX, false>::SMEM), st, a.nseg > 1 && !state_only, prm, maps);
+  constexpr int kSmem = Cfg<MAXDX, STATE_ONLY, PARTS>::SMEM;
+  auto kern = lin_tc_kernel<MAXDX, STATE_ONLY, PARTS>;
+  if (cudaError_t e = allow_smem(kern, kSmem); e != cudaSuccess) return e;
+  return launch_after(kern, static_cast<unsigned>(grid), threads(MAXDX, STATE_ONLY), kSmem, st, a.nseg > 1 && !STATE_ONLY, prm, maps);
+}
+template <int MAXDX>
+cudaError_t launch(const TcParams& prm, const Maps& maps, bool state_only, bool keep_state, cudaStream_t st) {
+  if (state_only) return keep_state ? launch<MAXDX, true, 3>(prm, maps, st) : launch<MAXDX, true, 2>(prm, maps, st);
+  return keep_state ? launch<MAXDX, false, 3>(prm, maps, st) : launch<MAXDX, false, 2>(prm, maps, st);
 }
 
 }  // namespace
@@ -671,23 +720,31 @@ cudaError_t launch_lin_tc(const LinArgs& a, bool state_only, cudaStream_t st) {
   TcParams prm = {};
   prm.a = a;
   Maps maps;
-  const void* seen[8] = {};
-  int width[8] = {}, count = 0, maxdx = 0;
-  auto index = [&](const void* x, int W) {   // one map per tensor, whichever roles it has
+  int maxdx = 0;
+  bool keep_state = false;
+  for (int i = 0; i < a.nprob; ++i) {
+    maxdx = std::max(maxdx, a.p[i].dx);
+    keep_state = keep_state || a.p[i].state_out;
+  }
+  const int out_cols = maxdx == 64 && keep_state ? Cfg<64, false, 3>::kOutCols : Cfg<64, false, 2>::kOutCols;
+  static_assert(Cfg<128, false, 3>::kOutCols == Cfg<64, false, 2>::kOutCols && Cfg<128, false, 2>::kOutCols == Cfg<64, false, 2>::kOutCols);
+  const void* seen[4] = {};
+  int width[4] = {}, count = 0;
+  auto input = [&](const void* x, int W) {   // one map per tensor, whichever roles it has
     for (int i = 0; i < count; ++i)
       if (seen[i] == x && width[i] == W) return i;
-    if (count == 8 || !encode_map(&maps.m[count], x, a.BH, a.N, W)) return -1;
+    if (count == 4 || !encode_map(&maps.in[count], x, a.BH, a.N, W, C, 64)) return -1;
     seen[count] = x;
     width[count] = W;
     return count++;
   };
   for (int i = 0; i < a.nprob; ++i) {
     const LinProblem& p = a.p[i];
-    prm.mi[i] = {index(p.x, p.dx), index(p.y, p.dx), index(p.z, p.dz), state_only ? 0 : index(p.out, p.dz)};
-    if (prm.mi[i].x < 0 || prm.mi[i].y < 0 || prm.mi[i].z < 0 || prm.mi[i].out < 0) return cudaErrorNotSupported;
-    maxdx = std::max(maxdx, p.dx);
+    prm.mi[i] = {input(p.x, p.dx), input(p.y, p.dx), input(p.z, p.dz)};
+    if (prm.mi[i].x < 0 || prm.mi[i].y < 0 || prm.mi[i].z < 0) return cudaErrorNotSupported;
+    if (!state_only && !encode_map(&maps.out[i], p.out, a.BH, a.N, p.dz, 32, out_cols)) return cudaErrorNotSupported;
   }
-  return maxdx == 64 ? launch<64>(prm, maps, state_only, st) : launch<128>(prm, maps, state_only, st);
+  return maxdx == 64 ? launch<64>(prm, maps, state_only, keep_state, st) : launch<128>(prm, maps, state_only, keep_state, st);
 }
 
 }  // namespace ia
