@@ -255,3 +255,60 @@ def test_few_long_sequences_run_in_segments(dt, d, N):
                                  "dv": (k, q, dO, True)}.items():
         want, bound, _, _ = P.linear_bounds(x, y, z, g, d ** -0.5, tc, reverse=rev)
         within(b[name], want, bound)
+
+
+@pytest.mark.parametrize("shape", [(1, 2, 1000, 64, 64), (1, 1, 1300, 128, 128), (2, 1, 900, 64, 128), (1, 2, 650, 128, 64)])
+@pytest.mark.parametrize("segments", [1, 2, 3, 5])
+def test_every_segment_count_and_with_or_without_the_state(shape, segments, monkeypatch):
+    """The tensor-core passes in their forms: whole and in segments, the final state taken or not, widths alike or not."""
+    device()
+    monkeypatch.setenv("IA_LINEAR_SEGMENTS", str(segments))
+    assert 1 <= ia.linear_prefill_segments(*shape, torch.bfloat16) <= segments
+    t = make(*shape, torch.bfloat16, seed=segments, state=True, grad=True)
+    q, k, v, dO, g = t["q"], t["k"], t["v"], t["dO"], t["g"]
+    scale = shape[3] ** -0.5
+    o, bo, S, bS = P.linear_bounds(q, k, v, g, scale, True, t["s"])
+    for want in (False, True):
+        r = ia.linear_prefill_fwd(q, k, v, g, state_in=t["s"], want_state=want)
+        within(r["o"], o, bo)
+        if want:
+            within(r["state"].view_as(S), S, bS)
+    b = ia.linear_fwd_bwd(q, k, v, g, dO)
+    ia.check_device_errors()
+    for name, (x, y, z, rev) in {"o": (q, k, v, False), "dq": (dO, v, k, False), "dk": (v, dO, q, True),
+                                 "dv": (k, q, dO, True)}.items():
+        want, bound, _, _ = P.linear_bounds(x, y, z, g, scale, True, reverse=rev)
+        within(b[name], want, bound)
+
+
+@pytest.mark.parametrize("dt,d,N", [(torch.bfloat16, 64, 1500), (torch.bfloat16, 128, 1500), (torch.float32, 40, 400)])
+def test_two_calls_at_once(dt, d, N):
+    """Calls on two streams, each with memory of its own, give what they give one after the other."""
+    device()
+    a, b = (make(1, 2, N, d, d, dt, seed=s, grad=True) for s in (1, 2))
+    want = [ia.linear_fwd_bwd(t["q"], t["k"], t["v"], t["g"], t["dO"]) for t in (a, b)]
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    torch.cuda.synchronize()
+    for _ in range(5):
+        got = [ia.linear_fwd_bwd(t["q"], t["k"], t["v"], t["g"], t["dO"], stream=st) for t, st in zip((a, b), streams)]
+        torch.cuda.synchronize()
+        for x, y in zip(want, got):
+            for n in x:
+                assert torch.equal(x[n], y[n])
+    ia.check_device_errors()
+
+
+def test_one_tensor_in_several_roles():
+    device()
+    t = make(2, 2, 300, 64, 64, torch.bfloat16, seed=9)
+    x, g = t["q"], t["g"]
+    r = ia.linear_prefill_fwd(x, x, x, g, want_state=True)
+    b = ia.linear_fwd_bwd(x, x, x, g, x)
+    c = x.clone()
+    r2 = ia.linear_prefill_fwd(x, c, c.clone(), g, want_state=True)
+    b2 = ia.linear_fwd_bwd(x, c, c.clone(), g, c.clone())
+    for n in r:
+        assert torch.equal(r[n], r2[n])
+    for n in b:
+        assert torch.equal(b[n], b2[n])
+    ia.check_device_errors()
