@@ -8,7 +8,9 @@
 // Both directions touch every value once (2 and 3 row-sized streams), so HBM
 // bounds them.  A row is held in registers by a group of threads (a warp where
 // its registers suffice), which makes the variance a second pass over
-// registers instead of a difference of large sums.  The rows to come are on
+// registers instead of a difference of large sums: about the mean of the warp's
+// own values, so that several warps exchange mean, squares and number once
+// instead of first one sum and then the other.  The rows to come are on
 // their way meanwhile: every thread copies its own vectors of the next rows
 // into its own slots of shared memory (cp.async), two or three rows ahead, which
 // takes neither registers nor barriers.  One row ahead in registers kept 32 KB
@@ -26,6 +28,15 @@
 // kernel adds the blocks' rows in a fixed order: no atomics, equal bits from
 // equal calls.  Rows wider than the registers hold (12280 columns) are read
 // again from L2 instead.
+//
+// Measured (a graph of calls; rows of up to 126 MB stay in L2): 16384 x 1024 bf16
+// forward 14.9 us, backward 24.5 (67 and 101 MB: 10.2 and 15.4 at HBM's rate);
+// 131072 x 128 fp32 22.2 and 37.6 (20.5, 30.7); 5003 x 777 fp32 9.3 and 16.3 (4.7,
+// 7.1); 2048 x 8192 bf16 25.1 and 31.7 (10.2, 15.4).  Instructions bound bf16 rows
+// of the forward pass (two exchanges a row and sizes and addresses formed per
+// copy: 394 a warp and row at D = 1024, 17.3 us), beside the launch and the first
+// rows' latency; ragged rows pay for their ends, and rows above 4096 columns read
+// the weights again for every row.
 #include <algorithm>
 #include <cmath>
 #include <cstdint>
@@ -72,7 +83,13 @@ struct Vec {
   // In flight to `slot` (own to the thread) until the copies' group is awaited.
   // Values at and past D become zero; those before the row (c < 0) are the
   // previous row's and are cleared by get().
+  // ALIGNED: whole vectors only; slots of columns past D are cleared beforehand.
+  template <bool ALIGNED>
   static __device__ __forceinline__ void fetch(uint4* slot, const T* row, int c, int D) {
+    if (ALIGNED) {
+      if (c < D) asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(slot)), "l"(row + c) : "memory");
+      return;
+    }
     const int left = (D - c) * static_cast<int>(sizeof(T));
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(slot)), "l"(left > 0 ? row + c : row - c % V),
                  "r"(left >= 16 ? 16 : left > 0 ? left : 0)
@@ -146,15 +163,28 @@ __device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_
 template <int N>
 __device__ __forceinline__ void copies_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
 
-// Sums NV values over a group of tpr threads (a power of two up to 32, or a
-// multiple of 32): shuffles, then one word per warp in shared memory.  `slot`
-// alternates between two buffers so that one barrier per call is enough.  All
-// lanes of a warp call it together.
+// Sums NV values over the lanes of a group in one warp (tpr threads a group, a
+// power of two up to 32 or a multiple of 32).  All lanes call it together.
+template <int NV>
+__device__ __forceinline__ void warp_sum(float (&x)[NV], int tpr) {
+  if (tpr >= 32) {
+#pragma unroll
+    for (int o = 16; o; o >>= 1)
+#pragma unroll
+      for (int i = 0; i < NV; ++i) x[i] += __shfl_xor_sync(0xffffffffu, x[i], o);
+  } else {
+    for (int o = tpr >> 1; o; o >>= 1)
+#pragma unroll
+      for (int i = 0; i < NV; ++i) x[i] += __shfl_xor_sync(0xffffffffu, x[i], o);
+  }
+}
+
+// Sums NV values over a group: in its warps, then one word per warp in shared
+// memory.  `slot` alternates between two buffers so that one barrier per call
+// is enough.
 template <int NV>
 __device__ __forceinline__ void group_sum(float (&x)[NV], int tpr, int group, int gt, float* buf, int slot) {
-  for (int o = min(tpr, 32) >> 1; o; o >>= 1)
-#pragma unroll
-    for (int i = 0; i < NV; ++i) x[i] += __shfl_xor_sync(0xffffffffu, x[i], o);
+  warp_sum<NV>(x, tpr);
   if (tpr <= 32) return;
   float* b = buf + (group * 2 + slot) * 32 * NV;
   const int w = gt >> 5, nw = tpr >> 5;
@@ -191,19 +221,20 @@ __device__ __forceinline__ void load_params(const float* __restrict__ p, int c, 
   }
 }
 
-// Forward: most threads per block and blocks of 256 per SM, by values per
-// thread.  (Backward: one block of up to 512 threads per SM.)
-constexpr int fwd_ctas(int E) { return E == 8 ? 4 : E == 16 ? 3 : 1; }
+// Forward: blocks of 256 threads per SM, by values per thread (ragged rows of 16
+// values spill with three blocks: 20000 x 777 fp32 38.1 us, 27.7 with two).
+// Backward: one block of up to 512 threads per SM.
+constexpr int fwd_ctas(int E, bool aligned) { return E == 8 ? 4 : E == 16 ? (aligned ? 3 : 2) : 1; }
 
 // NV vectors per thread: vector j of thread t covers the columns from
 // (j tpr + t) V - mis on, mis the group's offset from a 16-byte boundary.
 // HOLD: weights and biases stay in registers.
 template <typename T, int NV, bool HOLD, bool ALIGNED>
-__global__ void __launch_bounds__(HOLD ? 256 : 512, HOLD ? fwd_ctas(NV * Vec<T>::V) : 1) ln_fwd_kernel(long long rows, int D, int tpr, const T* x,
+__global__ void __launch_bounds__(HOLD ? 256 : 512, HOLD ? fwd_ctas(NV * Vec<T>::V, ALIGNED) : 1) ln_fwd_kernel(long long rows, int D, int tpr, const T* x,
                                                      const float* __restrict__ w, const float* __restrict__ b, float eps,
                                                      T* y, float* __restrict__ mean_out, float* __restrict__ rstd_out) {
   constexpr int V = Vec<T>::V, E = NV * V, kAhead = fwd_depth(NV);
-  __shared__ float buf[16 * 2 * 32];
+  __shared__ float4 buf[16 * 2 * 16];   // [groups][2][warps]: mean, squares about it, number of values
   const int group = threadIdx.x / tpr, gt = threadIdx.x - group * tpr, groups = blockDim.x / tpr;
   const float inv = 1.f / static_cast<float>(D);
   const long long step = static_cast<long long>(gridDim.x) * groups;
@@ -211,15 +242,23 @@ __global__ void __launch_bounds__(HOLD ? 256 : 512, HOLD ? fwd_ctas(NV * Vec<T>:
   const int mis = static_cast<int>(row * D % V);
   int slot = 0, at = 0;
   extern __shared__ uint4 ring[];   // [kAhead][NV][threads]
-  auto fetch = [&](long long r, int k) {
-    if (r < rows)
+  const T* ahead = x + row * D;     // the row to fetch next
+  int left = row < rows ? static_cast<int>((rows - 1 - row) / step) + 1 : 0;   // rows that are not fetched yet
+  auto fetch = [&](int k) {
+    if (left > 0) {
 #pragma unroll
       for (int j = 0; j < NV; ++j)
-        Vec<T>::fetch(ring + (k * NV + j) * blockDim.x + threadIdx.x, x + r * D, (j * tpr + gt) * V - mis, D);
+        Vec<T>::template fetch<ALIGNED>(ring + (k * NV + j) * blockDim.x + threadIdx.x, ahead, (j * tpr + gt) * V - mis, D);
+      ahead += step * D;
+      --left;
+    }
     copies_commit();
   };
+  if (ALIGNED)
+    for (int k = 0; k < kAhead * NV; ++k)
+      if ((k % NV * tpr + gt) * V >= D) ring[k * blockDim.x + threadIdx.x] = make_uint4(0u, 0u, 0u, 0u);
 #pragma unroll
-  for (int k = 0; k < kAhead - 1; ++k) fetch(row + k * step, k);
+  for (int k = 0; k < kAhead - 1; ++k) fetch(k);
   uint64_t held_w[HOLD ? E / 2 : 1], held_b[HOLD ? E / 2 : 1];
   if (HOLD)
 #pragma unroll
@@ -227,10 +266,25 @@ __global__ void __launch_bounds__(HOLD ? 256 : 512, HOLD ? fwd_ctas(NV * Vec<T>:
       load_params<V, ALIGNED>(w, (j * tpr + gt) * V - mis, D, 1.f, held_w + j * V / 2);
       load_params<V, ALIGNED>(b, (j * tpr + gt) * V - mis, D, 0.f, held_b + j * V / 2);
     }
+  // values of the row that this warp holds, where several share it
+  float count[1] = {0.f};
+  if (tpr > 32) {
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      const int c = (j * tpr + gt) * V - mis;
+      count[0] += static_cast<float>(max(0, min(D, c + V) - max(0, c)));
+    }
+    warp_sum<1>(count, 32);
+  }
+  const float warp_inv = tpr <= 32 ? inv : count[0] > 0.f ? 1.f / count[0] : 0.f;
+  const int nw = tpr >> 5;
+  int nw2 = 1;   // a power of two from nw on
+  while (nw2 < nw) nw2 *= 2;
   const int sub = tpr < 32 ? group % (32 / tpr) : 0;   // rows of a warp's groups follow one another
-  for (; row - sub < rows; row += step) {
+  T* out_row = y + row * D;
+  for (; row - sub < rows; row += step, out_row += step * D) {
     const bool in = row < rows;
-    fetch(row + (kAhead - 1) * step, at == 0 ? kAhead - 1 : at - 1);
+    fetch(at == 0 ? kAhead - 1 : at - 1);
     copies_wait<kAhead - 1>();
     uint64_t v[E / 2];
     float s[1];
@@ -245,10 +299,9 @@ __global__ void __launch_bounds__(HOLD ? 256 : 512, HOLD ? fwd_ctas(NV * Vec<T>:
 #pragma unroll
     for (int i = 0; i < E / 2; ++i) t = f2_add(t, v[i]);
     s[0] = f2_sum(t);
-    group_sum<1>(s, tpr, group, gt, buf, slot);
-    slot ^= 1;
-    const float mean = s[0] * inv;
-    const uint64_t minus = f2_twice(-mean);
+    warp_sum<1>(s, tpr);
+    const float near = s[0] * warp_inv;   // the mean of the warp's values
+    const uint64_t minus = f2_twice(-near);
     t = 0ull;
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
@@ -269,10 +322,26 @@ __global__ void __launch_bounds__(HOLD ? 256 : 512, HOLD ? fwd_ctas(NV * Vec<T>:
         for (int i = 0; i < V / 2; ++i) t = f2_fma(v[j * V / 2 + i], v[j * V / 2 + i], t);
     }
     s[0] = f2_sum(t);
-    group_sum<1>(s, tpr, group, gt, buf, slot);
-    slot ^= 1;
-    const float rstd = 1.f / sqrtf(s[0] * inv + eps);
-    const uint64_t r2 = f2_twice(rstd);
+    warp_sum<1>(s, tpr);
+    float mean = near;
+    if (tpr > 32) {
+      // The warps' means m, squares M about them and numbers n of values join
+      // in one exchange: mean = sum n m / D, squares = sum M + n (m - mean)^2.
+      float4* p = buf + (group * 2 + slot) * 16;
+      if ((gt & 31) == 0) p[gt >> 5] = make_float4(near, s[0], count[0], 0.f);
+      slot ^= 1;
+      named_sync(1 + group, tpr);
+      const int k = gt & (nw2 - 1);
+      const float4 m = k < nw ? p[k] : make_float4(0.f, 0.f, 0.f, 0.f);
+      mean = m.z * m.x;
+      for (int o = 1; o < nw2; o *= 2) mean += __shfl_xor_sync(0xffffffffu, mean, o);
+      mean *= inv;
+      const float d = m.x - mean;
+      s[0] = fmaf(m.z * d, d, m.y);
+      for (int o = 1; o < nw2; o *= 2) s[0] += __shfl_xor_sync(0xffffffffu, s[0], o);
+    }
+    const float rstd = __frsqrt_rn(fmaf(s[0], inv, eps));
+    const uint64_t r2 = f2_twice(rstd), d2 = f2_twice((near - mean) * rstd);   // (x - near) rstd + d2 is xhat
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
       const int c = (j * tpr + gt) * V - mis;
@@ -285,11 +354,11 @@ __global__ void __launch_bounds__(HOLD ? 256 : 512, HOLD ? fwd_ctas(NV * Vec<T>:
 #pragma unroll
       for (int i = 0; i < V / 2; ++i) {
         const int k = j * V / 2 + i;
-        r[i] = f2_fma(f2_mul(v[k], r2), HOLD ? held_w[k] : wv[i], HOLD ? held_b[k] : bv[i]);
+        r[i] = f2_fma(f2_fma(v[k], r2, d2), HOLD ? held_w[k] : wv[i], HOLD ? held_b[k] : bv[i]);
       }
       Vec<T> out;
       out.put_pairs(r);
-      out.template store<ALIGNED>(y + row * D, c, D);
+      out.template store<ALIGNED>(out_row, c, D);
     }
     if (gt == 0 && in) {
       if (mean_out) mean_out[row] = mean;
@@ -320,17 +389,25 @@ __global__ void __launch_bounds__(512, 1) ln_bwd_kernel(long long rows, int D, i
     for (int j = 0; j < NV; ++j) load_params<V, ALIGNED>(w, (j * tpr + gt) * V - mis, D, 1.f, held + j * V / 2);
   int slot = 0, at = 0;
   extern __shared__ uint4 ring[];   // [kAhead][2 NV][threads]; at the end the groups' sums, [groups][2][D]
-  auto fetch = [&](long long r, int k) {
-    if (r < rows)
+  long long ahead = row * D;   // offset of the row to fetch next
+  int left = row < rows ? static_cast<int>((rows - 1 - row) / step) + 1 : 0;   // rows that are not fetched yet
+  auto fetch = [&](int k) {
+    if (left > 0) {
 #pragma unroll
       for (int j = 0; j < NV; ++j) {
         const int c = (j * tpr + gt) * V - mis;
         uint4* q = ring + (k * 2 * NV + j) * blockDim.x + threadIdx.x;
-        Vec<T>::fetch(q, x + r * D, c, D);
-        Vec<T>::fetch(q + NV * blockDim.x, dy + r * D, c, D);
+        Vec<T>::template fetch<ALIGNED>(q, x + ahead, c, D);
+        Vec<T>::template fetch<ALIGNED>(q + NV * blockDim.x, dy + ahead, c, D);
       }
+      ahead += step * D;
+      --left;
+    }
     copies_commit();
   };
+  if (ALIGNED)
+    for (int k = 0; k < kAhead * 2 * NV; ++k)
+      if ((k % NV * tpr + gt) * V >= D) ring[k * blockDim.x + threadIdx.x] = make_uint4(0u, 0u, 0u, 0u);
   float next_mean, next_rstd;   // a row ahead: their latency is an iteration's
   auto statistics = [&](long long r) {
     next_mean = r < rows ? mean_in[r] : 0.f;
@@ -338,13 +415,14 @@ __global__ void __launch_bounds__(512, 1) ln_bwd_kernel(long long rows, int D, i
   };
   statistics(row);
 #pragma unroll
-  for (int k = 0; k < kAhead - 1; ++k) fetch(row + k * step, k);
+  for (int k = 0; k < kAhead - 1; ++k) fetch(k);
   const int sub = tpr < 32 ? group % (32 / tpr) : 0;   // rows of a warp's groups follow one another
-  for (; row - sub < rows; row += step) {
+  T* out_row = dx + row * D;
+  for (; row - sub < rows; row += step, out_row += step * D) {
     const bool in = row < rows;
     const float mean = next_mean, rstd = next_rstd;
     statistics(row + step);
-    fetch(row + (kAhead - 1) * step, at == 0 ? kAhead - 1 : at - 1);
+    fetch(at == 0 ? kAhead - 1 : at - 1);
     copies_wait<kAhead - 1>();
     uint64_t hat[E / 2], g[E / 2];
 #pragma unroll
@@ -391,7 +469,7 @@ __global__ void __launch_bounds__(512, 1) ln_bwd_kernel(long long rows, int D, i
       }
       Vec<T> out;
       out.put_pairs(r);
-      out.template store<ALIGNED>(dx + row * D, c, D);
+      out.template store<ALIGNED>(out_row, c, D);
     }
   }
   if (!part) return;
@@ -564,7 +642,7 @@ LnPlan plan_rows(long long rows, int D, int V, int E, int most, long long most_b
 // warp up to 512; 24 for the rows that 512 threads do not hold with 16.
 LnPlan fwd_plan(long long rows, int D, int V) {
   const int n = slots(D, V), E = n <= 256 ? 8 : n <= 4096 ? 16 : 24;
-  return plan_rows(rows, D, V, E, E == 24 ? 512 : 256, static_cast<long long>(fwd_ctas(E)) * num_sms());
+  return plan_rows(rows, D, V, E, E == 24 ? 512 : 256, static_cast<long long>(fwd_ctas(E, D % V == 0)) * num_sms());
 }
 LnPlan bwd_plan(long long rows, int D, int V) {
   const int n = slots(D, V), E = n <= 256 ? 8 : n <= 8192 ? 16 : 24;
