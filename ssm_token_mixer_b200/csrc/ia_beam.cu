@@ -633,7 +633,7 @@ __global__ void __launch_bounds__(kThreads) beam_merge_kernel(
 }
 
 // Spans per row: three CTAs for every SM when the rows are fewer (512 rows of
-// 50257: 36 us in one span each, 43 us in two), spans of at least two rounds of
+// 50257 in bf16: 26.4 us in one span each, 29.4 in two), spans of at least two rounds of
 // every warp, and no more list entries per request than one merge takes.
 int beam_splits(long long rows, int W, int V, int K, int per) {   // per: values of a vector
   const long long want = (static_cast<long long>(num_sms()) * 3 + rows - 1) / rows;
@@ -673,6 +673,10 @@ cudaError_t run_select(int G, int W, int V, int K, const void* logits, const flo
 }
 
 // ------------------------------------------------------------- state reorder
+// Reads each followed state once and writes each sequence's: HBM bounds it (16 x 4
+// sequences of 16 heads, M 64, d 128, 135 MB each way: 41.0 us, 85 % of the copy
+// rate).
+//
 // Up to three arrays, each [sequences][len] floats.
 struct Parts {
   const float* in[3];

@@ -65,7 +65,9 @@ __host__ __device__ inline SimtSmem simt_smem(int dx) {
 // It reads 16 bytes of shared memory per 8 multiply-adds of a lane, about
 // what an SM can supply, so it is bound by the FP32 pipe and shared memory
 // together.  Small CTAs (four per SM at widths up to 64) let one compute
-// while another loads or waits at a barrier.
+// while another loads or waits at a barrier.  Measured: fp32 prefill of B8 H16
+// N2048 d64 398 us (4.0 G multiply-adds, 28 % of the pipe's rate), of B2 H4 N300
+// 48 x 80 in 10 segments 24.2 us, of one chunk 11.2 us.
 template <bool BF16, bool STATE_ONLY>
 __global__ void __launch_bounds__(kThreads, 4) lin_simt_kernel(const __grid_constant__ LinArgs a) {
   extern __shared__ __align__(16) float sm[];

@@ -12,6 +12,10 @@
 //
 // With parents, a sequence reads its parent's state and writes its own: the
 // reordering of a beam search rides on a read and a write that happen anyway.
+//
+// Measured: 64 sequences of 16 heads of 128 x 128 in place 18.0 us (134 MB: 7.5 TB/s,
+// part of the 67 MB of states stays in L2), through parents into other buffers
+// 24.6 us; one sequence 3.3 us, the launch and one read's latency.
 #include <algorithm>
 
 #include "ia_device.cuh"
