@@ -333,6 +333,11 @@ IA_API ia_status_t ia_decode_step_ex(const ia_shape_t* shape, const ia_options_t
  *     the reverse direction of dk and dv); from t on, values that the
  *     definition leaves finite may be NaN as well.
  *   - State: [B,H,d_k,d_v] fp32, ia_linear_state_bytes() bytes.
+ *   - On the tensor cores the decayed scores and the state that meets the
+ *     queries are rounded to bf16 as operands; the state that is carried and
+ *     returned is not.
+ *   - Outputs and the workspace may not overlap inputs or one another, unless a
+ *     call says so.
  *   - d_k, d_v in 1 .. 256.
  */
 typedef struct {
@@ -396,7 +401,8 @@ IA_API ia_status_t ia_linear_decode_step(const ia_linear_shape_t* shape, const v
  * bias [D] fp32 (NULL: 1 and 0), mean and rstd [rows] fp32 (both optional):
  *   y = (x - mean) * rstd * weight + bias,  rstd = 1 / sqrt(var + eps), var the
  * mean square of x - mean.  Statistics in fp32, the variance from the centred
- * values.  1 <= D <= 2^24.  y may be x's buffer.
+ * values.  1 <= D <= 2^24.  y may be x's buffer (the same address), else no
+ * output may overlap an input.
  */
 IA_API ia_status_t ia_layer_norm_fwd(long long rows, int D, ia_dtype_t dtype, const void* x, const float* weight,
                                      const float* bias, float eps, void* y, float* mean, float* rstd,
@@ -432,7 +438,7 @@ IA_API ia_status_t ia_layer_norm_bwd(long long rows, int D, ia_dtype_t dtype, co
  * and where that bound could not separate two beams' candidates, their sums
  * are taken again in fp64.
  * 1 <= W <= 64, 1 <= K <= 64, V >= 1; end_token is in 0 .. V-1 when finished
- * is given.
+ * is given.  Outputs and the workspace may not overlap inputs or one another.
  */
 IA_API size_t ia_beam_select_workspace_bytes(int G, int W, int V, int K, ia_dtype_t dtype);
 IA_API ia_status_t ia_beam_select(int G, int W, int V, int K, ia_dtype_t dtype, const void* logits,

@@ -672,6 +672,17 @@ def _scratch(nbytes, dev, workspace):
     return workspace, _ad(workspace), _nbytes(workspace)
 
 
+def _apart(name, out, *others, in_place=False):
+    """A given output may not share memory with an input (with in_place: it may be an input's buffer as a whole)."""
+    a, n = out.data_ptr(), _nbytes(out)
+    for t in others:
+        if t is None:
+            continue
+        b = t.data_ptr()
+        if a < b + _nbytes(t) and b < a + n and not (in_place and a == b):
+            raise ValueError(f"{name} overlaps an input in memory")
+
+
 def linear_prefill_fwd(q, k, v, log_decay, scale=None, state_in=None, want_state=False, o=None, workspace=None,
                        stream=None):
     """Causal linear attention with one decay per head (see ia_linear_prefill_fwd in include/ia.h):
@@ -687,6 +698,7 @@ def linear_prefill_fwd(q, k, v, log_decay, scale=None, state_in=None, want_state
         _need("state_in", state_in, dtype=torch.float32, numel=n_state)
     if o is not None:
         _need("o", o, v.shape, q.dtype)
+        _apart("o", o, q, k, v, state_in)
     if workspace is not None:
         _need("workspace", workspace)
     dev = _place(("q", q), ("k", k), ("v", v), ("log_decay", log_decay), ("state_in", state_in), ("o", o),
@@ -748,6 +760,7 @@ def linear_decode_step(q, k, v, log_decay, state, scale=None, state_out=None, pa
             raise ValueError("state_out is needed with parents: a state may have several followers")
     if o is not None:
         _need("o", o, v.shape, q.dtype)
+        _apart("o", o, q, k, v, state, state_out)
     dev = _place(("q", q), ("k", k), ("v", v), ("log_decay", log_decay), ("state", state),
                         ("state_out", state_out), ("parents", parents), ("o", o))
     out = state if state_out is None else state_out
@@ -783,6 +796,7 @@ def layer_norm_fwd(x, weight=None, bias=None, eps=1e-5, y=None, stream=None):
     rows, D, code = _check_rows(x, weight, bias)
     if y is not None:
         _need("y", y, x.shape, x.dtype)
+        _apart("y", y, x, in_place=True)
     dev = _place(("x", x), ("weight", weight), ("bias", bias), ("y", y))
     ctx, raw = _on(dev, stream)
     with ctx:
@@ -811,6 +825,7 @@ def layer_norm_bwd(dy, x, mean, rstd, weight=None, want_params=True, dx=None, wo
         _need(name, t, dtype=torch.float32, numel=rows)
     if dx is not None:
         _need("dx", dx, x.shape, x.dtype)
+        _apart("dx", dx, dy, x, in_place=True)
     if workspace is not None:
         _need("workspace", workspace)
     dev = _place(("x", x), ("dy", dy), ("mean", mean), ("rstd", rstd), ("weight", weight), ("dx", dx),

@@ -376,14 +376,15 @@ __global__ void __launch_bounds__(kThreads, 4) beam_scan_kernel(const T* __restr
   }
   __syncthreads();
   const int n = sm.found;
+  uint64_t* mine = keys + static_cast<size_t>(at) * K;
   for (int i = tid; i < n; i += kThreads) {
     const uint64_t key = found[i];
     int rank = 0;
 #pragma unroll 4
     for (int j = 0; j < n; ++j) rank += found[j] > key;
-    if (rank < K) keys[at * K + rank] = key;
+    if (rank < K) mine[rank] = key;
   }
-  for (int i = n + tid; i < K; i += kThreads) keys[at * K + i] = 0;
+  for (int i = n + tid; i < K; i += kThreads) mine[i] = 0;
 
   // maximum and sum of the CTA.  A NaN logit made its lane's sum NaN; +inf made inf - inf.
   if (warp == 0) {

@@ -250,3 +250,20 @@ def test_beam_search_end_to_end():
     # the two runs differ by fp32 matrix products of another batch size: 128 terms of about 0.05
     assert abs(total - float(scores[0, 0])) < steps * 1e-4
     assert torch.isfinite(scores).all() and (scores[0, :-1] >= scores[0, 1:]).all()
+
+
+def test_two_selections_at_once_and_a_given_workspace():
+    device()
+    sets = [data(3, 8, 50257, torch.bfloat16, seed=1), data(2, 64, 3001, torch.float32, seed=2)]
+    ks = [16, 64]
+    want = [ia.beam_select(x, s, k) for (x, s), k in zip(sets, ks)]
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    works = [torch.full((ia.beam_select_workspace_bytes(*x.shape, k, x.dtype),), 255, dtype=torch.uint8, device="cuda")
+             for (x, _), k in zip(sets, ks)]
+    torch.cuda.synchronize()
+    for _ in range(5):
+        got = [ia.beam_select(x, s, k, workspace=w, stream=st) for (x, s), k, w, st in zip(sets, ks, works, streams)]
+        torch.cuda.synchronize()
+        for a, b in zip(want, got):
+            assert all(torch.equal(a[n], b[n]) for n in a)
+    ia.check_device_errors()

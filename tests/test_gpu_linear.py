@@ -312,3 +312,30 @@ def test_one_tensor_in_several_roles():
     for n in b:
         assert torch.equal(b[n], b2[n])
     ia.check_device_errors()
+
+
+def test_decode_captured_through_parents():
+    """Steps of a beam search in one graph: two buffers take turns, the parents are what their tensor holds at replay."""
+    device()
+    B, H, d, W = 6, 2, 64, 3
+    g = torch.Generator().manual_seed(3)
+    q, k, v = (torch.randn(B, H, d, generator=g).bfloat16().cuda() for _ in range(3))
+    decay = torch.tensor([-0.1, -0.5]).cuda()
+    start = torch.randn(B * H * d * d, generator=g).cuda()
+    bufs = [start.clone(), torch.empty_like(start)]
+    parents = torch.zeros(B // W, W, dtype=torch.int32, device="cuda")
+    graph = torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph):
+        a = ia.linear_decode_step(q, k, v, decay, bufs[0], state_out=bufs[1], parents=parents)
+        b = ia.linear_decode_step(k, q, v, decay, bufs[1], state_out=bufs[0], parents=parents)
+    for seed in range(3):
+        parents.copy_(torch.randint(0, W, (B // W, W), generator=torch.Generator().manual_seed(seed), dtype=torch.int32))
+        now = bufs[0].clone()
+        graph.replay()
+        torch.cuda.synchronize()
+        other = torch.empty_like(now)
+        x = ia.linear_decode_step(q, k, v, decay, now, state_out=other, parents=parents)
+        y = ia.linear_decode_step(k, q, v, decay, other, state_out=now, parents=parents)
+        assert torch.equal(a["o"], x["o"]) and torch.equal(b["o"], y["o"]) and torch.equal(bufs[0], now)
+    ia.check_device_errors()

@@ -136,3 +136,27 @@ def test_constant_rows_and_graph():
     torch.cuda.synchronize()
     for n in want:
         assert torch.equal(want[n], got[n])
+
+
+@pytest.mark.parametrize("dt", [torch.bfloat16, torch.float32])
+def test_backward_captured_and_two_calls_at_once(dt):
+    device()
+    sets = [data(700, 320, dt), data(333, 777, dt)]
+    stats = [ia.layer_norm_fwd(x, w, b) for x, w, b, _ in sets]
+    run = lambda i, **kw: ia.layer_norm_bwd(sets[i][3], sets[i][0], stats[i]["mean"], stats[i]["rstd"], sets[i][1], **kw)  # noqa: E731
+    want = [run(0), run(1)]
+    graph = torch.cuda.CUDAGraph()
+    work = torch.empty(ia.layer_norm_bwd_workspace_bytes(700, 320, dt), dtype=torch.uint8, device="cuda")
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph):
+        got = run(0, workspace=work)
+    for t in got.values():
+        t.zero_()
+    graph.replay()
+    torch.cuda.synchronize()
+    assert all(torch.equal(got[n], want[0][n]) for n in got)
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    for _ in range(5):
+        both = [run(i, stream=st) for i, st in enumerate(streams)]
+        torch.cuda.synchronize()
+        assert all(torch.equal(both[i][n], want[i][n]) for i in (0, 1) for n in want[i])

@@ -242,3 +242,21 @@ def test_binding_refuses_strided_tensors(lib, monkeypatch):
 def test_sizes_beyond_an_int_are_refused(lib):
     with pytest.raises(ValueError, match="2\\^31"):
         ia._small("x", 3, 1 << 31)
+
+
+def test_outputs_may_not_overlap_inputs(lib):
+    q, v = torch.zeros(1, 1, 8, 16), torch.zeros(1, 1, 8, 16)
+    g = torch.zeros(1)
+    with pytest.raises(ValueError, match="overlaps"):
+        ia.linear_prefill_fwd(q, q.clone(), v, g, o=v)
+    step = [torch.zeros(1, 1, 16) for _ in range(3)]
+    with pytest.raises(ValueError, match="overlaps"):
+        ia.linear_decode_step(*step, g, torch.zeros(256), o=step[0])
+    buf = torch.zeros(9, 16)
+    with pytest.raises(ValueError, match="overlaps"):
+        ia.layer_norm_fwd(buf[:8], y=buf[1:])
+    with pytest.raises(ValueError, match="overlaps"):
+        ia.layer_norm_bwd(torch.zeros(8, 16), buf[1:], torch.zeros(8), torch.zeros(8), dx=buf[:8])
+    for same in (dict(x=buf, y=buf), dict(x=buf, y=None)):      # in place as a whole: stops only at the CPU tensors
+        with pytest.raises(ValueError, match="CUDA"):
+            ia.layer_norm_fwd(**same)
