@@ -339,3 +339,41 @@ def test_decode_captured_through_parents():
         y = ia.linear_decode_step(k, q, v, decay, other, state_out=now, parents=parents)
         assert torch.equal(a["o"], x["o"]) and torch.equal(b["o"], y["o"]) and torch.equal(bufs[0], now)
     ia.check_device_errors()
+
+
+@pytest.mark.parametrize("dt", [torch.float32, torch.bfloat16])
+def test_training_step_through_norm_and_attention(dt):
+    """Layer norm, linear attention and both backward passes as one step, against autograd of the definitions in fp64."""
+    device()
+    B, N, H, d = 2, 150, 3, 64
+    D = H * d
+    gen = torch.Generator().manual_seed(12)
+    x = torch.randn(B, N, D, generator=gen).to(dt).cuda()
+    w, b = (torch.randn(D, generator=gen) * 0.2 + 1).cuda(), (torch.randn(D, generator=gen) * 0.1).cuda()
+    dO = torch.randn(B, H, N, d, generator=gen).to(dt).cuda()
+    decay = torch.tensor([-0.02, -0.3, 0.0]).cuda()
+
+    n = ia.layer_norm_fwd(x, w, b)
+    h = n["y"].view(B, N, H, d).transpose(1, 2).contiguous()
+    r = ia.linear_fwd_bwd(h, h, h, decay, dO)
+    dh = r["dq"].float() + r["dk"].float() + r["dv"].float()
+    dy = dh.transpose(1, 2).reshape(B, N, D).to(dt)
+    g = ia.layer_norm_bwd(dy, x, n["mean"], n["rstd"], w)
+    ia.check_device_errors()
+
+    x64, w64, b64 = (t.double().requires_grad_() for t in (x, w, b))
+    y = torch.nn.functional.layer_norm(x64, (D,), w64, b64)
+    q = y.view(B, N, H, d).transpose(1, 2)
+    t = torch.arange(N, device="cuda")
+    far = (t[:, None] - t[None]).double()
+    mask = torch.where(far >= 0, torch.exp(decay.double()[:, None, None] * far.clamp(min=0)), 0.0)
+    o = d ** -0.5 * ((q @ q.transpose(-1, -2)) * mask) @ q
+    (o * dO.double()).sum().backward()
+    # fp32: a path sums at most 450 terms (150 tokens, 64 and 192 columns, and what is around them), 450 U of a sum of
+    # magnitudes some 20 times the sum of random signs: 5.4e-4.  bf16: h, P, o, the three gradients, dy and dx are
+    # rounded, eight times half a unit 2^-9 of the magnitudes a value is formed from, up to three in a row on a path
+    # whose magnitudes are a few times its value; as norms, 8 * 2^-9 * 3.
+    tol = 5.4e-4 if dt == torch.float32 else 8 * 2.0 ** -9 * 3
+    for name, got, want in (("o", r["o"], o), ("dx", g["dx"], x64.grad), ("dweight", g["dweight"], w64.grad),
+                            ("dbias", g["dbias"], b64.grad)):
+        assert (got.double() - want).norm() <= tol * want.norm(), name
