@@ -40,6 +40,13 @@ __device__ __forceinline__ void fetch(float* dst, const void* p, long long i, bo
   }
 }
 
+// Four elements, all in or all out.
+__device__ __forceinline__ void fetch4(float* dst, const void* p, long long i, bool in) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(dst)), "l"(static_cast<const float*>(p) + (in ? i : 0)),
+               "r"(in ? 16 : 0)
+               : "memory");
+}
+
 // Row stride in floats of a shared tile of `w` columns: a multiple of 4 whose
 // quarter is odd, so that float4 reads of consecutive rows by consecutive
 // lanes fall into different banks.
@@ -61,18 +68,19 @@ __host__ __device__ inline SimtSmem simt_smem(int dx) {
 }
 
 // The CUDA-core kernel: fp32 throughout, any widths up to 256, one CTA per
-// (b,h, block of 64 z columns, segment), 4 x 4 outputs per thread and step.
-// It reads 16 bytes of shared memory per 8 multiply-adds of a lane, about
-// what an SM can supply, so it is bound by the FP32 pipe and shared memory
-// together.  Small CTAs (four per SM at widths up to 64) let one compute
+// (b,h, block of 64 z columns, segment), R x 4 outputs per thread and step.
+// With R = 4 it reads 16 bytes of shared memory per 8 multiply-adds of a lane,
+// about what an SM can supply, so it is bound by the FP32 pipe and shared
+// memory together.  Small CTAs (four per SM at widths up to 64) let one compute
 // while another loads or waits at a barrier.  Measured: fp32 prefill of B8 H16
-// N2048 d64 398 us (4.0 G multiply-adds, 28 % of the pipe's rate), of B2 H4 N300
-// 48 x 80 in 10 segments 24.2 us, of one chunk 11.2 us.
-template <bool BF16, bool STATE_ONLY>
-__global__ void __launch_bounds__(kThreads, 4) lin_simt_kernel(const __grid_constant__ LinArgs a) {
+// N2048 d64 396 us (4.0 G multiply-adds, 28 % of the pipe's rate), of B2 H4 N300
+// 48 x 80 in 10 segments 21.4 us, of one chunk 9.5 us.
+template <bool BF16, bool STATE_ONLY, int T>
+__global__ void __launch_bounds__(T, 512 / T) lin_simt_kernel(const __grid_constant__ LinArgs a) {
   extern __shared__ __align__(16) float sm[];
   __shared__ int bad;          // least position in the chunk whose z holds a NaN or an infinity, C if none
   __shared__ float pw[C + 1];  // lambda^n
+  constexpr int R = T == 128 ? 4 : 2;   // rows per thread and step
   const int tid = threadIdx.x;
   const int nseg = STATE_ONLY ? a.nseg - 1 : a.nseg;
   const long long stream = blockIdx.x / nseg;
@@ -90,6 +98,7 @@ __global__ void __launch_bounds__(kThreads, 4) lin_simt_kernel(const __grid_cons
   const SimtSmem o = simt_smem(dx);
   const int dxs = lin_pad(dx), zs = lin_pad(kLinZB), as = lin_pad(C);
   const int dx4 = (dx + 3) / 4 * 4, zw4 = (zw + 3) / 4 * 4;
+  const bool wide = !BF16 && dx % 4 == 0 && dz % 4 == 0;   // rows of whole 16-byte pieces
   float *X = sm + o.X, *Y = sm + o.Y, *S = sm + o.S, *Z = sm + o.Z, *A = sm + o.A;
 
   const float graw = a.log_decay[h];
@@ -104,7 +113,7 @@ __global__ void __launch_bounds__(kThreads, 4) lin_simt_kernel(const __grid_cons
   const float* s0 = seg == 0 ? pr.state_in : STATE_ONLY ? nullptr : pr.seg;
   const long long soff = seg == 0 ? bh * dx * static_cast<long long>(dz)
                                   : (bh * (a.nseg - 1) + seg - 1) * dx * static_cast<long long>(dz);
-  for (int e = tid; e < dx4 * zw4; e += kThreads) {
+  for (int e = tid; e < dx4 * zw4; e += T) {
     const int i = e / zw4, j = e - i * zw4;
     S[i * zs + j] = (s0 && i < dx && j < zw) ? s0[soff + static_cast<long long>(i) * dz + z0 + j] : 0.f;
   }
@@ -122,44 +131,65 @@ __global__ void __launch_bounds__(kThreads, 4) lin_simt_kernel(const __grid_cons
     // A warp per row, its lanes along the columns; every copy is in flight
     // before the first is waited for (a chunk cost six DRAM round trips with
     // plain loads, half of its 10 us).
-    for (int i = lane; i < dx4; i += 32) {
-#pragma unroll 8
-      for (int t = warp; t < C; t += kThreads / 32) {
-        const bool in = t < L && i < dx;
-        if (!STATE_ONLY) fetch<BF16>(X + t * dxs + i, pr.x, (row0 + t) * dx + i, in);
-        fetch<BF16>(Y + t * dxs + i, pr.y, (row0 + t) * dx + i, in);
+    auto check = [&](int t, int j) {   // (each thread checks what it copied)
+      if (!isfinite(Z[t * zs + j])) {   // 0 * z of the masked half would reach the tokens before it
+        atomicMin(&bad, pr.reverse ? C - 1 - t : t);
+        Z[t * zs + j] = 0.f;
       }
-    }
-    for (int j = lane; j < zw4; j += 32) {
+    };
+    if (wide) {
+      const int nx = dx / 4, nz = zw / 4;
+#pragma unroll 4
+      for (int e = tid; e < C * nx; e += T) {
+        const int t = e / nx, i = (e - t * nx) * 4;
+        if (!STATE_ONLY) fetch4(X + t * dxs + i, pr.x, (row0 + t) * dx + i, t < L);
+        fetch4(Y + t * dxs + i, pr.y, (row0 + t) * dx + i, t < L);
+      }
+#pragma unroll 4
+      for (int e = tid; e < C * nz; e += T) {
+        const int t = e / nz, j = (e - t * nz) * 4;
+        fetch4(Z + t * zs + j, pr.z, (row0 + t) * dz + z0 + j, t < L);
+      }
+      asm volatile("cp.async.wait_all;" ::: "memory");
+      for (int e = tid; e < C * nz; e += T) {
+        const int t = e / nz, j = (e - t * nz) * 4;
+        for (int d = 0; d < 4; ++d) check(t, j + d);
+      }
+    } else {
+      for (int i = lane; i < dx4; i += 32) {
 #pragma unroll 8
-      for (int t = warp; t < C; t += kThreads / 32)
-        fetch<BF16>(Z + t * zs + j, pr.z, (row0 + t) * dz + z0 + j, t < L && j < zw);
-    }
-    if (!BF16) asm volatile("cp.async.wait_all;" ::: "memory");
-    for (int j = lane; j < zw4; j += 32)
-      for (int t = warp; t < C; t += kThreads / 32)
-        if (!isfinite(Z[t * zs + j])) {   // 0 * z of the masked half would reach the tokens before it
-          atomicMin(&bad, pr.reverse ? C - 1 - t : t);
-          Z[t * zs + j] = 0.f;
+        for (int t = warp; t < C; t += T / 32) {
+          const bool in = t < L && i < dx;
+          if (!STATE_ONLY) fetch<BF16>(X + t * dxs + i, pr.x, (row0 + t) * dx + i, in);
+          fetch<BF16>(Y + t * dxs + i, pr.y, (row0 + t) * dx + i, in);
         }
+      }
+      for (int j = lane; j < zw4; j += 32) {
+#pragma unroll 8
+        for (int t = warp; t < C; t += T / 32)
+          fetch<BF16>(Z + t * zs + j, pr.z, (row0 + t) * dz + z0 + j, t < L && j < zw);
+      }
+      if (!BF16) asm volatile("cp.async.wait_all;" ::: "memory");
+      for (int j = lane; j < zw4; j += 32)
+        for (int t = warp; t < C; t += T / 32) check(t, j);
+    }
     __syncthreads();
     if (!STATE_ONLY) {
       // A = X Y^T, masked and decayed; thread rows t, t + C/4, .. so that the
       // lanes of a warp read neighbouring rows of Y
-      constexpr int Q = C / 4;
-      for (int tile = tid; tile < Q * Q; tile += kThreads) {
+      constexpr int Q = C / 4, QR = C / R;
+      for (int tile = tid; tile < QR * Q; tile += T) {
         const int tr = tile / Q, tc = tile % Q;
-        float acc[4][4] = {};
+        float acc[R][4] = {};
 #pragma unroll 2
         for (int i = 0; i < dx4; i += 4) {
-          float4 xv[4], yv[4];
+          float4 xv[R], yv[4];
 #pragma unroll
-          for (int r = 0; r < 4; ++r) {
-            xv[r] = *reinterpret_cast<const float4*>(X + (tr + r * Q) * dxs + i);
-            yv[r] = *reinterpret_cast<const float4*>(Y + (tc + r * Q) * dxs + i);
-          }
+          for (int r = 0; r < R; ++r) xv[r] = *reinterpret_cast<const float4*>(X + (tr + r * QR) * dxs + i);
 #pragma unroll
-          for (int r = 0; r < 4; ++r)
+          for (int r = 0; r < 4; ++r) yv[r] = *reinterpret_cast<const float4*>(Y + (tc + r * Q) * dxs + i);
+#pragma unroll
+          for (int r = 0; r < R; ++r)
 #pragma unroll
             for (int s = 0; s < 4; ++s) {
               acc[r][s] = fmaf(xv[r].x, yv[s].x, acc[r][s]);
@@ -169,10 +199,10 @@ __global__ void __launch_bounds__(kThreads, 4) lin_simt_kernel(const __grid_cons
             }
         }
 #pragma unroll
-        for (int r = 0; r < 4; ++r)
+        for (int r = 0; r < R; ++r)
 #pragma unroll
           for (int s = 0; s < 4; ++s) {
-            const int t = tr + r * Q, u = tc + s * Q;
+            const int t = tr + r * QR, u = tc + s * Q;
             const int far = pr.reverse ? u - t : t - u;
             A[t * as + u] = far < 0 ? 0.f : acc[r][s] * pw[far];
           }
@@ -180,20 +210,19 @@ __global__ void __launch_bounds__(kThreads, 4) lin_simt_kernel(const __grid_cons
       __syncthreads();
       // out = scale (A Z + lambda^(p+1) X S)
       const int jt = zw4 / 4;
-      for (int tile = tid; tile < Q * jt; tile += kThreads) {
+      for (int tile = tid; tile < QR * jt; tile += T) {
         const int tr = tile / jt, j0 = (tile - tr * jt) * 4;
-        float acc[4][4] = {}, acc2[4][4] = {};
-        auto gemm = [&](const float* lhs, int ls, const float* rhs, int K, float (&c4)[4][4]) {
+        float acc[R][4] = {}, acc2[R][4] = {};
+        auto gemm = [&](const float* lhs, int ls, const float* rhs, int K, float (&c4)[R][4]) {
 #pragma unroll 2
           for (int i = 0; i < K; i += 4) {
-            float4 xv[4], sv[4];
+            float4 xv[R], sv[4];
 #pragma unroll
-            for (int r = 0; r < 4; ++r) {
-              xv[r] = *reinterpret_cast<const float4*>(lhs + (tr + r * Q) * ls + i);
-              sv[r] = *reinterpret_cast<const float4*>(rhs + (i + r) * zs + j0);
-            }
+            for (int r = 0; r < R; ++r) xv[r] = *reinterpret_cast<const float4*>(lhs + (tr + r * QR) * ls + i);
 #pragma unroll
-            for (int r = 0; r < 4; ++r) {
+            for (int r = 0; r < 4; ++r) sv[r] = *reinterpret_cast<const float4*>(rhs + (i + r) * zs + j0);
+#pragma unroll
+            for (int r = 0; r < R; ++r) {
               const float xs[4] = {xv[r].x, xv[r].y, xv[r].z, xv[r].w};
 #pragma unroll
               for (int k = 0; k < 4; ++k) {
@@ -208,8 +237,8 @@ __global__ void __launch_bounds__(kThreads, 4) lin_simt_kernel(const __grid_cons
         gemm(X, dxs, S, dx4, acc2);
         gemm(A, as, Z, C, acc);
 #pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          const int t = tr + r * Q;
+        for (int r = 0; r < R; ++r) {
+          const int t = tr + r * QR;
           if (t >= L) continue;
           const float hd = pw[(pr.reverse ? C - 1 - t : t) + 1];
 #pragma unroll
@@ -226,14 +255,14 @@ __global__ void __launch_bounds__(kThreads, 4) lin_simt_kernel(const __grid_cons
       __syncthreads();
     }
     // S <- lambda^L S + sum_s (lambda^(L-1-p_s) y_s) z_s^T
-    for (int t = warp; t < C; t += kThreads / 32) {
+    for (int t = warp; t < C; t += T / 32) {
       const float w = t < L ? pw[Lw - 1 - (pr.reverse ? C - 1 - t : t)] : 0.f;
       for (int i = lane; i < dx4; i += 32) Y[t * dxs + i] *= w;
     }
     __syncthreads();
     const float dec = bad < C ? __int_as_float(0x7fc00000) : expm1f(g * Lw);
     const int jt = zw4 / 4;
-    for (int tile = tid; tile < (dx4 / 4) * jt; tile += kThreads) {
+    for (int tile = tid; tile < (dx4 / 4) * jt; tile += T) {
       const int i0 = (tile / jt) * 4, j0 = (tile % jt) * 4;
       float acc[4][4] = {};
 #pragma unroll 8
@@ -272,7 +301,7 @@ __global__ void __launch_bounds__(kThreads, 4) lin_simt_kernel(const __grid_cons
     doff = bh * dx * static_cast<long long>(dz);
   }
   if (dst)
-    for (int e = tid; e < dx * zw; e += kThreads) {
+    for (int e = tid; e < dx * zw; e += T) {
       const int i = e / zw, j = e - i * zw;
       dst[doff + static_cast<long long>(i) * dz + z0 + j] = S[i * zs + j];
     }
@@ -314,9 +343,18 @@ cudaError_t simt_launch(const LinArgs& a, int max_dx, bool state_only, cudaStrea
   const size_t bytes = sizeof(float) * simt_smem(max_dx).total;
   const long long grid = static_cast<long long>(a.BH) * a.first[a.nprob] * (state_only ? a.nseg - 1 : a.nseg);
   if (grid > (1LL << 31) - 1) return cudaErrorInvalidConfiguration;
-  auto kern = state_only ? lin_simt_kernel<BF16, true> : lin_simt_kernel<BF16, false>;
-  if (cudaError_t e = allow_smem(kern, bytes); e != cudaSuccess) return e;
-  return launch_after(kern, static_cast<unsigned>(grid), kThreads, bytes, st, a.nseg > 1 && !state_only, a);
+  // Where SMs hold one or two CTAs, for want of CTAs or of shared memory, 256
+  // threads of two rows a step shorten a chunk (B2 H4 N300 48 x 80: 24.3 us with
+  // 128, 21.4 with 256; B4 H16 N2048 d128 771 and 713); where four of 128 threads
+  // fit and there are enough, those read less of shared memory per product (B8
+  // H16 N2048 d64 396 us, and 478 with 256).
+  auto go = [&](auto kern, int threads) {
+    if (cudaError_t e = allow_smem(kern, bytes); e != cudaSuccess) return e;
+    return launch_after(kern, static_cast<unsigned>(grid), threads, bytes, st, a.nseg > 1 && !state_only, a);
+  };
+  if (grid <= 2LL * num_sms() || bytes > 56 * 1024)
+    return state_only ? go(lin_simt_kernel<BF16, true, 256>, 256) : go(lin_simt_kernel<BF16, false, 256>, 256);
+  return state_only ? go(lin_simt_kernel<BF16, true, 128>, 128) : go(lin_simt_kernel<BF16, false, 128>, 128);
 }
 
 }  // namespace
