@@ -4,8 +4,8 @@
 // HBM bounds it (latency at small batches).
 //
 // A CTA takes CW columns of one (b,h) and all its rows: thread (r, c) holds
-// VEC columns of the rows r, r + R, ..., all loaded before the first is used,
-// so that a CTA has its whole slice in flight; the sum over rows is a sum over
+// VEC columns of the rows r, r + R, ..., four or eight loaded before the first
+// is used, so that an SM has 128 KB in flight; the sum over rows is a sum over
 // r at the end, in shared memory and in a fixed order.  With few (b,h) the
 // slices are narrower (32 columns, one 128-byte line per row), which puts the
 // step on four times as many SMs without any exchange between them.
@@ -13,9 +13,12 @@
 // With parents, a sequence reads its parent's state and writes its own: the
 // reordering of a beam search rides on a read and a write that happen anyway.
 //
-// Measured: 64 sequences of 16 heads of 128 x 128 in place 18.0 us (134 MB: 7.5 TB/s,
-// part of the 67 MB of states stays in L2), through parents into other buffers
-// 24.6 us; one sequence 3.3 us, the launch and one read's latency.
+// Measured: 64 sequences of 16 heads of 128 x 128 through parents into another
+// buffer 18.3 us (114 MB: 94 % of the copy rate; 24.0 with 16 rows in flight, two
+// CTAs per SM and plain stores, 20.4 with stores that L2 need not keep), in
+// place 15.9 us (part of the 67 MB of states stays in L2); 256 of 64 x 64 22.4 us
+// through parents of 8 beams (111 MB; 49.5 before); one sequence 2.6 us, the
+// launch and one read's latency.
 #include <algorithm>
 
 #include "ia_device.cuh"
@@ -26,7 +29,6 @@ namespace ia {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kDepth = 16;   // rows of a thread in flight
 
 template <typename T>
 __device__ __forceinline__ float ld(const T* p, long long i) {
@@ -54,15 +56,23 @@ __device__ __forceinline__ Vec<VEC> load_vec(const float* p) {
   }
   return r;
 }
+// apart: the state goes to another buffer, whose lines L2 need not keep while
+// parents are still to be read.
 template <int VEC>
-__device__ __forceinline__ void store_vec(float* p, const Vec<VEC>& r) {
-  if constexpr (VEC == 4) *reinterpret_cast<float4*>(p) = make_float4(r.v[0], r.v[1], r.v[2], r.v[3]);
-  else *p = r.v[0];
+__device__ __forceinline__ void store_vec(float* p, const Vec<VEC>& r, bool apart) {
+  if constexpr (VEC == 4) {
+    const float4 x = make_float4(r.v[0], r.v[1], r.v[2], r.v[3]);
+    if (apart) __stcs(reinterpret_cast<float4*>(p), x);
+    else *reinterpret_cast<float4*>(p) = x;
+  } else {
+    *p = r.v[0];
+  }
 }
 
 // tc: threads across the CW columns; R = kThreads / tc row groups
-template <typename T, int VEC>
-__global__ void __launch_bounds__(kThreads) lin_decode_kernel(
+// kDepth: rows of a thread in flight, for five or four CTAs per SM.
+template <typename T, int VEC, int kDepth>
+__global__ void __launch_bounds__(kThreads, kDepth == 4 ? 5 : 4) lin_decode_kernel(
     int H, int dk, int dv, int cw, int tc, const T* __restrict__ q, const T* __restrict__ k, const T* __restrict__ v,
     const float* __restrict__ log_decay, float scale, const float* sin, const int* __restrict__ parents, int beams,
     float* sout, T* __restrict__ o, int* err) {   // sout may be sin: every entry is read and written by one thread
@@ -73,6 +83,7 @@ __global__ void __launch_bounds__(kThreads) lin_decode_kernel(
   const int h = static_cast<int>(bh % H);
   const int col = static_cast<int>(blockIdx.y) * cw + (tid % tc) * VEC;
   const int r0 = tid / tc, R = kThreads / tc;
+  const bool apart = sout != sin;
   const bool active = r0 < R && (tid % tc) * VEC < cw && col < dv;
 
   long long src = bh;
@@ -125,7 +136,7 @@ __global__ void __launch_bounds__(kThreads) lin_decode_kernel(
         n.v[e] = fmaf(lam, s[d].v[e], ki * vv.v[e]);
         acc.v[e] = fmaf(qi, n.v[e], acc.v[e]);
       }
-      store_vec<VEC>(out + static_cast<long long>(i) * dv, n);
+      store_vec<VEC>(out + static_cast<long long>(i) * dv, n, apart);
     }
   }
 #pragma unroll
@@ -158,8 +169,15 @@ cudaError_t launch(const ia_linear_shape_t& s, const void* q, const void* k, con
                                     static_cast<const T*>(v), log_decay, scale, sin, parents, beams, sout,
                                     static_cast<T*>(o), err);
   };
-  if (vec) go(lin_decode_kernel<T, 4>);
-  else go(lin_decode_kernel<T, 1>);
+  // Rows of a thread: with few, a kernel of fewer registers and one more CTA per
+  // SM (256 sequences of 16 heads of 64 x 64: 18.5 us, and 23 with eight rows).
+  const int rows = (s.d_k + kThreads / tc - 1) / (kThreads / tc);
+  if (vec) {
+    if (rows <= 4) go(lin_decode_kernel<T, 4, 4>);
+    else go(lin_decode_kernel<T, 4, 8>);
+  } else {
+    go(lin_decode_kernel<T, 1, 8>);
+  }
   mark_launch_end(st);
   return cudaGetLastError();
 }
