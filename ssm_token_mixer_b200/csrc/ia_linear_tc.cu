@@ -40,7 +40,10 @@
 // loops of the roles are kept short on purpose: with everything unrolled the
 // warps spent six of seven issue slots waiting for instructions (three roles
 // of straight-line code do not fit an SM's instruction caches; ncu, B8 H16
-// N2048 d64).  Waits are bounded mbarrier waits with a CTA-wide abort flag.
+// N2048 d64).  Only the warp that issues the products runs straight-line code:
+// its issuing is on the chunk's path (training of B4 H16 N2048 d128 137.4 us with
+// four products a turn, 132.0 with all).  Waits are bounded mbarrier waits with
+// a CTA-wide abort flag.
 #include <algorithm>
 #include <cuda.h>
 
@@ -72,10 +75,10 @@ template <int MAXDX, bool STATE_ONLY, int PARTS>
 struct Cfg {
   // Stages.  X is released late (by G3), Y by G4; Z is needed first and released
   // last.  What the third part of w z takes comes from X and, at d = 64, from
-  // half of the output tile (prefill of B8 H16 N2048 d64: 29.5 us with two parts,
-  // 33.9 with three; with one buffer of w z and three stages of X 37.4, with two
-  // stages of Z and three of X 39.5.  B4 H16 d128: 40.2 and 42.9; with two stages of
-  // X and no output tile 46.7).
+  // half of the output tile (prefill of B8 H16 N2048 d64: 29.3 us with two parts,
+  // 33.6 with three; before the last step, at 33.9, 37.4 with one buffer of w z
+  // and three stages of X, 39.5 with two stages of Z and three of X.  B4 H16 d128:
+  // 38.5 and 41.7; at 42.9, 46.7 with two stages of X and no output tile).
   static constexpr bool kFull3 = PARTS == 3 && !STATE_ONLY;
   static constexpr int NX = STATE_ONLY ? 0 : MAXDX == 64 ? (kFull3 ? 2 : 3) : kFull3 ? 1 : 2;
   static constexpr int NY = STATE_ONLY && PARTS == 2 ? 3 : 2;
@@ -578,10 +581,10 @@ __global__ void __launch_bounds__(has_w(MAXDX, STATE_ONLY) ? 640 : 512, 1) lin_t
       constexpr uint64_t kTok = (2 * kAtom) >> 4;   // 16 tokens (or rows of S) further
       auto g1 = [&](int c) {
         const uint64_t x = kmajor(sX(c)), y = kmajor(sY(c));
-#pragma unroll 1
-        for (int b = 0; b < nbx; ++b)
 #pragma unroll
-          for (int kk = 0; kk < 4; ++kk) {
+        for (int b = 0; b < MAXDX / 64; ++b)
+#pragma unroll
+          for (int kk = 0; b < nbx && kk < 4; ++kk) {
             const uint64_t step = (b * kBox + kk * 32) >> 4;
             mma_ss(lead, tmem + K::kTA + 128 * (c & 1), x + step, y + step, idesc_bf16(128, 128, 0, 0), b + kk > 0);
           }
@@ -589,10 +592,10 @@ __global__ void __launch_bounds__(has_w(MAXDX, STATE_ONLY) ? 640 : 512, 1) lin_t
       };
       auto g3 = [&](int c) {
         const uint64_t x = kmajor(sX(c)), sb = mnmajor(K::S_SB);
-#pragma unroll 1
-        for (int b = 0; b < nbx; ++b)
 #pragma unroll
-          for (int kk = 0; kk < 4; ++kk)
+        for (int b = 0; b < MAXDX / 64; ++b)
+#pragma unroll
+          for (int kk = 0; b < nbx && kk < 4; ++kk)
             mma_ss(lead, tmem + K::kTO1 + (K::kO1Twice ? 64 * (c & 1) : 0), x + ((b * kBox + kk * 32) >> 4), sb + (4 * b + kk) * kTok, idesc_bf16(128, 64, 0, 1), b + kk > 0);
         commit_to(lead, bars + kSFree);
         commit_to(lead, bars + kFreeX + c % kNX);
@@ -603,11 +606,11 @@ __global__ void __launch_bounds__(has_w(MAXDX, STATE_ONLY) ? 640 : 512, 1) lin_t
         const int zb = c % K::NZ;
         const uint64_t y = mnmajor(sY(c)), zw = mnmajor(K::S_ZW + zb * PARTS * kBox);
         if (K::kO1Twice) {   // the parts one after the other
-#pragma unroll 4
+#pragma unroll
           for (int kk = 0; kk < 8 * PARTS; ++kk)
             mma_ss(lead, tmem + k_col(c), y + (kk & 7) * kTok, zw + kk * kTok, idesc_bf16(128, 64, 1, 1), kk > 0);
         } else {             // the first two side by side, the third into the second's columns
-#pragma unroll 4
+#pragma unroll
           for (int kk = 0; kk < 8; ++kk)
             mma_ss(lead, tmem + k_col(c), y + kk * kTok, zw + kk * kTok, idesc_bf16(K::kHalf ? 64 : 128, 128, 1, 1), kk > 0);
           if (PARTS == 3)
@@ -623,7 +626,7 @@ __global__ void __launch_bounds__(has_w(MAXDX, STATE_ONLY) ? 640 : 512, 1) lin_t
       };
       auto g2 = [&](int c) {
         const uint64_t z = mnmajor(sZ(c));
-#pragma unroll 4
+#pragma unroll
         for (int kk = 0; kk < 8; ++kk)
           mma_ts(lead, tmem + K::kTO2, tmem + K::kTA + 128 * (c & 1) + 8 * kk, z + kk * kTok, idesc_bf16(128, 64, 0, 1), kk > 0);
         commit_to(lead, bars + kOFull);
