@@ -273,12 +273,13 @@ __global__ void __launch_bounds__(has_w(MAXDX, STATE_ONLY) ? 640 : 512, 1) lin_t
     const uint8_t* zs = smem + sZ(c);
     if (c >= K::NZ && !warp_wait(kZFree + c % K::NZ, c / K::NZ - 1)) return false;   // G4 has read the buffer
     if (!warp_wait(kFullZ + c % NT, c / NT)) return false;
+    // (two turns at a time: training of B8 H16 N2048 d64 104.3 us with one, 102.0)
     const __nv_bfloat162 zero = __float2bfloat162_rn(0.f);
     __nv_bfloat162 probe = zero;   // 0 * z: NaN if any z is not finite
     uint32_t off = (4 * half * kRoleThreads + u) * 16;
     int t = 64 * half + (u >> 3);
     uint4 zn = *reinterpret_cast<const uint4*>(zs + off);
-#pragma unroll 1
+#pragma unroll 2
     for (int i = 0; i < kIter; ++i) {
       const uint32_t zz[4] = {zn.x, zn.y, zn.z, zn.w};
       if (i + 1 < kIter) zn = *reinterpret_cast<const uint4*>(zs + off + 16 * kRoleThreads);
