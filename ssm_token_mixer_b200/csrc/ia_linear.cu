@@ -415,12 +415,12 @@ LinPlan lin_plan(const ia_linear_shape_t& s, bool train) {
   const long long slots = static_cast<long long>(num_sms()) * (p.tc || width > 128 ? 1 : width > 64 ? 2 : 4);
   // In microseconds on a B200: a chunk of the full pass and of the state-only
   // pass, what a wave of CTAs costs beside its chunks, the launch of the
-  // state-only pass, and the carry over n segments.  Measured: 56 chunks of
-  // d = 64 and 16 heads take 79.5 us whole, 65.6 in 2 segments, 40.0 in 4, 27.3
-  // in 8 (planned), 38.4 in 12; 55 of d = 128 take 110.7, 82.9, 53.9 in 4
-  // (planned), 69.9 in 5, 61.9 in 8; 8 chunks of d = 64 and one head 15.3 whole,
-  // 15.6, 12.6, 11.0 in 8 (planned); of 16 heads 15.5 whole (planned) and 16.4
-  // in 4.
+  // state-only pass, and the carry over n segments.  Measured with the state
+  // out: 56 chunks of d = 64 and 16 heads take 87.9 us whole, 73.1 in 2 segments,
+  // 44.0 in 4, 29.3 in 8 (planned), 41.7 in 12; 55 of d = 128 take 116.8, 90.0, 57.8
+  // in 4 (planned), 76.2 in 5, 67.2 in 8; 8 chunks of d = 64 and one head 16.5
+  // whole, 16.5, 13.3, 11.4 in 8 (planned); of 16 heads 16.7 whole (planned) and
+  // 17.1 in 4; training over 32 chunks of 16 heads 45.4 whole, 40.0 in 2 (planned).
   const bool wide = (p.tc && !train ? s.d_k : width) > 64;   // the tensor-core pass: x and y alone
   const double full = p.tc ? (wide ? 1.95 : 1.3) : (wide ? 40.0 : 20.0);
   const double state = p.tc ? (wide ? 0.8 : 0.75) : 0.45 * full;
