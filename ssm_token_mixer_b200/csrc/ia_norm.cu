@@ -45,6 +45,7 @@
 #include "ia_device.cuh"
 #include "ia_internal.h"
 #include "ia_launch.h"
+#include "ia_rows.h"
 
 namespace ia {
 namespace {
@@ -84,15 +85,15 @@ struct Vec {
   // Values at and past D become zero; those before the row (c < 0) are the
   // previous row's and are cleared by get().
   // ALIGNED: whole vectors only; slots of columns past D are cleared beforehand.
+  // mis: the row's first element modulo V.
   template <bool ALIGNED>
-  static __device__ __forceinline__ void fetch(uint4* slot, const T* row, int c, int D) {
+  static __device__ __forceinline__ void fetch(uint4* slot, const T* row, int c, int D, int mis) {
     if (ALIGNED) {
       if (c < D) asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(slot)), "l"(row + c) : "memory");
       return;
     }
-    const int left = (D - c) * static_cast<int>(sizeof(T));
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(slot)), "l"(left > 0 ? row + c : row - c % V),
-                 "r"(left >= 16 ? 16 : left > 0 ? left : 0)
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(slot)), "l"(row + copy_column(c, D, mis)),
+                 "r"(copy_bytes(c, D, sizeof(T)))
                  : "memory");
   }
   template <bool ALIGNED>
@@ -248,7 +249,7 @@ __global__ void __launch_bounds__(HOLD ? 256 : 512, HOLD ? fwd_ctas(NV * Vec<T>:
     if (left > 0) {
 #pragma unroll
       for (int j = 0; j < NV; ++j)
-        Vec<T>::template fetch<ALIGNED>(ring + (k * NV + j) * blockDim.x + threadIdx.x, ahead, (j * tpr + gt) * V - mis, D);
+        Vec<T>::template fetch<ALIGNED>(ring + (k * NV + j) * blockDim.x + threadIdx.x, ahead, (j * tpr + gt) * V - mis, D, mis);
       ahead += step * D;
       --left;
     }
@@ -397,8 +398,8 @@ __global__ void __launch_bounds__(512, 1) ln_bwd_kernel(long long rows, int D, i
       for (int j = 0; j < NV; ++j) {
         const int c = (j * tpr + gt) * V - mis;
         uint4* q = ring + (k * 2 * NV + j) * blockDim.x + threadIdx.x;
-        Vec<T>::template fetch<ALIGNED>(q, x + ahead, c, D);
-        Vec<T>::template fetch<ALIGNED>(q + NV * blockDim.x, dy + ahead, c, D);
+        Vec<T>::template fetch<ALIGNED>(q, x + ahead, c, D, mis);
+        Vec<T>::template fetch<ALIGNED>(q + NV * blockDim.x, dy + ahead, c, D, mis);
       }
       ahead += step * D;
       --left;
