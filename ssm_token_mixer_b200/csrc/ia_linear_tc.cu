@@ -369,6 +369,7 @@ __global__ void __launch_bounds__(has_w(MAXDX, STATE_ONLY) ? 640 : 512, 1) lin_t
                 };
 #pragma unroll
                 for (int i = 0; i < 8; ++i) w[i] = pack_bf16(val(2 * i), val(2 * i + 1));
+                __syncwarp();   // d >= 0 differs between lanes, and the store is the whole warp's
               }
             }
             tmem_st8(ta + 16 * gr + 8 * hf, w);   // columns of A that this lane has read already
@@ -442,6 +443,7 @@ __global__ void __launch_bounds__(has_w(MAXDX, STATE_ONLY) ? 640 : 512, 1) lin_t
         if (p >= from)
 #pragma unroll
           for (int i = 0; i < 8; ++i) w[i] = 0x7fc07fc0u;   // NaN
+        __syncwarp();   // p >= from differs between lanes, and the next loads from TMEM are the whole warp's
         *reinterpret_cast<uint4*>(stage + (((2 * at) ^ swz) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
         *reinterpret_cast<uint4*>(stage + (((2 * at + 1) ^ swz) << 4)) = make_uint4(w[4], w[5], w[6], w[7]);
         if (K::kOutCols == 32 && q == 1) stage_out(z0, t0, false);
