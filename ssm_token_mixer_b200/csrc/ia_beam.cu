@@ -41,10 +41,18 @@
 // ulp of ex2.approx (2^-22) and by ln 2 |t| (2^-24 + 2^-24 + 2^-26) from x - m,
 // the product and log2 e, a lane's tree of 8 adds 3 2^-24, and these add up in
 // fp64.  t is at most 3 above 0; below it the terms' weights keep their mean
-// |t| under log2 V.  So a lse is off by at most 4.2e-7 + 9.3e-8 log2 V, and
-// where two neighbours in the chosen order come from different beams and lie
-// within twice that, the CTA takes those beams' sums again in fp64 and orders
-// once more (4 % of calls at 64 x 8 x 50257, K = 16, normal logits).
+// |t| under log2 V.  So a lse is off by at most 4.2e-7 + 9.3e-8 log2 V = eps / 2,
+// and candidates of two beams are in order where their scores are more than eps
+// apart.  Where two neighbours in the chosen order come from different beams and
+// lie within eps, or a candidate that was not chosen lies within eps of the last
+// chosen one and comes from another beam, the CTA takes those beams' sums again
+// in fp64 and orders once more (4 % of calls at 64 x 8 x 50257, K = 16, normal
+// logits).  That is enough: if a candidate b was put behind a of another beam
+// against the exact order, they lie within eps, and so do all between them; the
+// chain from a to b changes beams next to an entry of a's beam and next to one of
+// b's, so both are taken again.  The other beams' candidates were more than eps
+// from what they might change places with, and an exact sum moves a score by
+// eps / 2 at most, so their order stands.
 #include <algorithm>
 #include <cmath>
 #include <cstdint>
@@ -413,16 +421,16 @@ __device__ __forceinline__ bool better(const Cand& a, const Cand& b) {
 
 constexpr int kHeld = (kMergeMost > kMaxW * kMaxK ? kMergeMost : kMaxW * kMaxK) / kThreads;   // entries per thread of the merge
 constexpr int kMergeEntries = kMergeMost > kMaxW * kMaxK ? kMergeMost : kMaxW * kMaxK;
-// of n candidates spread over the threads, the K1-th best of the threads' best
-// is reached by at most K1 ceil(n / threads)
-constexpr int kFew = (kMaxK + 1) * (kMergeEntries / kThreads);
+// of n candidates spread over the threads, the K-th best of the threads' best
+// is reached by at most K ceil(n / threads)
+constexpr int kFew = kMaxK * (kMergeEntries / kThreads);
 static_assert(kFew >= kThreads, "one entry per thread fits without narrowing");
 // fp32 and finite: scores below the type's range count as its lowest
 __device__ __forceinline__ float as_float(double s) { return fmaxf(static_cast<float>(s), -3.402823466e38f); }
 
 struct MergeSmem {
   Cand few[kFew];
-  Cand best[kMaxK + 1];
+  Cand best[kMaxK];
   float tbest[kThreads];
   float span_m[kMergeMost];
   double span_s[kMergeMost];
@@ -535,14 +543,13 @@ __global__ void __launch_bounds__(kThreads) beam_merge_kernel(
   };
 
   const Cand none = {-__builtin_huge_val(), ~0ull};
-  const int K1 = K + 1;   // one more than wanted, to see how close the first one left out is
   for (int round = 0; round < 2; ++round) {
     if (tid == 0) {
       sm.nfew = 0;
       sm.again = 0;
       sm.thr = 0;
     }
-    // A bound that at least K1 candidates reach: the K1-th largest of the
+    // A bound that at least K candidates reach: the K-th largest of the
     // threads' best in fp32 (rounding keeps the order)
     float mine = -kInf;
     Cand top = none;
@@ -561,20 +568,25 @@ __global__ void __launch_bounds__(kThreads) beam_merge_kernel(
         const float4 o = *reinterpret_cast<const float4*>(sm.tbest + i);
         reach += (o.x >= mine) + (o.y >= mine) + (o.z >= mine) + (o.w >= mine);
       }
-      if (reach >= K1) atomicMax(&sm.thr, ordered(mine));
+      if (reach >= K) atomicMax(&sm.thr, ordered(mine));
     }
     __syncthreads();
     const unsigned thr = sm.thr;
+    // listed with it: what lies within eps of the bound, so all that is that close
+    // to the last chosen one (2^-22: the roundings to fp32)
+    const float least = thr ? unordered(thr) : -kInf;
+    const float near = least - fmaf(fabsf(least), 0x1p-22f, static_cast<float>(eps));
 #pragma unroll
     for (int j = 0; j < kHeld; ++j) {
       if (j * kThreads >= n) break;
       Cand c;
-      if (!entry(j, c) || ordered(as_float(c.score)) < thr) continue;
+      if (!entry(j, c) || as_float(c.score) < near) continue;
       const int at = atomicAdd(&sm.nfew, 1);
       if (at < kFew) sm.few[at] = c;
     }
     __syncthreads();
-    if (sm.nfew > kFew) {   // more ties in fp32 than fit: the bound from exact scores, through the same list
+    const bool many = sm.nfew > kFew;
+    if (many) {   // more of them than fit: the bound from exact scores, through the same list
       __syncthreads();
       if (tid == 0) {
         sm.nfew = 0;
@@ -584,7 +596,7 @@ __global__ void __launch_bounds__(kThreads) beam_merge_kernel(
       __syncthreads();
       int rank = 0;
       for (int i = 0; i < kThreads; ++i) rank += better(sm.few[i], top);
-      if (rank == K1 - 1 && top.at != ~0ull) sm.best[0] = top;
+      if (rank == K - 1 && top.at != ~0ull) sm.best[0] = top;
       __syncthreads();
       const Cand bound = sm.best[0];
 #pragma unroll
@@ -596,25 +608,34 @@ __global__ void __launch_bounds__(kThreads) beam_merge_kernel(
     }
     __syncthreads();
     const int m = sm.nfew;
-    for (int i = tid; i < K1; i += kThreads) sm.best[i] = none;
+    for (int i = tid; i < K; i += kThreads) sm.best[i] = none;
     __syncthreads();
     for (int i = tid; i < m; i += kThreads) {
       const Cand c = sm.few[i];
       int rank = 0;
       for (int j = 0; j < m; ++j) rank += better(sm.few[j], c);
-      if (rank < K1) sm.best[rank] = c;
+      if (rank < K) sm.best[rank] = c;
     }
     __syncthreads();
-    if (round == 1) break;
-    // neighbours from different beams that fp32 sums cannot tell apart
-    for (int i = tid; i < K; i += kThreads) {
-      const Cand a = sm.best[i], b = sm.best[i + 1];
+    if (round == 1 || W == 1) break;
+    // candidates of different beams that fp32 sums cannot tell apart: neighbours
+    // among the chosen, and what is left out just behind the last of them
+    auto compare = [&](const Cand& a, const Cand& b) {
       const uint32_t wa = static_cast<uint32_t>(a.at >> 32), wb = static_cast<uint32_t>(b.at >> 32);
-      if (b.at == ~0ull || wa == wb || a.score - b.score > eps) continue;
+      if (wa == wb || a.score - b.score > eps) return;
       sm.again = 1;
       if (sm.lse[wa] == sm.lse[wa]) sm.redo[wa] = 1;   // (a finished beam has no sum)
       if (sm.lse[wb] == sm.lse[wb]) sm.redo[wb] = 1;
-    }
+    };
+    for (int i = tid; i < K - 1; i += kThreads)
+      if (sm.best[i + 1].at != ~0ull) compare(sm.best[i], sm.best[i + 1]);
+    const Cand last = sm.best[K - 1];
+    if (last.at != ~0ull)
+      for (int i = tid; i < m; i += kThreads)
+        if (better(last, sm.few[i])) compare(last, sm.few[i]);
+    if (many)   // what is close to the last one is not all listed: every beam with a sum
+      for (int w = tid; w < W; w += kThreads)
+        if (sm.lse[w] == sm.lse[w]) sm.again = sm.redo[w] = 1;
     __syncthreads();
     if (!sm.again) break;
     for (int w = 0; w < W; ++w)
