@@ -411,12 +411,18 @@ __global__ void __launch_bounds__(kThreads, 4) beam_scan_kernel(const T* __restr
   }
 }
 
-struct Cand {   // a candidate's exact order: higher score, then lower beam and token
+// A candidate's exact order: higher score, then lower beam, higher logit, lower
+// token.  The logit decides within a beam, where the sum of beam score, logit
+// and lse may round two logits (1e-30 and 3e-30, say) to one score.
+struct Cand {
   double score;
-  uint64_t at;   // beam << 32 | token
+  uint64_t at;    // beam << 32 | token
+  float logit;    // 0 for a finished beam
 };
 __device__ __forceinline__ bool better(const Cand& a, const Cand& b) {
-  return a.score > b.score || (a.score == b.score && a.at < b.at);
+  if (a.score != b.score) return a.score > b.score;
+  if (a.logit != b.logit && a.at >> 32 == b.at >> 32) return a.logit > b.logit;
+  return a.at < b.at;
 }
 
 constexpr int kHeld = (kMergeMost > kMaxW * kMaxK ? kMergeMost : kMaxW * kMaxK) / kThreads;   // entries per thread of the merge
@@ -429,11 +435,15 @@ static_assert(kFew >= kThreads, "one entry per thread fits without narrowing");
 __device__ __forceinline__ float as_float(double s) { return fmaxf(static_cast<float>(s), -3.402823466e38f); }
 
 struct MergeSmem {
-  Cand few[kFew];
+  union {
+    struct {              // until the beams' sums are formed
+      float span_m[kMergeMost];
+      double span_s[kMergeMost];
+    };
+    Cand few[kFew];
+  };
   Cand best[kMaxK];
   float tbest[kThreads];
-  float span_m[kMergeMost];
-  double span_s[kMergeMost];
   double lse[kMaxW];      // NaN: no candidates
   double red[kThreads / 32];
   float redm[kThreads / 32];
@@ -533,16 +543,18 @@ __global__ void __launch_bounds__(kThreads) beam_merge_kernel(
       if (i != w * per_row || !isfinite(sc)) return false;
       c.score = sc;
       c.at = static_cast<uint64_t>(w) << 32 | static_cast<uint32_t>(end_token);
+      c.logit = 0.f;
       return true;
     }
     const double lse = sm.lse[w];
     if (!(lse == lse) || !key[j]) return false;
-    c.score = static_cast<double>(sc) + (static_cast<double>(key_value(key[j])) - lse);
+    c.logit = key_value(key[j]);
+    c.score = static_cast<double>(sc) + (static_cast<double>(c.logit) - lse);
     c.at = static_cast<uint64_t>(w) << 32 | key_index(key[j]);
     return true;
   };
 
-  const Cand none = {-__builtin_huge_val(), ~0ull};
+  const Cand none = {-__builtin_huge_val(), ~0ull, 0.f};
   for (int round = 0; round < 2; ++round) {
     if (tid == 0) {
       sm.nfew = 0;

@@ -80,3 +80,20 @@ def test_all_equal_rows_in_several_spans():
     for V in (40001, 100003):
         for W, K in ((2, 1), (3, 2), (2, 8), (5, 4)):
             check(torch.full((1, W, V), 0.25, device="cuda"), torch.full((1, W), -1.0, device="cuda"), K)
+
+
+@pytest.mark.parametrize("K", [1, 2, 3, 4, 6])
+def test_logits_that_differ_below_a_sum(K):
+    """Within a beam the scores differ exactly as the logits do, also where beam score + logit rounds to one number."""
+    device()
+    V = 5000
+    x = torch.full((1, 2, V), -5.0, device="cuda")
+    x[0, :, 7] = 1e-30
+    x[0, :, 4000] = 3e-30
+    x[0, :, 100] = 0.0
+    x[0, 0, 4500] = 2e-30
+    s = torch.tensor([[-3.0, -9.0]], device="cuda")
+    r = ia.beam_select(x, s, K)
+    ia.check_device_errors()
+    want = [(0, 4000), (0, 4500), (0, 7), (0, 100), (0, 0), (0, 1)][:K]
+    assert list(zip(r["parents"][0].tolist(), r["tokens"][0].tolist())) == want
