@@ -55,6 +55,7 @@
 // eps / 2 at most, so their order stands.
 #include <algorithm>
 #include <cmath>
+#include <cstddef>
 #include <cstdint>
 
 #include "ia_device.cuh"
@@ -443,7 +444,7 @@ struct MergeSmem {
     Cand few[kFew];
   };
   Cand best[kMaxK];
-  float tbest[kThreads];
+  alignas(16) float tbest[kThreads];   // read four at a time
   double lse[kMaxW];      // NaN: no candidates
   double red[kThreads / 32];
   float redm[kThreads / 32];
@@ -451,6 +452,8 @@ struct MergeSmem {
   int nfew, again;
   unsigned char redo[kMaxW];
 };
+
+static_assert(alignof(MergeSmem) == 16 && offsetof(MergeSmem, tbest) % 16 == 0, "its float4 reads");
 
 // lse of one row in fp64, by the whole CTA.
 template <typename T>
