@@ -458,11 +458,11 @@ static_assert(alignof(MergeSmem) == 16 && offsetof(MergeSmem, tbest) % 16 == 0, 
 // lse of one row in fp64, by the whole CTA.
 template <typename T>
 __device__ __noinline__ double exact_lse(const T* x, int V, MergeSmem& sm) {
-  const unsigned full = 0xffffffffu;
+  const unsigned full = 0xffffffffu, n = V;   // unsigned: a thread's last index may pass 2^31 by its stride
   const int tid = threadIdx.x;
   float m = -kInf;
 #pragma unroll 8
-  for (int i = tid; i < V; i += kThreads) m = fmaxf(m, to_f(x[i]));
+  for (unsigned i = tid; i < n; i += kThreads) m = fmaxf(m, to_f(x[i]));
 #pragma unroll
   for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(full, m, o));
   __syncthreads();
@@ -470,12 +470,12 @@ __device__ __noinline__ double exact_lse(const T* x, int V, MergeSmem& sm) {
   __syncthreads();
   for (int w = 0; w < kThreads / 32; ++w) m = fmaxf(m, sm.redm[w]);
   double part[4] = {0.0, 0.0, 0.0, 0.0};   // four in flight; a fixed order
-  int i = tid;
-  for (; i + 3 * kThreads < V; i += 4 * kThreads) {
+  unsigned i = tid;
+  for (; i + 3 * kThreads < n; i += 4 * kThreads) {
 #pragma unroll
     for (int k = 0; k < 4; ++k) part[k] += exp(static_cast<double>(to_f(x[i + k * kThreads])) - m);
   }
-  for (; i < V; i += kThreads) part[0] += exp(static_cast<double>(to_f(x[i])) - m);
+  for (; i < n; i += kThreads) part[0] += exp(static_cast<double>(to_f(x[i])) - m);
   double s = (part[0] + part[1]) + (part[2] + part[3]);
 #pragma unroll
   for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(full, s, o);

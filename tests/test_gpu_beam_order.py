@@ -1,4 +1,6 @@
 """The order of a beam selection among beams that fp32 sums of exponentials cannot tell apart."""
+import math
+
 import pytest
 import torch
 
@@ -97,3 +99,19 @@ def test_logits_that_differ_below_a_sum(K):
     ia.check_device_errors()
     want = [(0, 4000), (0, 4500), (0, 7), (0, 100), (0, 0), (0, 1)][:K]
     assert list(zip(r["parents"][0].tolist(), r["tokens"][0].tolist())) == want
+
+
+def test_the_longest_vocabulary():
+    """V = 2^31 - 1: the fp64 sums of two equal beams run to the last index that an int holds, and no further."""
+    device()
+    V = 2**31 - 1
+    torch.cuda.empty_cache()
+    if torch.cuda.mem_get_info()[0] < 10 * 2**30:
+        pytest.skip("not enough free memory")
+    x = torch.zeros(1, 2, V, dtype=torch.bfloat16, device="cuda")
+    x[0, :, 5] = x[0, :, V - 1] = 12.0
+    r = ia.beam_select(x, torch.full((1, 2), -1.0, device="cuda"), 3)
+    ia.check_device_errors()
+    assert r["parents"].tolist() == [[0, 0, 1]] and r["tokens"].tolist() == [[5, V - 1, 5]]
+    want = -1.0 + 12.0 - math.log(V - 2 + 2 * math.exp(12.0))
+    assert (r["scores"].cpu().double() - want).abs().max() <= 1e-9 + P.U * abs(want)   # fp64 sums, rounded once
