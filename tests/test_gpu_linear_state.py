@@ -1,0 +1,52 @@
+"""The state of linear attention: fp32 accuracy of what the sequence calls return and of what many steps of decoding keep.
+
+U = 2^-24 is half an fp32 step.  Tokens are few here and the rest zero, so that a state's roundings can be counted."""
+import math
+
+import pytest
+import torch
+
+import ops_plain as P
+import ssm_token_mixer_b200 as ia
+from gpu_common import device
+
+pytestmark = pytest.mark.gpu
+U = P.U
+
+
+def sparse(N, at, dk, dv, seed):
+    """q, k, v [1,2,N,.] with tokens at the given places only."""
+    gen = torch.Generator().manual_seed(seed)
+    q, k, v = (torch.zeros(1, 2, N, d) for d in (dk, dk, dv))
+    for t in at:
+        q[:, :, t], k[:, :, t], v[:, :, t] = (torch.randn(1, 2, d, generator=gen) for d in (dk, dk, dv))
+    return [x.bfloat16().cuda() for x in (q, k, v)]
+
+
+@pytest.mark.parametrize("dk,dv", [(64, 64), (128, 128), (64, 128), (128, 64)])
+@pytest.mark.parametrize("N,at", [(2, (0, 1)), (7, (0, 3, 6)), (128, (2, 60, 125)), (300, (5, 130, 290)), (900, (100, 520, 890))])
+@pytest.mark.parametrize("segments", [1, 2, 4])
+def test_returned_state(dk, dv, N, at, segments, monkeypatch):
+    """The weighted values of a returned state enter its product in three bf16 parts, which leave 2^-24 of a value; with
+    two, 2^-16 would be left, several times this bound."""
+    device()
+    monkeypatch.setenv("IA_LINEAR_SEGMENTS", str(segments))
+    q, k, v = sparse(N, at, dk, dv, seed=N + dk)
+    g = torch.tensor([-0.003, -0.011]).cuda()
+    assert ia.linear_path(1, 2, N, dk, dv, "bf16") == "tensor_core"
+    got = ia.linear_prefill_fwd(q, k, v, g, want_state=True)["state"].view(2, dk, dv).double()
+    ia.check_device_errors()
+    want, bound = torch.zeros_like(got), torch.zeros_like(got)
+    chunks = -(-N // 128)
+    for t in at:
+        for h in range(2):
+            far = N - 1 - t
+            term = math.exp(float(g[h]) * far) * torch.outer(k[0, h, t].double(), v[0, h, t].double())
+            want[h] += term
+            # the weight (expf's 2 ulp and its argument's rounding), its product, what three parts leave; three
+            # accumulations of at most two steps each, the parts' sum; per chunk the decay's 2 ulp, its product and a sum
+            n = 4 + abs(float(g[h])) * far + 1 + 1 + 3 * 2 * 2 + 1 + 6 * chunks
+            bound[h] += n * U * term.abs()
+    assert bound.max() <= 40 * U * want.abs().max() * 3 + 1e-30
+    over = (got - want).abs() - bound
+    assert (over <= 0).all(), f"{((got - want).abs() / bound.clamp(min=1e-30)).max().item():.2f} times the bound"
