@@ -45,6 +45,11 @@ inline int lin_zblocks(int dz) { return (dz + kLinZB - 1) / kLinZB; }
 // multiples still give lambda^0 = 1 and lambda^n = 0 (0 * -inf would be NaN).
 __host__ __device__ inline float lin_log_decay(float g) { return g > -1e30f ? g : -1e30f; }
 
+// Decays above 1/2 are taken from expm1, so that those near 1 keep their bits;
+// below, where 1 + expm1 would cancel, from exp.  Exponents above this are the
+// former's.
+constexpr float kLinSlow = -0.693147f;
+
 bool lin_tc_supported(const ia_linear_shape_t& s);
 constexpr int kLinTcChunk = 128;
 

@@ -3,6 +3,12 @@
 // with S [d_k][d_v] fp32 read and written once: 8 d_k d_v bytes per (b,h), so
 // HBM bounds it (latency at small batches).
 //
+// Where lambda > 1/2, lambda S is formed as S + (lambda - 1) S with expm1: lambda
+// rounded to fp32 is off by up to 2^-25, every step the same way, which 4096 steps
+// of a lambda near 1 make 1.2e-4 of a state.  Below 1/2 that sum would cancel, and
+// a product is the accurate form.  The two have loops of their own; a choice per
+// entry took 4 to 10 % more time.
+//
 // A CTA takes CW columns of one (b,h) and all its rows: thread (r, c) holds
 // VEC columns of the rows r, r + R, ..., four or eight loaded before the first
 // is used, so that an SM has 128 KB in flight; the sum over rows is a sum over
@@ -14,12 +20,13 @@
 // reordering of a beam search rides on a read and a write that happen anyway.
 //
 // Measured: 64 sequences of 16 heads of 128 x 128 through parents into another
-// buffer 18.3 us (114 MB: 94 % of the copy rate; 24.0 with 16 rows in flight, two
+// buffer 18.2 us (114 MB: 95 % of the copy rate; 24.0 with 16 rows in flight, two
 // CTAs per SM and plain stores, 20.4 with stores that L2 need not keep), in
-// place 15.9 us (part of the 67 MB of states stays in L2); 256 of 64 x 64 22.4 us
+// place 14.1 us (part of the 67 MB of states stays in L2); 256 of 64 x 64 22.4 us
 // through parents of 8 beams (111 MB; 49.5 before); one sequence 2.6 us, the
 // launch and one read's latency.
 #include <algorithm>
+#include <type_traits>
 
 #include "ia_device.cuh"
 #include "ia_internal.h"
@@ -96,7 +103,7 @@ __global__ void __launch_bounds__(kThreads, kDepth == 4 ? 5 : 4) lin_decode_kern
   }
   const float graw = log_decay[h];
   if (!(graw <= 0.f) && tid == 0) atomicOr(err, kErrParamRange);
-  const float lam = expf(lin_log_decay(graw));
+  const float gl = lin_log_decay(graw);
 
   const float* in = sin + src * dk * dv + col;
   float* out = sout + bh * dk * dv + col;
@@ -112,6 +119,8 @@ __global__ void __launch_bounds__(kThreads, kDepth == 4 ? 5 : 4) lin_decode_kern
     }
   };
   fetch(r0);
+  const bool slow = gl > kLinSlow;
+  const float a = slow ? expm1f(gl) : expf(gl);
   if (tid < dk) {
     sk[tid] = ld(k, bh * dk + tid);
     sq[tid] = ld(q, bh * dk + tid);
@@ -123,22 +132,27 @@ __global__ void __launch_bounds__(kThreads, kDepth == 4 ? 5 : 4) lin_decode_kern
     acc.v[e] = 0.f;
   }
   __syncthreads();
-  for (int base = r0; base < dk; base += kDepth * R) {
-    if (base != r0) fetch(base);
+  auto rows = [&](auto near_one) {
+    for (int base = r0; base < dk; base += kDepth * R) {
+      if (base != r0) fetch(base);
 #pragma unroll
-    for (int d = 0; d < kDepth; ++d) {
-      const int i = base + d * R;
-      if (!active || i >= dk) continue;
-      const float ki = sk[i], qi = sq[i];
-      Vec<VEC> n;
+      for (int d = 0; d < kDepth; ++d) {
+        const int i = base + d * R;
+        if (!active || i >= dk) continue;
+        const float ki = sk[i], qi = sq[i];
+        Vec<VEC> n;
 #pragma unroll
-      for (int e = 0; e < VEC; ++e) {
-        n.v[e] = fmaf(lam, s[d].v[e], ki * vv.v[e]);
-        acc.v[e] = fmaf(qi, n.v[e], acc.v[e]);
+        for (int e = 0; e < VEC; ++e) {
+          const float x = s[d].v[e];
+          n.v[e] = near_one() ? fmaf(ki, vv.v[e], fmaf(a, x, x)) : fmaf(a, x, ki * vv.v[e]);
+          acc.v[e] = fmaf(qi, n.v[e], acc.v[e]);
+        }
+        store_vec<VEC>(out + static_cast<long long>(i) * dv, n, apart);
       }
-      store_vec<VEC>(out + static_cast<long long>(i) * dv, n, apart);
     }
-  }
+  };
+  if (slow) rows(std::true_type());
+  else rows(std::false_type());
 #pragma unroll
   for (int e = 0; e < VEC; ++e) part[tid * VEC + e] = acc.v[e];
   __syncthreads();
@@ -170,7 +184,7 @@ cudaError_t launch(const ia_linear_shape_t& s, const void* q, const void* k, con
                                     static_cast<T*>(o), err);
   };
   // Rows of a thread: with few, a kernel of fewer registers and one more CTA per
-  // SM (256 sequences of 16 heads of 64 x 64: 18.5 us, and 23 with eight rows).
+  // SM (256 sequences of 16 heads of 64 x 64: 18.0 us, and 23 with eight rows).
   const int rows = (s.d_k + kThreads / tc - 1) / (kThreads / tc);
   if (vec) {
     if (rows <= 4) go(lin_decode_kernel<T, 4, 4>);

@@ -3,6 +3,7 @@
 U = 2^-24 is half an fp32 step.  Tokens are few here and the rest zero, so that a state's roundings can be counted."""
 import math
 
+import numpy as np
 import pytest
 import torch
 
@@ -50,3 +51,29 @@ def test_returned_state(dk, dv, N, at, segments, monkeypatch):
     assert bound.max() <= 40 * U * want.abs().max() * 3 + 1e-30
     over = (got - want).abs() - bound
     assert (over <= 0).all(), f"{((got - want).abs() / bound.clamp(min=1e-30)).max().item():.2f} times the bound"
+
+
+def test_decode_does_not_drift():
+    """4096 steps whose decay lies midway between two fp32 numbers: its rounding would shift every entry the same way.
+
+    Rounded to fp32, such a decay is off by 2^-25, and 4096 steps by 1.2e-4.  What remains is rounded once a step, which
+    as a random walk is sqrt(4096) U = 3.8e-6 per entry and vanishes in the mean over 8192 entries, and the 2 ulp of
+    expm1 at 2^-11, which add up to 4096 * 2^-34 = 2.4e-7."""
+    device()
+    T, d = 4096, 64
+    g = -np.float32(2.0) ** -11 * (1 + np.arange(4096, dtype=np.float32) * np.float32(2.0) ** -20)
+    exact = np.exp(g.astype(np.float64))
+    off = (exact.astype(np.float32).astype(np.float64) - exact) / exact
+    g = torch.tensor([g[off.argmax()], g[off.argmin()]]).cuda()
+    assert off.max() > 2.9e-8 and off.min() < -2.9e-8
+    gen = torch.Generator().manual_seed(1)
+    s = torch.randn(1, 2, d, d, generator=gen).cuda()
+    z = torch.zeros(1, 2, d, dtype=torch.bfloat16, device="cuda")
+    state = s.flatten().clone()
+    for _ in range(T):
+        ia.linear_decode_step(z, z, z, g, state)
+    ia.check_device_errors()
+    want = torch.exp(g.double() * T)[None, :, None, None] * s.double()
+    rel = (state.view_as(s).double() / want - 1)[0]
+    assert rel.mean((1, 2)).abs().max() <= 1e-6
+    assert rel.abs().max() <= 6 * math.sqrt(T) * U
