@@ -9,9 +9,10 @@
 //   out_t = scale (sum_s P_ts z_s + lambda^(p_t + 1) x_t S)
 //   S    <- lambda^L S + sum_s lambda^(L-1-p_s) y_s z_s^T      (L tokens in it)
 // Every power of lambda that appears has an exponent >= 0, so nothing
-// overflows for any decay, and lambda^L S is formed as S + (lambda^L - 1) S
-// with expm1, whose relative error does not add up over hundreds of chunks
-// when lambda is close to 1.
+// overflows for any decay.  lambda^L S is formed as S + (lambda^L - 1) S with
+// expm1 where lambda^L > 1/2, whose relative error does not add up over hundreds
+// of chunks when lambda is close to 1, and as a product below, where that sum
+// would cancel (and leave 0 for a lambda^L under 2^-25).
 #include <algorithm>
 #include <cmath>
 #include <cstdint>
@@ -260,7 +261,8 @@ __global__ void __launch_bounds__(T, 512 / T) lin_simt_kernel(const __grid_const
       for (int i = lane; i < dx4; i += 32) Y[t * dxs + i] *= w;
     }
     __syncthreads();
-    const float dec = bad < C ? __int_as_float(0x7fc00000) : expm1f(g * Lw);
+    const bool slow = g * Lw > kLinSlow;
+    const float dec = bad < C ? __int_as_float(0x7fc00000) : lin_decay(g * Lw);
     const int jt = zw4 / 4;
     for (int tile = tid; tile < (dx4 / 4) * jt; tile += T) {
       const int i0 = (tile / jt) * 4, j0 = (tile % jt) * 4;
@@ -282,10 +284,10 @@ __global__ void __launch_bounds__(T, 512 / T) lin_simt_kernel(const __grid_const
       for (int r = 0; r < 4; ++r) {
         float4* sp = reinterpret_cast<float4*>(S + (i0 + r) * zs + j0);
         float4 s = *sp;
-        s.x = fmaf(dec, s.x, s.x) + acc[r][0];
-        s.y = fmaf(dec, s.y, s.y) + acc[r][1];
-        s.z = fmaf(dec, s.z, s.z) + acc[r][2];
-        s.w = fmaf(dec, s.w, s.w) + acc[r][3];
+        s.x = fmaf(dec, s.x, slow ? s.x : 0.f) + acc[r][0];
+        s.y = fmaf(dec, s.y, slow ? s.y : 0.f) + acc[r][1];
+        s.z = fmaf(dec, s.z, slow ? s.z : 0.f) + acc[r][2];
+        s.w = fmaf(dec, s.w, slow ? s.w : 0.f) + acc[r][3];
         *sp = s;
       }
     }
@@ -320,8 +322,9 @@ __global__ void __launch_bounds__(kThreads) lin_carry_kernel(const __grid_consta
   const long long e = static_cast<long long>(blockIdx.y) * kThreads + threadIdx.x;
   if (e >= per) return;
   const long long bh = blockIdx.x;
-  const double dec = expm1(static_cast<double>(lin_log_decay(a.log_decay[bh % a.H])) * chunk * a.cps);
-  const float decf = static_cast<float>(dec);
+  const double far = static_cast<double>(lin_log_decay(a.log_decay[bh % a.H])) * chunk * a.cps;
+  const bool slow = far > kLinSlow;
+  const float decf = static_cast<float>(slow ? expm1(far) : exp(far));
   float* s = pr.seg + bh * (a.nseg - 1) * per + e;
   float run = s[0];
   constexpr int kBatch = 8;   // loads in flight
@@ -332,7 +335,7 @@ __global__ void __launch_bounds__(kThreads) lin_carry_kernel(const __grid_consta
 #pragma unroll
     for (int j = 0; j < kBatch; ++j)
       if (i + j < a.nseg - 1) {
-        run = fmaf(decf, run, run) + v[j];
+        run = fmaf(decf, run, slow ? run : 0.f) + v[j];
         s[(i + j) * per] = run;
       }
   }

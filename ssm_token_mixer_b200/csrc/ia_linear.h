@@ -49,6 +49,10 @@ __host__ __device__ inline float lin_log_decay(float g) { return g > -1e30f ? g 
 // below, where 1 + expm1 would cancel, from exp.  Exponents above this are the
 // former's.
 constexpr float kLinSlow = -0.693147f;
+#ifdef __CUDACC__
+// exp(e) - 1 or exp(e), by that rule: what S is multiplied with, beside S or alone.
+__device__ __forceinline__ float lin_decay(float e) { return e > kLinSlow ? expm1f(e) : expf(e); }
+#endif
 
 bool lin_tc_supported(const ia_linear_shape_t& s);
 constexpr int kLinTcChunk = 128;

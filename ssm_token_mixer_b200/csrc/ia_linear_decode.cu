@@ -120,7 +120,7 @@ __global__ void __launch_bounds__(kThreads, kDepth == 4 ? 5 : 4) lin_decode_kern
   };
   fetch(r0);
   const bool slow = gl > kLinSlow;
-  const float a = slow ? expm1f(gl) : expf(gl);
+  const float a = lin_decay(gl);
   if (tid < dk) {
     sk[tid] = ld(k, bh * dk + tid);
     sq[tid] = ld(q, bh * dk + tid);

@@ -462,7 +462,7 @@ __global__ void __launch_bounds__(has_w(MAXDX, STATE_ONLY) ? 640 : 512, 1) lin_t
     const long long per_state = static_cast<long long>(dx) * dz;
     const long long at_state = static_cast<long long>(row) * dz + z0 + col;
     uint64_t S[kCols / 2];       // its columns in pairs
-    const float dec_full = expm1f(g * C);
+    const float dec_full = lin_decay(g * C);
     {
       const float* s0 = seg == 0 ? (pr.state_in ? pr.state_in + bh * per_state : nullptr)
                                  : STATE_ONLY ? nullptr : pr.seg + (static_cast<long long>(bh) * (a.nseg - 1) + seg - 1) * per_state;
@@ -487,8 +487,16 @@ __global__ void __launch_bounds__(has_w(MAXDX, STATE_ONLY) ? 640 : 512, 1) lin_t
     for (int c = -1; c < n; ++c) {
       if (c >= 0) {
       const int L = min(C, a.N - chunk_at(c) * C);
-      const float dec = L == C || rev ? dec_full : expm1f(g * L);
+      const bool whole = L == C || rev;
+      const float dec = whole ? dec_full : lin_decay(g * L);
       const uint64_t dec2 = f2_pack(dec, dec);
+      if (g * (whole ? C : L) > kLinSlow) {   // before K is there, and two loops rather than a choice per entry
+#pragma unroll
+        for (int i = 0; i < kCols / 2; ++i) S[i] = f2_fma(dec2, S[i], S[i]);
+      } else {
+#pragma unroll
+        for (int i = 0; i < kCols / 2; ++i) S[i] = f2_mul(dec2, S[i]);
+      }
       if (STATE_ONLY ? !warp_wait(k_full(c), c >> 1) : !warp_wait(kKFull, c)) break;
       tc_fence_after();
       const uint32_t tk = tmem + (static_cast<uint32_t>(warp - 8) << 21) + k_col(c);
@@ -508,8 +516,7 @@ __global__ void __launch_bounds__(has_w(MAXDX, STATE_ONLY) ? 640 : 512, 1) lin_t
           for (int k = 0; k < 8; ++k) {
             uint64_t add = f2_pack(__uint_as_float(v[2 * k]), __uint_as_float(v[2 * k + 1]));
             if (!K::kO1Twice) add = f2_add(add, f2_pack(__uint_as_float(w[2 * k]), __uint_as_float(w[2 * k + 1])));
-            uint64_t& S2 = S[8 * i + k];
-            S2 = f2_add(f2_fma(dec2, S2, S2), add);
+            S[8 * i + k] = f2_add(S[8 * i + k], add);
           }
         }
       }

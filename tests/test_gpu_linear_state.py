@@ -53,6 +53,39 @@ def test_returned_state(dk, dv, N, at, segments, monkeypatch):
     assert (over <= 0).all(), f"{((got - want).abs() / bound.clamp(min=1e-30)).max().item():.2f} times the bound"
 
 
+@pytest.mark.parametrize("dt,d", [(torch.bfloat16, 64), (torch.bfloat16, 128), (torch.float32, 64), (torch.float32, 40)])
+@pytest.mark.parametrize("decay", [-1e-3, -0.04, -0.3, -0.69, -0.7, -2.5, -9.0])
+@pytest.mark.parametrize("N", [1, 2, 9, 33, 150, 400])
+@pytest.mark.parametrize("segments", [1, 3])
+def test_a_state_that_only_decays(dt, d, decay, N, segments, monkeypatch):
+    """Keys of zero (padding): the state after them is lambda^N times the one before, to fp32, however small that is."""
+    if decay * N < -80:
+        pytest.skip("below fp32's range")
+    device()
+    monkeypatch.setenv("IA_LINEAR_SEGMENTS", str(segments))
+    gen = torch.Generator().manual_seed(N)
+    q, k, v = torch.zeros(1, 1, N, d), torch.zeros(1, 1, N, d), torch.randn(1, 1, N, d, generator=gen)
+    s = torch.randn(1, 1, d, d, generator=gen).cuda()
+    g = torch.tensor([decay]).cuda()
+    args = [x.to(dt).cuda() for x in (q, k, v)]
+    got = ia.linear_prefill_fwd(*args, g, state_in=s, want_state=True)["state"].view(d, d).double()
+    ia.check_device_errors()
+    exact = float(g[0].double())
+    want = math.exp(exact * N) * s.view(d, d).double()
+    # per chunk (32 tokens at least): the decay's 2 ulp (4 U, and as much again where it is taken from 1), a product and
+    # a sum; the exponents' roundings add up to |g| N U
+    n = (-(-N // 32)) * 8 + abs(exact) * N + 8
+    assert ((got - want).abs() <= n * U * want.abs()).all(), ((got / want - 1).abs().max() / U).item()
+    # and token by token
+    state = s.flatten().clone()
+    x = [a[:, :, 0].contiguous() for a in args]
+    for _ in range(N):
+        ia.linear_decode_step(*x, g, state)
+    ia.check_device_errors()
+    n = N * 8 + abs(exact) * N + 8
+    assert ((state.view(d, d).double() - want).abs() <= n * U * want.abs()).all()
+
+
 def test_decode_does_not_drift():
     """4096 steps whose decay lies midway between two fp32 numbers: its rounding would shift every entry the same way.
 
