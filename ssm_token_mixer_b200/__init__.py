@@ -672,15 +672,19 @@ def _scratch(nbytes, dev, workspace):
     return workspace, _ad(workspace), _nbytes(workspace)
 
 
-def _apart(name, out, *others, in_place=False):
-    """A given output may not share memory with an input (with in_place: it may be an input's buffer as a whole)."""
+def _apart(name, out, *others, in_place=()):
+    """A given output or workspace may not share memory with the others (None skipped); it may be the buffer of one of
+    in_place as a whole."""
     a, n = out.data_ptr(), _nbytes(out)
     for t in others:
-        if t is None:
-            continue
+        if t is not None:
+            b = t.data_ptr()
+            if a < b + _nbytes(t) and b < a + n:
+                raise ValueError(f"{name} overlaps an input or another output in memory")
+    for t in in_place:
         b = t.data_ptr()
-        if a < b + _nbytes(t) and b < a + n and not (in_place and a == b):
-            raise ValueError(f"{name} overlaps an input in memory")
+        if a < b + _nbytes(t) and b < a + n and a != b:
+            raise ValueError(f"{name} overlaps an input in memory without being its buffer")
 
 
 def linear_prefill_fwd(q, k, v, log_decay, scale=None, state_in=None, want_state=False, o=None, workspace=None,
@@ -698,9 +702,10 @@ def linear_prefill_fwd(q, k, v, log_decay, scale=None, state_in=None, want_state
         _need("state_in", state_in, dtype=torch.float32, numel=n_state)
     if o is not None:
         _need("o", o, v.shape, q.dtype)
-        _apart("o", o, q, k, v, state_in)
+        _apart("o", o, q, k, v, log_decay, state_in)
     if workspace is not None:
         _need("workspace", workspace)
+        _apart("workspace", workspace, q, k, v, log_decay, state_in, o)
     dev = _place(("q", q), ("k", k), ("v", v), ("log_decay", log_decay), ("state_in", state_in), ("o", o),
                         ("workspace", workspace))
     ref = ctypes.byref(shp)
@@ -725,6 +730,7 @@ def linear_fwd_bwd(q, k, v, log_decay, dO, scale=None, workspace=None, stream=No
     _need("dO", dO, v.shape, q.dtype)
     if workspace is not None:
         _need("workspace", workspace)
+        _apart("workspace", workspace, q, k, v, log_decay, dO)
     dev = _place(("q", q), ("k", k), ("v", v), ("log_decay", log_decay), ("dO", dO), ("workspace", workspace))
     ref = ctypes.byref(shp)
     ctx, raw = _on(dev, stream)
@@ -746,31 +752,40 @@ def linear_decode_step(q, k, v, log_decay, state, scale=None, state_out=None, pa
     another buffer."""
     lib = load_library()
     shp = _check_linear_args(3, q, k, v, log_decay)
-    n_state = shp.B * shp.H * shp.d_k * shp.d_v
-    _need("state", state, dtype=torch.float32, numel=n_state)
+    B, H, d_k = q.shape
+    d_v = v.shape[2]
+    n_state = B * H * d_k * d_v
+    if not (_ok(state, None, torch.float32) and state.numel() == n_state):
+        _need("state", state, dtype=torch.float32, numel=n_state)
     if state_out is not None:
         _need("state_out", state_out, dtype=torch.float32, numel=n_state)
     beams = 0
     if parents is not None:
-        _need("parents", parents, dtype=torch.int32, numel=shp.B)
+        _need("parents", parents, dtype=torch.int32, numel=B)
         if parents.dim() != 2:
             raise ValueError(f"parents must be [B/beams, beams], got shape {tuple(parents.shape)}")
         beams = parents.shape[1]
         if state_out is None:
             raise ValueError("state_out is needed with parents: a state may have several followers")
+    out = state if state_out is None else state_out
     if o is not None:
         _need("o", o, v.shape, q.dtype)
-        _apart("o", o, q, k, v, state, state_out)
+        _apart("o", o, q, k, v, log_decay, state, state_out, parents)
     dev = _place(("q", q), ("k", k), ("v", v), ("log_decay", log_decay), ("state", state),
                         ("state_out", state_out), ("parents", parents), ("o", o))
-    out = state if state_out is None else state_out
+    aq, ak, av, ag, at = _ad(q), _ad(k), _ad(v), _ad(log_decay), _ad(out)
+    ap = None if parents is None else _ad(parents)
+    # the state may not share memory with what a step reads (state itself is looked at by the library)
+    end, heads = at + 4 * n_state, B * H * (4 if q.dtype is torch.float32 else 2)
+    if (aq < end and at < aq + heads * d_k or ak < end and at < ak + heads * d_k or av < end and at < av + heads * d_v or
+            ag < end and at < ag + 4 * H or ap is not None and ap < end and at < ap + 4 * B):
+        _apart("state" if state_out is None else "state_out", out, q, k, v, log_decay, parents)
     ctx, raw = _on(dev, stream)
     with ctx:
         if o is None:
             o = torch.empty_like(v)
-        rc = lib.ia_linear_decode_step(ctypes.byref(shp), _ad(q), _ad(k), _ad(v), _ad(log_decay),
-                                       shp.d_k ** -0.5 if scale is None else scale, _ad(state), _ad(parents),
-                                       beams, _ad(out), _ad(o), raw)
+        rc = lib.ia_linear_decode_step(ctypes.byref(shp), aq, ak, av, ag, d_k ** -0.5 if scale is None else scale,
+                                       _ad(state), ap, beams, at, _ad(o), raw)
     _check(rc, "ia_linear_decode_step")
     return {"o": o, "state": out}
 
@@ -796,7 +811,7 @@ def layer_norm_fwd(x, weight=None, bias=None, eps=1e-5, y=None, stream=None):
     rows, D, code = _check_rows(x, weight, bias)
     if y is not None:
         _need("y", y, x.shape, x.dtype)
-        _apart("y", y, x, in_place=True)
+        _apart("y", y, weight, bias, in_place=(x,))
     dev = _place(("x", x), ("weight", weight), ("bias", bias), ("y", y))
     ctx, raw = _on(dev, stream)
     with ctx:
@@ -825,9 +840,10 @@ def layer_norm_bwd(dy, x, mean, rstd, weight=None, want_params=True, dx=None, wo
         _need(name, t, dtype=torch.float32, numel=rows)
     if dx is not None:
         _need("dx", dx, x.shape, x.dtype)
-        _apart("dx", dx, dy, x, in_place=True)
+        _apart("dx", dx, weight, mean, rstd, in_place=(dy, x))
     if workspace is not None:
         _need("workspace", workspace)
+        _apart("workspace", workspace, dy, x, weight, mean, rstd, dx)
     dev = _place(("x", x), ("dy", dy), ("mean", mean), ("rstd", rstd), ("weight", weight), ("dx", dx),
                         ("workspace", workspace))
     ctx, raw = _on(dev, stream)
@@ -870,6 +886,7 @@ def beam_select(logits, scores, K, finished=None, end_token=0, workspace=None, s
             raise TypeError(f"finished has dtype {finished.dtype}, expected bool or uint8")
     if workspace is not None:
         _need("workspace", workspace)
+        _apart("workspace", workspace, logits, scores, finished)
     dev = _place(("logits", logits), ("scores", scores), ("finished", finished), ("workspace", workspace))
     ctx, raw = _on(dev, stream)
     with ctx:
@@ -891,6 +908,7 @@ def _reorder(call, where, shp, per, B, state, parents, out, stream):
     G, wout = parents.shape
     if out is not None:
         _need("out", out, dtype=torch.float32, numel=per * G * wout)
+        _apart("out", out, parents)   # state: see the library
     dev = _place(("state", state), ("parents", parents), ("out", out))
     ctx, raw = _on(dev, stream)
     with ctx:
