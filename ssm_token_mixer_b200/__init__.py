@@ -608,6 +608,7 @@ def _on(idx, stream):
 
 
 def _linear_shape(B, H, N, d_k, d_v, dtype) -> IALinearShape:
+    _small("shape", B, H, N, d_k, d_v)
     code = dtype if isinstance(dtype, int) else (IA_BF16 if dtype in (torch.bfloat16, "bf16") else IA_F32)
     return IALinearShape(int(B), int(H), int(N), int(d_k), int(d_v), code)
 
@@ -639,7 +640,7 @@ def linear_fwd_bwd_segments(B, H, N, d_k, d_v, dtype) -> int:
 
 def _small(name, *sizes):
     """The library takes sizes as C ints, which would drop higher bits without a word."""
-    if max(sizes) > 0x7fffffff:
+    if max(sizes) > 0x7fffffff or min(sizes) < -0x80000000:
         raise ValueError(f"{name}: sizes above 2^31 - 1 are not supported, got {sizes}")
 
 
@@ -827,6 +828,7 @@ def layer_norm_fwd(x, weight=None, bias=None, eps=1e-5, y=None, stream=None):
 
 def layer_norm_bwd_workspace_bytes(rows, D, dtype) -> int:
     code = dtype if isinstance(dtype, int) else (IA_BF16 if dtype in (torch.bfloat16, "bf16") else IA_F32)
+    _small("D", D)
     return int(load_library().ia_layer_norm_bwd_workspace_bytes(int(rows), int(D), code))
 
 
@@ -864,6 +866,7 @@ def layer_norm_bwd(dy, x, mean, rstd, weight=None, want_params=True, dx=None, wo
 
 def beam_select_workspace_bytes(G, W, V, K, dtype) -> int:
     code = dtype if isinstance(dtype, int) else (IA_BF16 if dtype in (torch.bfloat16, "bf16") else IA_F32)
+    _small("logits", G, W, V, K)
     return int(load_library().ia_beam_select_workspace_bytes(int(G), int(W), int(V), int(K), code))
 
 
@@ -878,7 +881,7 @@ def beam_select(logits, scores, K, finished=None, end_token=0, workspace=None, s
         raise ValueError(f"logits must be [G,W,V], got shape {tuple(logits.shape)}")
     code = _dtype_code(logits)
     G, W, V = logits.shape
-    _small("logits", G, W, V, K)
+    _small("logits, K, end_token", G, W, V, K, end_token)
     _need("scores", scores, (G, W), torch.float32)
     if finished is not None:
         _need("finished", finished, (G, W))
@@ -923,6 +926,7 @@ def state_reorder(state, parents, B, H, M, d_xi, d_v, out=None, stream=None):
     """The layer's states after a beam selection: sequence g*beams + j of the result is sequence g*(B/G) +
     parents[g, j] of state (flat fp32, B sequences), parents [G, beams] int32; a parent of -1 gives a zero state.
     Returns out (allocated here when None); out=state reorders in place, moving only the beams that change."""
+    _small("shape", B, H, M, d_xi, d_v)
     shp = make_shape(B, H, 1, d_xi, d_v, M, IA_F32)
     return _reorder(load_library().ia_state_reorder, "ia_state_reorder", shp, state_bytes(1, H, M, d_xi, d_v) // 4, B,
                     state, parents, out, stream)

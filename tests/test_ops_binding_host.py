@@ -115,3 +115,27 @@ def test_beam_and_reorder():
     passes(lambda: ia.linear_state_reorder(st, par, 2, H, DK, DV, out=st))
     out = torch.zeros_like(st)
     refused(lambda: ia.linear_state_reorder(st, out.view(torch.int32)[3:5].view(1, 2), 2, H, DK, DV, out=out))
+
+
+BIG = 2**32   # as a C int: 0
+
+
+def test_sizes_that_a_c_int_would_cut_off():
+    par = torch.zeros(1, 2, dtype=torch.int32)
+    st = torch.zeros(2 * H * DK * DV)
+    x, s = torch.zeros(1, 2, 9), torch.zeros(1, 2)
+    fin = torch.zeros(1, 2, dtype=torch.bool)
+    for call in (lambda: ia.linear_state_bytes(BIG + 1, H, DK, DV), lambda: ia.linear_path(1, H, BIG + 5, DK, DV, "bf16"),
+                 lambda: ia.linear_prefill_workspace_bytes(1, H, 5, BIG + DK, DV, "f32"),
+                 lambda: ia.linear_fwd_bwd_workspace_bytes(1, BIG + H, 5, DK, DV, "f32"),
+                 lambda: ia.linear_prefill_segments(1, H, BIG + 5, DK, DV, "f32"),
+                 lambda: ia.linear_fwd_bwd_segments(1, H, 5, DK, BIG + DV, "f32"),
+                 lambda: ia.linear_state_reorder(st, par, BIG + 2, H, DK, DV),
+                 lambda: ia.state_reorder(st, par, 2, H, BIG + 1, DK, DV),
+                 lambda: ia.layer_norm_bwd_workspace_bytes(4, BIG + 8, "f32"),
+                 lambda: ia.beam_select_workspace_bytes(1, 2, BIG + 9, 2, "f32"),
+                 lambda: ia.beam_select(x, s, BIG + 2), lambda: ia.beam_select(x, s, 2, finished=fin, end_token=BIG + 3),
+                 lambda: ia.beam_select(x, s, 2, finished=fin, end_token=-BIG)):
+        with pytest.raises(ValueError, match="2\\^31"):
+            call()
+    assert ia.linear_state_bytes(2, H, DK, DV) == st.numel() * 4
