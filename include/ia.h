@@ -334,8 +334,9 @@ IA_API ia_status_t ia_decode_step_ex(const ia_shape_t* shape, const ia_options_t
  *     definition leaves finite may be NaN as well.
  *   - State: [B,H,d_k,d_v] fp32, ia_linear_state_bytes() bytes.
  *   - On the tensor cores the decayed scores and the state that meets the
- *     queries are rounded to bf16 as operands; the state that is carried and
- *     returned is not.
+ *     queries are operands in two bf16 parts, which keep 2^-16 of a value: a
+ *     bf16 output is off by its own rounding.  The state that is carried and
+ *     returned is fp32.
  *   - Outputs and the workspace may not overlap inputs or one another, unless a
  *     call says so.
  *   - d_k, d_v in 1 .. 256.

@@ -419,15 +419,16 @@ LinPlan lin_plan(const ia_linear_shape_t& s, bool train) {
   // In microseconds on a B200: a chunk of the full pass and of the state-only
   // pass, what a wave of CTAs costs beside its chunks, the launch of the
   // state-only pass, and the carry over n segments.  Measured with the state
-  // out: 56 chunks of d = 64 and 16 heads take 87.9 us whole, 73.1 in 2 segments,
-  // 44.0 in 4, 29.3 in 8 (planned), 41.7 in 12; 55 of d = 128 take 116.8, 90.0, 57.8
-  // in 4 (planned), 76.2 in 5, 67.2 in 8; 8 chunks of d = 64 and one head 16.5
-  // whole, 16.5, 13.3, 11.4 in 8 (planned); of 16 heads 16.7 whole (planned) and
-  // 17.1 in 4; training over 32 chunks of 16 heads 45.4 whole, 40.0 in 2 (planned).
+  // out: 56 chunks of d = 64 and 16 heads take 97.5 us whole, 78.5 in 2 segments,
+  // 46.2 in 4, 30.9 in 8 (planned), 43.7 in 12; 55 of d = 128 take 131.7, 98.2, 63.1
+  // in 4 (planned), 83.3 in 5, 72.1 in 8; 8 chunks of d = 64 and one head 17.9
+  // whole, 17.6, 13.9, 11.4 in 8 (planned); of 16 heads 18.0 whole, 16.1 in 4, 15.1
+  // in 8 (planned); 16 chunks of 64 heads 31.9 whole, 29.6 in 2 (planned); training
+  // over 32 chunks of 16 heads 56.9 whole, 46.9 in 2 (planned).
   // On CUDA cores B2 H4 N300 48 x 80 takes 64.4 us whole, 33.0 in 5, 21.4 in 10
   // (planned), B8 H16 N2048 d64 468, 397 in 4 (planned), 391 in 10.
   const bool wide = (p.tc && !train ? s.d_k : width) > 64;   // the tensor-core pass: x and y alone
-  const double full = p.tc ? (wide ? 1.95 : 1.3) : (wide ? 40.0 : 20.0);
+  const double full = p.tc ? (wide ? 2.2 : 1.45) : (wide ? 40.0 : 20.0);
   const double state = p.tc ? (wide ? 0.8 : 0.75) : 0.45 * full;
   const double wave = 4.5, state_wave = 3.0, extra = 1.5, carry = 2.0, carry_each = 0.04;
   if (const char* env = std::getenv("IA_LINEAR_SEGMENTS")) {   // forced count (tuning and tests)

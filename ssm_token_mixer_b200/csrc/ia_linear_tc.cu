@@ -6,19 +6,22 @@
 // the sequence, chunk after chunk.  Four contractions per chunk (tcgen05, bf16
 // operands, fp32 accumulators in TMEM):
 //   G1  A  = X Y^T            128 x 128 x dx   operands straight from TMA
-//   G2  O2 = P Z              128 x 64 x 128   P = decayed, masked A, from TMEM
-//   G3  O1 = X S              128 x 64 x dx    S = the entering state in bf16
+//   G2  O2 = P Z              128 x 64 x 256   P = decayed, masked A, from TMEM
+//   G3  O1 = X S              128 x 64 x 2 dx  S = the entering state
 //   G4  K  = Y^T (w Z)        dx x 64 x 256    w z in two bf16 parts, or three
 //   out = scale (O2 + lambda^(p+1) O1),  S <- lambda^L S + K in fp32 registers
 //
 // Rounding.  Decays multiply fp32 accumulators wherever they can: A before it
-// is rounded to P, O1 after the product, S in registers.  Only the weights
-// w = lambda^(L-1-p) of G4 sit on a contracted index, and w z is split into
-// bf16 parts.  Where the caller takes the final state in fp32 there are three
-// (2^-25 of a value left over): the state is off by 1.4e-7 (N = 2048, d = 64) to
-// 3.8e-7 (d = 128), less than token by token in fp32 (6e-7).  Where the state only
-// feeds outputs of 8 bits there are two (2^-17 left over, 2.5e-6).  P and the S
-// operand are rounded to bf16 once, like the output.
+// becomes P, O1 after the product, S in registers.  What has to be an operand
+// although it is no input (P, S, and w z with the weights w = lambda^(L-1-p) of
+// G4) goes in as bf16 parts.  P and S have two, which leave 2^-16 of a value,
+// and so have w z where the state only feeds outputs of 8 bits: an output is off
+// by its own rounding (1.66e-3 of the outputs' norm; 2.34e-3 with P and S rounded
+// to bf16 once, where training of B8 H16 N2048 d64 took 103 us and not 121, of B4
+// H16 N2048 d128 131 and not 158, and prompts a tenth less).  Where the caller
+// takes the final state in fp32, w z has three (2^-24 of a value): the state is
+// off by 1.4e-7 (N = 2048, d = 64) to 3.8e-7 (d = 128), less than token by token in
+// fp32 (6e-7).
 //
 // Roles (448 threads, four warps at most on a quarter of the registers: 128 a
 // thread; or 576, five warps: 96):
@@ -29,8 +32,9 @@
 //               not read.
 //   warps 4-7   O: O1, O2 from TMEM, out through shared memory and TMA stores,
 //               each warp its 32 rows by itself (stores straight from the
-//               registers, 32 bytes a lane, were 5 % slower)
-//   warps 8-11  S: K from TMEM, S in registers, S in bf16 to shared memory for
+//               registers, 32 bytes a lane, were 5 % slower).  With d = 64 the
+//               rows are staged in z's own tile, which G2 was the last to read
+//   warps 8-11  S: K from TMEM, S in registers, its parts to shared memory for
 //               the next chunk's G3
 //   warps 12-15 W: w z for G4 (where there are none, O does it; a pass for the
 //               states alone has nothing else for P and O to do)
@@ -74,17 +78,16 @@ constexpr uint32_t kAtom = 1024;        // 8 rows of 128 bytes
 template <int MAXDX, bool STATE_ONLY, int PARTS>
 struct Cfg {
   // Stages.  X is released late (by G3), Y by G4; Z is needed first and released
-  // last.  What the third part of w z takes comes from X and, at d = 64, from
-  // half of the output tile (prefill of B8 H16 N2048 d64: 29.3 us with two parts,
-  // 33.6 with three; before the last step, at 33.9, 37.4 with one buffer of w z
-  // and three stages of X, 39.5 with two stages of Z and three of X.  B4 H16 d128:
-  // 38.5 and 41.7; at 42.9, 46.7 with two stages of X and no output tile).
+  // last.  The second part of S and the third of w z leave X two stages at d = 64
+  // when the state is taken (three with outputs staged in z's tile) and one at
+  // d = 128, where outputs keep a tile of their own: staged in z's, with four and
+  // three of those, training of B4 H16 N2048 d128 takes 161 us, and 158.
   static constexpr bool kFull3 = PARTS == 3 && !STATE_ONLY;
-  static constexpr int NX = STATE_ONLY ? 0 : MAXDX == 64 ? (kFull3 ? 2 : 3) : kFull3 ? 1 : 2;
+  static constexpr bool kOutInZ = MAXDX == 64;
+  static constexpr int NX = STATE_ONLY ? 0 : MAXDX == 64 ? (kFull3 ? 2 : 3) : 1;
   static constexpr int NY = STATE_ONLY && PARTS == 2 ? 3 : 2;
-  static constexpr int NT = MAXDX == 64 || STATE_ONLY || kFull3 ? 3 : 2;
+  static constexpr int NT = STATE_ONLY ? 3 : MAXDX == 64 ? (kFull3 ? 3 : 4) : kFull3 ? 2 : 3;
   static constexpr int NZ = MAXDX == 64 || STATE_ONLY ? 2 : 1;         // buffers of w z
-  static constexpr int kOutCols = kFull3 && MAXDX == 64 ? 32 : 64;     // columns staged for a store
   // TMEM columns (A twice, with P in its place).  With wide X a second O1 lets
   // G3 go first, so that X's stage is loaded again early: its stages alone do
   // not hide the load (forward of B4 H16 N2048 d128 44.6 us without, 41.5 with).
@@ -100,18 +103,19 @@ struct Cfg {
   static constexpr int S_Y = NX * TX;
   static constexpr int S_Z = S_Y + NY * TX;
   static constexpr int S_ZW = S_Z + NT * kBox;          // each: its parts
-  static constexpr int S_SB = S_ZW + NZ * PARTS * kBox; // [dx][64] bf16, 128-byte swizzled
-  static constexpr int S_OUT = S_SB + (STATE_ONLY ? 0 : MAXDX * 128);
-  static constexpr int S_BAR = S_OUT + (STATE_ONLY ? 0 : C * 2 * kOutCols);
-  static constexpr int S_POW = S_BAR + 304;             // lambda^n, n = 0 .. C - 1
+  static constexpr int kSPart = MAXDX * 128;            // [dx][64] bf16, 128-byte swizzled
+  static constexpr int S_SB = S_ZW + NZ * PARTS * kBox; // S in two parts
+  static constexpr int S_OUT = S_SB + (STATE_ONLY ? 0 : 2 * kSPart);
+  static constexpr int S_BAR = S_OUT + (STATE_ONLY || kOutInZ ? 0 : kBox);
+  static constexpr int S_POW = S_BAR + 320;             // lambda^n, n = 0 .. C - 1
   static constexpr int SMEM = S_POW + C * 4 + 1024;     // + alignment of the base
-  static_assert(NX <= 3 && NY <= 3 && NT <= 3 && NZ <= 2, "their barriers");
+  static_assert(NX <= 3 && NY <= 3 && NT <= 4 && NZ <= 2, "their barriers");
   static_assert(SMEM <= 232448, "what a CTA may have");
 };
 
 enum Bar {
-  kFullX = 0, kFullY = 3, kFullZ = 6, kFreeX = 9, kFreeY = 12, kFreeZ = 15, kAFull = 18, kPReady = 20, kZReady = 22,
-  kZFree = 24, kSReady = 26, kSFree, kKFull, kOFull, kOFree, kDrain, kBars
+  kFullX = 0, kFullY = 3, kFullZ = 6, kFreeX = 10, kFreeY = 13, kFreeZ = 16, kAFull = 20, kPReady = 22, kZReady = 24,
+  kZFree = 26, kSReady = 28, kSFree, kKFull, kOFull, kOFree, kDrain, kBars
 };
 
 struct Maps {
@@ -142,6 +146,10 @@ __device__ __forceinline__ uint64_t f2_add(uint64_t a, uint64_t b) {
 }
 __device__ __forceinline__ float bf_lo(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float bf_hi(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
+// What a pair has left beside its bf16 part w (exact).
+__device__ __forceinline__ uint64_t rest2(uint64_t v, uint32_t w) {
+  return f2_fma(f2_pack(bf_lo(w), bf_hi(w)), f2_pack(-1.f, -1.f), v);
+}
 
 // True in one lane of the (converged) warp.  Unlike a test of the lane number
 // it tells the compiler that a single thread runs the branch, so the operands
@@ -226,7 +234,7 @@ __global__ void __launch_bounds__(has_w(MAXDX, STATE_ONLY) ? 640 : 512, 1) lin_t
   uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(smem + K::S_BAR + 8 * kBars);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + K::S_BAR + 8 * kBars + 4);
   int* bad = reinterpret_cast<int*>(smem + K::S_BAR + 8 * kBars + 8);   // [kBad]
-  static_assert(8 * kBars + 8 + 4 * kBad <= 304, "barriers and flags fit their slot");
+  static_assert(8 * kBars + 8 + 4 * kBad <= 320, "barriers and flags fit their slot");
   const uint32_t sbase = smem_u32(smem);
   auto sX = [&](int c) { return (c % kNX) * K::TX; };
   auto sY = [&](int c) { return K::S_Y + (c % NY) * K::TX; };
@@ -241,7 +249,8 @@ __global__ void __launch_bounds__(has_w(MAXDX, STATE_ONLY) ? 640 : 512, 1) lin_t
       const bool warps4 = i == kPReady || i == kPReady + 1 || i == kSReady || i == kOFree ||
                           i == kZReady || i == kZReady + 1;
       const bool warps8 = STATE_ONLY && (i == kZReady || i == kZReady + 1);
-      mbar_init(bars + i, warps8 ? 8 : warps4 ? 4 : 1);
+      const bool stored = K::kOutInZ && !STATE_ONLY && i >= kFreeZ && i < kFreeZ + NT;   // by O's warps
+      mbar_init(bars + i, warps8 ? 8 : warps4 || stored ? 4 : 1);
     }
     for (int i = 0; i < kBad; ++i) bad[i] = C;
     *abort_flag = 0;
@@ -284,7 +293,7 @@ __global__ void __launch_bounds__(has_w(MAXDX, STATE_ONLY) ? 640 : 512, 1) lin_t
       const uint32_t zz[4] = {zn.x, zn.y, zn.z, zn.w};
       if (i + 1 < kIter) zn = *reinterpret_cast<const uint4*>(zs + off + 16 * kRoleThreads);
       const float wt = t < L ? pw[rev ? t : L - 1 - t] : 0.f;
-      const uint64_t w2 = f2_pack(wt, wt), minus = f2_pack(-1.f, -1.f);
+      const uint64_t w2 = f2_pack(wt, wt);
       uint32_t part[PARTS][4];
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
@@ -293,7 +302,7 @@ __global__ void __launch_bounds__(has_w(MAXDX, STATE_ONLY) ? 640 : 512, 1) lin_t
 #pragma unroll
         for (int k = 0; k < PARTS; ++k) {
           part[k][e] = pack2(v);
-          if (k + 1 < PARTS) v = f2_fma(f2_pack(bf_lo(part[k][e]), bf_hi(part[k][e])), minus, v);   // exact
+          if (k + 1 < PARTS) v = rest2(v, part[k][e]);
         }
       }
 #pragma unroll
@@ -349,10 +358,14 @@ __global__ void __launch_bounds__(has_w(MAXDX, STATE_ONLY) ? 640 : 512, 1) lin_t
           const uint64_t ff = f2_pack(f, f);
 #pragma unroll
           for (int hf = 0; hf < 2; ++hf) {   // 16 columns at a time
-            uint32_t w[8];
+            uint32_t w[16];   // of 16 columns: the first parts of their 8 pairs, then the second ones
+            auto split = [&](int i, uint64_t pair) {
+              w[i] = pack2(pair);
+              w[8 + i] = pack2(rest2(pair, w[i]));
+            };
             if (side < 0) {
 #pragma unroll
-              for (int i = 0; i < 8; ++i) w[i] = 0u;
+              for (int i = 0; i < 16; ++i) w[i] = 0u;
             } else {
               uint32_t v[16];
               tmem_ld16(ta + 32 * gr + 16 * hf, v);
@@ -360,7 +373,7 @@ __global__ void __launch_bounds__(has_w(MAXDX, STATE_ONLY) ? 640 : 512, 1) lin_t
               if (side > 0) {
 #pragma unroll
                 for (int i = 0; i < 8; ++i)
-                  w[i] = pack2(f2_mul(f2_mul(f2_pack(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1])), e[8 * hf + i]), ff));
+                  split(i, f2_mul(f2_mul(f2_pack(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1])), e[8 * hf + i]), ff));
               } else {
                 // select, not multiply: a masked score may be infinite or NaN
                 auto val = [&](int j) {
@@ -368,11 +381,11 @@ __global__ void __launch_bounds__(has_w(MAXDX, STATE_ONLY) ? 640 : 512, 1) lin_t
                   return d >= 0 ? __uint_as_float(v[j]) * pw[max(d, 0)] : 0.f;
                 };
 #pragma unroll
-                for (int i = 0; i < 8; ++i) w[i] = pack_bf16(val(2 * i), val(2 * i + 1));
+                for (int i = 0; i < 8; ++i) split(i, f2_pack(val(2 * i), val(2 * i + 1)));
                 __syncwarp();   // d >= 0 differs between lanes, and the store is the whole warp's
               }
             }
-            tmem_st8(ta + 16 * gr + 8 * hf, w);   // columns of A that this lane has read already
+            tmem_st16(ta + 32 * gr + 16 * hf, w);   // the columns of A that it came from
           }
         }
         tmem_st_wait();
@@ -389,26 +402,6 @@ __global__ void __launch_bounds__(has_w(MAXDX, STATE_ONLY) ? 640 : 512, 1) lin_t
     const float hd = a.scale * expf(g * (p + 1));
     const uint64_t scale2 = f2_pack(a.scale, a.scale), hd2 = f2_pack(hd, hd);
     const CUtensorMap* mo = &maps.out[pi];
-    constexpr int kRow = 2 * K::kOutCols;                  // bytes; a warp stages its 32 rows of them
-    uint8_t* stage = smem + K::S_OUT + u * kRow;
-    const int swz = K::kOutCols == 64 ? u & 7 : (u >> 1) & 3;
-    auto stage_free = [&]() {   // the warp's last store has left its rows
-      if (lane == 0) bulk_wait_read_0();
-      __syncwarp();
-    };
-    auto stage_out = [&](int col, int t0, bool last) {
-      fence_async_smem();
-      if (last) tc_fence_before();
-      __syncwarp();
-      if (lane == 0) {
-        if (last) mbar_arrive(bars + kOFree);
-        const int t = t0 + 32 * (warp - 4);
-        if (t < a.N) {
-          tma_store_3d(mo, sbase + K::S_OUT + (warp - 4) * 32 * kRow, col, t, bh);
-          bulk_commit();
-        }
-      }
-    };
 #pragma unroll 1
     for (int c = -1; c < n; ++c) {
       if (!kW && c + 1 < n) alive = alive && weigh(c + 1, u, STATE_ONLY);
@@ -422,12 +415,13 @@ __global__ void __launch_bounds__(has_w(MAXDX, STATE_ONLY) ? 640 : 512, 1) lin_t
       const int from = *reinterpret_cast<volatile int*>(bad + c % kBad);
       if (u == 0) bad[(c + kBad - 1) % kBad] = C;   // the last chunk's: every warp has read it before this kOFull
       const uint32_t to = tmem + (static_cast<uint32_t>(warp - 4) << 21);
-      const int t0 = chunk_at(c) * C;
-      if (K::kOutCols == 64) stage_free();
+      const int off = (K::kOutInZ ? sZ(c) : K::S_OUT) + 128 * u;   // this thread's row, 128-byte swizzled like z
+      if (!K::kOutInZ) {   // the warp's last store has left its rows
+        if (lane == 0) bulk_wait_read_0();
+        __syncwarp();
+      }
 #pragma unroll 1
       for (int q = 0; q < 4; ++q) {
-        const int at = K::kOutCols == 64 ? q : q & 1;      // 32-byte piece of the staged row
-        if (K::kOutCols == 32 && at == 0) stage_free();
         uint32_t v1[16], v2[16], w[8];
         tmem_ld16(to + K::kTO1 + (K::kO1Twice ? 64 * (c & 1) : 0) + 16 * q, v1);
         tmem_ld16(to + K::kTO2 + 16 * q, v2);
@@ -444,11 +438,24 @@ __global__ void __launch_bounds__(has_w(MAXDX, STATE_ONLY) ? 640 : 512, 1) lin_t
 #pragma unroll
           for (int i = 0; i < 8; ++i) w[i] = 0x7fc07fc0u;   // NaN
         __syncwarp();   // p >= from differs between lanes, and the next loads from TMEM are the whole warp's
-        *reinterpret_cast<uint4*>(stage + (((2 * at) ^ swz) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
-        *reinterpret_cast<uint4*>(stage + (((2 * at + 1) ^ swz) << 4)) = make_uint4(w[4], w[5], w[6], w[7]);
-        if (K::kOutCols == 32 && q == 1) stage_out(z0, t0, false);
+        *reinterpret_cast<uint4*>(smem + off + (((2 * q) ^ (u & 7)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
+        *reinterpret_cast<uint4*>(smem + off + (((2 * q + 1) ^ (u & 7)) << 4)) = make_uint4(w[4], w[5], w[6], w[7]);
       }
-      stage_out(K::kOutCols == 64 ? z0 : z0 + 32, t0, true);
+      fence_async_smem();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) {
+        mbar_arrive(bars + kOFree);
+        const int t = chunk_at(c) * C + u;   // of the warp's first row
+        if (t < a.N) {
+          tma_store_3d(mo, sbase + off, z0, t, bh);
+          bulk_commit();
+        }
+        if (K::kOutInZ) {
+          bulk_wait_read_0();
+          mbar_arrive(bars + kFreeZ + c % NT);
+        }
+      }
     }
     if (lane == 0) bulk_wait_all();
   } else if (warp < 12) {
@@ -476,9 +483,17 @@ __global__ void __launch_bounds__(has_w(MAXDX, STATE_ONLY) ? 640 : 512, 1) lin_t
     auto write_operand = [&]() {   // and K has been read: the next G4 may overwrite it
       if (holds)
 #pragma unroll
-        for (int j = 0; j < kCols / 8; ++j)
-          *reinterpret_cast<uint4*>(smem + K::S_SB + row * 128 + (((col / 8 + j) ^ (row & 7)) << 4)) =
-              make_uint4(pack2(S[4 * j]), pack2(S[4 * j + 1]), pack2(S[4 * j + 2]), pack2(S[4 * j + 3]));
+        for (int j = 0; j < kCols / 8; ++j) {
+          uint32_t w[8];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            w[k] = pack2(S[4 * j + k]);
+            w[4 + k] = pack2(rest2(S[4 * j + k], w[k]));
+          }
+          uint8_t* dst = smem + K::S_SB + row * 128 + (((col / 8 + j) ^ (row & 7)) << 4);
+          *reinterpret_cast<uint4*>(dst) = make_uint4(w[0], w[1], w[2], w[3]);
+          *reinterpret_cast<uint4*>(dst + K::kSPart) = make_uint4(w[4], w[5], w[6], w[7]);
+        }
       fence_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(bars + kSReady);
@@ -603,10 +618,13 @@ __global__ void __launch_bounds__(has_w(MAXDX, STATE_ONLY) ? 640 : 512, 1) lin_t
       auto g3 = [&](int c) {
         const uint64_t x = kmajor(sX(c)), sb = mnmajor(K::S_SB);
 #pragma unroll
-        for (int b = 0; b < MAXDX / 64; ++b)
+        for (int part = 0; part < 2; ++part)
 #pragma unroll
-          for (int kk = 0; b < nbx && kk < 4; ++kk)
-            mma_ss(lead, tmem + K::kTO1 + (K::kO1Twice ? 64 * (c & 1) : 0), x + ((b * kBox + kk * 32) >> 4), sb + (4 * b + kk) * kTok, idesc_bf16(128, 64, 0, 1), b + kk > 0);
+          for (int b = 0; b < MAXDX / 64; ++b)
+#pragma unroll
+            for (int kk = 0; b < nbx && kk < 4; ++kk)
+              mma_ss(lead, tmem + K::kTO1 + (K::kO1Twice ? 64 * (c & 1) : 0), x + ((b * kBox + kk * 32) >> 4),
+                     sb + (part * K::kSPart >> 4) + (4 * b + kk) * kTok, idesc_bf16(128, 64, 0, 1), part + b + kk > 0);
         commit_to(lead, bars + kSFree);
         commit_to(lead, bars + kFreeX + c % kNX);
       };
@@ -637,10 +655,10 @@ __global__ void __launch_bounds__(has_w(MAXDX, STATE_ONLY) ? 640 : 512, 1) lin_t
       auto g2 = [&](int c) {
         const uint64_t z = mnmajor(sZ(c));
 #pragma unroll
-        for (int kk = 0; kk < 8; ++kk)
-          mma_ts(lead, tmem + K::kTO2, tmem + K::kTA + 128 * (c & 1) + 8 * kk, z + kk * kTok, idesc_bf16(128, 64, 0, 1), kk > 0);
+        for (int kk = 0; kk < 16; ++kk)   // 16 tokens of P's first part, then of its second
+          mma_ts(lead, tmem + K::kTO2, tmem + K::kTA + 128 * (c & 1) + 8 * kk, z + (kk >> 1) * kTok, idesc_bf16(128, 64, 0, 1), kk > 0);
         commit_to(lead, bars + kOFull);
-        commit_to(lead, bars + kFreeZ + c % NT);
+        if (!K::kOutInZ) commit_to(lead, bars + kFreeZ + c % NT);
       };
       bool ok = true;
       if (!STATE_ONLY) {
@@ -692,18 +710,17 @@ __global__ void __launch_bounds__(has_w(MAXDX, STATE_ONLY) ? 640 : 512, 1) lin_t
   if (warp == 0) tmem_dealloc(tmem, 512);
 }
 
-// [BH][N][W] bf16 as boxes of `cols` (64 or 32) columns x `rows` tokens of one
-// (b,h), swizzled over the box's row; tokens past N read as zero and are not
-// written.
-bool encode_map(CUtensorMap* m, const void* x, int BH, int N, int W, int rows, int cols) {
+// [BH][N][W] bf16 as boxes of 64 columns x `rows` tokens of one (b,h), 128-byte
+// swizzled; tokens past N read as zero and are not written.
+bool encode_map(CUtensorMap* m, const void* x, int BH, int N, int W, int rows) {
   const EncodeTiledFn enc = encode_tiled();
   if (!enc) return false;
   const cuuint64_t dims[3] = {static_cast<cuuint64_t>(W), static_cast<cuuint64_t>(N), static_cast<cuuint64_t>(BH)};
   const cuuint64_t strides[2] = {static_cast<cuuint64_t>(W) * 2, static_cast<cuuint64_t>(N) * W * 2};
-  const cuuint32_t box[3] = {static_cast<cuuint32_t>(cols), static_cast<cuuint32_t>(rows), 1};
+  const cuuint32_t box[3] = {64, static_cast<cuuint32_t>(rows), 1};
   const cuuint32_t estr[3] = {1, 1, 1};
   return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(x), dims, strides, box, estr,
-             CU_TENSOR_MAP_INTERLEAVE_NONE, cols == 64 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
              CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
@@ -739,14 +756,12 @@ cudaError_t launch_lin_tc(const LinArgs& a, bool state_only, cudaStream_t st) {
     maxdx = std::max(maxdx, a.p[i].dx);
     keep_state = keep_state || a.p[i].state_out;
   }
-  const int out_cols = maxdx == 64 && keep_state ? Cfg<64, false, 3>::kOutCols : Cfg<64, false, 2>::kOutCols;
-  static_assert(Cfg<128, false, 3>::kOutCols == Cfg<64, false, 2>::kOutCols && Cfg<128, false, 2>::kOutCols == Cfg<64, false, 2>::kOutCols);
   const void* seen[4] = {};
   int width[4] = {}, count = 0;
   auto input = [&](const void* x, int W) {   // one map per tensor, whichever roles it has
     for (int i = 0; i < count; ++i)
       if (seen[i] == x && width[i] == W) return i;
-    if (count == 4 || !encode_map(&maps.in[count], x, a.BH, a.N, W, C, 64)) return -1;
+    if (count == 4 || !encode_map(&maps.in[count], x, a.BH, a.N, W, C)) return -1;
     seen[count] = x;
     width[count] = W;
     return count++;
@@ -755,7 +770,7 @@ cudaError_t launch_lin_tc(const LinArgs& a, bool state_only, cudaStream_t st) {
     const LinProblem& p = a.p[i];
     prm.mi[i] = {input(p.x, p.dx), input(p.y, p.dx), input(p.z, p.dz)};
     if (prm.mi[i].x < 0 || prm.mi[i].y < 0 || prm.mi[i].z < 0) return cudaErrorNotSupported;
-    if (!state_only && !encode_map(&maps.out[i], p.out, a.BH, a.N, p.dz, 32, out_cols)) return cudaErrorNotSupported;
+    if (!state_only && !encode_map(&maps.out[i], p.out, a.BH, a.N, p.dz, 32)) return cudaErrorNotSupported;
   }
   return maxdx == 64 ? launch<64>(prm, maps, state_only, keep_state, st) : launch<128>(prm, maps, state_only, keep_state, st);
 }

@@ -5,10 +5,12 @@ with the bounds that the kernels' roundings give.
 Bounds.  A sum of n products in fp32 is off by at most n u sum|terms|, u =
 2^-24 (and the smaller second-order terms), whatever its order.  ``magnitude``
 is that sum of absolute terms, from the same recurrence on absolute values.
-The tensor-core path also rounds each decayed score and each entry of the
-entering state to bf16 once (2^-8 each, on disjoint groups of terms), so it
-adds 2^-8 magnitude; its weighted values reach the state in two bf16 parts,
-whose second rounding leaves 2^-16.  A bf16 result adds 2^-8 of itself.
+For the tensor-core path they leave room for one rounding of each decayed
+score and each entry of the entering state to bf16 (2^-8 each, on disjoint
+groups of terms: 2^-8 magnitude) and for weighted values that reach the state
+in two bf16 parts (2^-16).  The kernels keep more of both, which
+test_gpu_linear_accuracy.py and test_gpu_linear_state.py hold them to.  A bf16
+result adds 2^-8 of itself.
 """
 import torch
 
