@@ -19,7 +19,6 @@ namespace {
 
 constexpr size_t kMaxSmem = 232448;   // 227 KB opt-in shared memory per block on sm_100
 
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
 bool env_set(const char* name) {
   const char* s = std::getenv(name);

@@ -92,11 +92,6 @@ __device__ __forceinline__ uint64_t make_key(float x, uint32_t idx) {
 __device__ __forceinline__ float key_value(uint64_t k) { return unordered(static_cast<uint32_t>(k >> 32)); }
 __device__ __forceinline__ uint32_t key_index(uint64_t k) { return 0xffffffffu - static_cast<uint32_t>(k); }
 
-__device__ __forceinline__ uint64_t f2_add(uint64_t a, uint64_t b) {
-  uint64_t r;
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
 __device__ __forceinline__ float ex2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -823,7 +818,6 @@ cudaError_t run_reorder(const Parts& p, long long groups, int win, int wout, con
   return cudaGetLastError();
 }
 
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
 // Checks shared by both reorder calls; bytes: of one sequence's state.
 ia_status_t check_reorder(int B, int win, int wout, const int* parents, const void* in, void* out, size_t bytes) {

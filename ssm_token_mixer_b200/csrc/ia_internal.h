@@ -4,6 +4,7 @@
 
 #include <cuda.h>
 #include <cuda_runtime.h>
+#include <cstdint>
 
 #include "../../include/ia.h"
 
@@ -114,6 +115,9 @@ cudaError_t launch_ex_tc(const ia_shape_t& s, const ia_options_t* opt, const TcP
                          const void* state_in, float* o, float* num, float* den, void* state_out, void* ws,
                          cudaStream_t st);
 int num_sms();
+
+// The alignment that every entry point asks of its tensors.
+inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
 // Shape check shared by every entry point: positive dims (N only when
 // need_n), a known dtype, and B*H within int range.

@@ -775,7 +775,6 @@ cudaError_t run_ex_direction(const ia_shape_t& s, const void* q, const void* k, 
   return launch_ex_any(s, s.N, q, k, v, a, st);
 }
 
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
 constexpr size_t kMaxSmem = 232448;
 

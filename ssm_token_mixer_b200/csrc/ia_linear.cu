@@ -390,7 +390,6 @@ bool valid_linear(const ia_linear_shape_t* s, bool need_n) {
   return true;
 }
 bool widths_ok(const ia_linear_shape_t& s) { return s.d_k <= kMaxWidth && s.d_v <= kMaxWidth; }
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 bool overlap(const void* a, const void* b, size_t na, size_t nb) {
   const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
   return x < y + nb && y < x + na;

@@ -18,7 +18,7 @@ struct LinProblem {
   const void* x;
   const void* y;
   const void* z;
-  void* out;                // null: only the end state is wanted
+  void* out;                // not written by a pass for the end states alone
   const float* state_in;    // [BH][dx][dz] or null
   float* state_out;         // same or null
   float* seg;               // [BH][nseg - 1][dx][dz]: end states of the segments but the last

@@ -139,11 +139,6 @@ __device__ __forceinline__ uint32_t pack2(uint64_t v) {
   f2_unpack(v, lo, hi);
   return pack_bf16(lo, hi);
 }
-__device__ __forceinline__ uint64_t f2_add(uint64_t a, uint64_t b) {
-  uint64_t r;
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
 __device__ __forceinline__ float bf_lo(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float bf_hi(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
 // What a pair has left beside its bf16 part w (exact).

@@ -52,11 +52,6 @@ namespace {
 
 constexpr int kMaxHeld = 12280;   // widest row held in registers (512 threads, 24 values, less what an offset takes)
 
-__device__ __forceinline__ uint64_t f2_add(uint64_t a, uint64_t b) {
-  uint64_t r;
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
 __device__ __forceinline__ uint64_t f2_twice(float x) { return f2_pack(x, x); }
 __device__ __forceinline__ float f2_sum(uint64_t v) {
   float lo, hi;
@@ -721,7 +716,6 @@ cudaError_t ln_bwd(long long rows, int D, const void* dy, const void* x, const f
   return launch_after(ln_reduce_kernel, (2 * D + 31) / 32, 1024, 0, st, D <= kMaxHeld, D, static_cast<int>(blocks), part, dw, db);
 }
 
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 bool valid_norm(long long rows, int D, ia_dtype_t dt) {
   return rows > 0 && D > 0 && (dt == IA_F32 || dt == IA_BF16) && rows <= (1LL << 62) / D / 8;
 }
