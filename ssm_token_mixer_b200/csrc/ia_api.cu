@@ -19,12 +19,10 @@ namespace {
 
 constexpr size_t kMaxSmem = 232448;   // 227 KB opt-in shared memory per block on sm_100
 
-
 bool env_set(const char* name) {
   const char* s = std::getenv(name);
   return s && s[0] && std::strcmp(s, "0") != 0;
 }
-
 
 bool use_tc(const ia_shape_t& s) {
   if (env_set("IA_PREFILL_SIMT")) return false;   // debug switch: force the CUDA-core path

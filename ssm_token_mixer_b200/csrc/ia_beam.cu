@@ -818,7 +818,6 @@ cudaError_t run_reorder(const Parts& p, long long groups, int win, int wout, con
   return cudaGetLastError();
 }
 
-
 // Checks shared by both reorder calls; bytes: of one sequence's state.
 ia_status_t check_reorder(int B, int win, int wout, const int* parents, const void* in, void* out, size_t bytes) {
   if (win <= 0 || wout <= 0 || win > kMaxW || wout > kMaxW || B % win != 0) return IA_ERR_INVALID_ARG;

@@ -775,7 +775,6 @@ cudaError_t run_ex_direction(const ia_shape_t& s, const void* q, const void* k, 
   return launch_ex_any(s, s.N, q, k, v, a, st);
 }
 
-
 constexpr size_t kMaxSmem = 232448;
 
 ExArgs make_args(const ia_shape_t* s, const ia_options_t* opt, const float* delta, const float* A) {

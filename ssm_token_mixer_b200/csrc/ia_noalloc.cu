@@ -34,7 +34,6 @@ static_assert(sizeof(HeadTables) == 20992 && kStaticMaxHeads == 99,
 // start at zero.
 static __device__ __align__(256) unsigned char g_static_scratch[kStaticScratchBytes];
 
-
 }  // namespace
 }  // namespace ia
 
