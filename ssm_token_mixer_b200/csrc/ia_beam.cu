@@ -20,12 +20,14 @@
 // rows' lists.
 //
 // Bound.  Reading the logits once would take 7.9 us for 64 x 8 x 50257 in bf16 and
-// 15.7 in fp32; both kernels take 23.4 and 31.1 (34.4 and 31.1 with 16 bytes a
-// round and values listed).  Instructions bound the scan: unpacking, maximum,
-// exponential and sum of 16 values are some 110 of the 130 that a warp runs a
-// round; 512 rows on 592 places leave 3 or 4 CTAs on an SM, and beginning and
-// end of a row, which no other row's rounds cover, are 5 us of it.  The loads
-// are one round ahead; two ahead move more registers than they hide (24.5 us).
+// 15.7 in fp32; both kernels take 24.6 and 32.2 (34.4 and 31.1 with 16 bytes a
+// round and values listed).  Two things bound the scan, about alike: instructions
+// (unpacking, maximum, exponential and sum of 16 values are some 110 of the 130
+// that a warp runs a round; issue slots are 57 % busy) and an uneven spread (512
+// rows on 592 places leave 3 or 4 CTAs on an SM, 38 % of the warps active, and
+// beginning and end of a row, which no other row's rounds cover, are 5 us of it).
+// The loads are one round ahead; two ahead move more registers than they hide
+// (1 us).  A call that takes sums again in fp64 is longer: 155 us for fp32 logits.
 //
 // Order keys.  (value, lower index first) is one 64-bit number: the fp32 value
 // mapped to an order-preserving integer above the complement of the index.

@@ -74,8 +74,10 @@ __host__ __device__ inline SimtSmem simt_smem(int dx) {
 // about what an SM can supply, so it is bound by the FP32 pipe and shared
 // memory together.  Small CTAs (four per SM at widths up to 64) let one compute
 // while another loads or waits at a barrier.  Measured: fp32 prefill of B8 H16
-// N2048 d64 396 us (4.0 G multiply-adds, 28 % of the pipe's rate), of B2 H4 N300
-// 48 x 80 in 10 segments 21.4 us, of one chunk 9.5 us.
+// N2048 d64 400 us (4.0 G multiply-adds, 28 % of the pipe's rate), of B2 H4 N300
+// 48 x 80 in 10 segments 21.1 us, of one chunk 9.5 us.  bf16 of the widths that the
+// tensor cores do not take is no faster: prefill of B4 H16 N2048 d96 609 us, training
+// 1760 (d128 on the tensor cores 48 and 157).
 template <bool BF16, bool STATE_ONLY, int T>
 __global__ void __launch_bounds__(T, 512 / T) lin_simt_kernel(const __grid_constant__ LinArgs a) {
   extern __shared__ __align__(16) float sm[];

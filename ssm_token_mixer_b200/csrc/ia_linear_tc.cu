@@ -46,8 +46,17 @@
 // of straight-line code do not fit an SM's instruction caches; ncu, B8 H16
 // N2048 d64).  Only the warp that issues the products runs straight-line code:
 // its issuing is on the chunk's path (training of B4 H16 N2048 d128 137.4 us with
-// four products a turn, 132.0 with all).  Waits are bounded mbarrier waits with
-// a CTA-wide abort flag.
+// four products a turn, 132.0 with all).  Letting G4 wait for K alone and not for
+// the operand of S as well changed nothing (training of B8 H16 N2048 d64 122.7 us
+// with, 121.0 without).  Waits are bounded mbarrier waits with a CTA-wide abort
+// flag.
+//
+// Pairs of times in these comments that are below the present ones were taken
+// before P and S had second parts.
+//
+// Measured: prefill with the state of B8 H16 N2048 d64 36.0 us, of B4 H16 N2048
+// d128 48.4; training 122 and 157.  Tensor pipe 44 to 48 % active, issue slots 45
+// to 54 %: what bounds a chunk is the chain of its four roles, P's above all.
 #include <algorithm>
 #include <cuda.h>
 

@@ -31,8 +31,9 @@
 //
 // Measured (a graph of calls; rows of up to 126 MB stay in L2): 16384 x 1024 bf16
 // forward 14.9 us, backward 24.6 (67 and 101 MB: 10.2 and 15.4 at HBM's rate);
-// 131072 x 128 fp32 22.4 and 37.7 (20.5, 30.7); 5003 x 777 fp32 9.5 and 16.4 (4.7,
-// 7.1); 2048 x 8192 bf16 25.1 and 31.7 (10.2, 15.4).  Instructions bound bf16 rows
+// 131072 x 128 fp32 22.4 and 37.7 (20.5, 30.7); 5003 x 777 fp32 9.5 and 15.8 (4.7,
+// 7.1); 2048 x 8192 bf16 25.1 and 31.7 (10.2, 15.4).  The forms that hold 24 values a
+// thread spill (backward 64 to 128 bytes a thread).  Instructions bound bf16 rows
 // of the forward pass (two exchanges a row and sizes and addresses formed per
 // copy: 394 a warp and row at D = 1024, 17.3 us), beside the launch and the first
 // rows' latency; ragged rows pay for their ends, and rows above 4096 columns read
