@@ -437,7 +437,8 @@ IA_API ia_status_t ia_layer_norm_bwd(long long rows, int D, ia_dtype_t dtype, co
  *   - Places that no candidate is left for: score -inf, parent and token -1.
  * The order is that of the exact scores: sums run in fp32 with a known bound,
  * and where that bound could not separate two beams' candidates, their sums
- * are taken again in fp64.
+ * are taken again in fp64.  Beams of equal logits tie exactly; beams whose
+ * logits are the same numbers at other tokens may differ in fp64's last bits.
  * 1 <= W <= 64, 1 <= K <= 64, V >= 1; end_token is in 0 .. V-1 when finished
  * is given.  Outputs and the workspace may not overlap inputs or one another.
  */
