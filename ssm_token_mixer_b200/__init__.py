@@ -772,8 +772,11 @@ def linear_decode_step(q, k, v, log_decay, state, scale=None, state_out=None, pa
     if o is not None:
         _need("o", o, v.shape, q.dtype)
         _apart("o", o, q, k, v, log_decay, state, state_out, parents)
-    dev = _place(("q", q), ("k", k), ("v", v), ("log_decay", log_decay), ("state", state),
-                        ("state_out", state_out), ("parents", parents), ("o", o))
+    dev = q.get_device()
+    if not (0 <= dev == k.get_device() == v.get_device() == log_decay.get_device() == state.get_device() and
+            state_out is None and o is None):
+        dev = _place(("q", q), ("k", k), ("v", v), ("log_decay", log_decay), ("state", state),
+                     ("state_out", state_out), ("parents", parents), ("o", o))
     aq, ak, av, ag, at = _ad(q), _ad(k), _ad(v), _ad(log_decay), _ad(out)
     ap = None if parents is None else _ad(parents)
     # the state may not share memory with what a step reads (state itself is looked at by the library)
